@@ -70,6 +70,8 @@ typedef enum { KV_BF16 = 0, KV_F32 = 1 } kv_dtype;
 typedef enum { KV_SCORE_ADA = 0, KV_SCORE_LAVA = 1, KV_SCORE_CRITICAL = 2 } kv_score_mode;
 typedef enum { KV_GROUP_MEAN = 0, KV_GROUP_MAX = 1 } kv_group_reduce;
 typedef enum { KV_OP_SCORE = 0, KV_OP_ALLOCATE = 1, KV_OP_COMPACT = 2, KV_OP_DECODE = 3 } kv_op;
+/* ops of the paged cache, for kv_paged_workspace_size */
+typedef enum { KV_OP_PAGE_MAP = 4, KV_OP_PAGED_WRITE = 5, KV_OP_PAGED_DECODE = 6 } kv_paged_op;
 typedef enum { KV_TERMS_MEAN_POOLED = 0, KV_TERMS_L2 = 1 } kv_terms_kind;
 typedef enum { KV_PROJ_CRIT_GQA = 0, KV_PROJ_LAPROX = 1 } kv_proj_kind;
 
@@ -413,6 +415,134 @@ KV_API kv_status flat_decode_attn_noalloc(const kv_shape* shape, const void* q,
                                           void* k_flat, void* v_flat, const int64_t* cu_off,
                                           int32_t* lens, int64_t flat_capacity_rows,
                                           float softmax_scale, void* out, void* stream);
+
+/*
+ * The paged cache
+ * ---------------
+ * A flat cache is sized once; a paged cache grows and shrinks while it is served.  K and V rows
+ * live in a pool of pages of `page` rows; a block table lists the pages of each sequence (or of
+ * each of its KV heads), and a ring lists the pages that are free.  Rows that eviction drops give
+ * whole pages back, and any sequence can take them.
+ *
+ * One step of serving:  kv_page_map (tables, slots and lengths for the rows the step adds or
+ * drops), kv_paged_write (prompt rows, or kv_compact's rows, to their slots), paged_decode_attn
+ * (one new token per sequence; it stores the token's own K and V row).
+ *
+ * `tables` = 1: the KV heads of a sequence share its table, a page holds `page` rows of every
+ * KV head.  `tables` = hkv: every KV head has its own table and length, as head-adaptive budgets
+ * need, and a page holds rows of one head.  With U = seqs * tables and Hp = hkv / tables:
+ *   k_pages, v_pages [num_pages][Hp][page][d] dtype, pages page_stride elements apart
+ *   block_table      [U][max_pages] int32: page number of rows [j * page, (j + 1) * page)
+ *   lens             [U] int32: rows held
+ * A slot names a row of the pool: page number * page + row within the page (int64), -1 for none.
+ * Table u belongs to sequence u / tables (and, with head tables, KV head u % tables).  A caller
+ * with L layers in one call takes seqs = batch * layers.
+ *
+ * Limits: page a power of two from 8 to 256, d <= 128 (a multiple of 8), hq / hkv <= 8,
+ * hkv <= 256, max_pages * page and num_pages below 2^31, a page_stride below 2^40 bytes, and
+ * for kv_page_map at most KV_PAGE_MAP_MAX_TABLES tables.
+ * Alignment: rows (k, v, q, out, k_pages, ...) 16 bytes, strides multiples of 16 bytes, tables
+ * only their element's, so that slices can be passed.
+ */
+typedef struct {
+  int32_t seqs, hq, hkv, d;
+  int32_t tables;       /* block tables per sequence: 1 or hkv                              */
+  int32_t page;         /* rows per page                                                    */
+  int32_t max_pages;    /* columns of block_table                                           */
+  int32_t dtype;        /* kv_dtype of the rows                                             */
+  int64_t num_pages;    /* pages of the pool                                                */
+  int64_t page_stride;  /* elements from a page to the next; 0 means dense (Hp * page * d)  */
+} kv_paged_shape;
+
+#define KV_PAGE_MAP_MAX_TABLES 16384
+
+/* Bytes of device workspace `op` (kv_paged_op) needs for `shape` (0 for an invalid shape).
+ * The same rules as kv_workspace_size: zeroed once before its first use, error word in the
+ * first 256 bytes, calls that share one are ordered on one stream. */
+KV_API size_t kv_paged_workspace_size(int op, const kv_paged_shape* shape);
+
+/*
+ * kv_page_map -- block tables, slot map and free ring brought from the lengths held to the
+ * lengths asked for, on the GPU (no host round trip; capturable).
+ * (The method's pages have no counterpart: they describe one flat tensor per layer.)
+ *
+ * Table u holds lens[u] rows; it gains add[u] rows (add > 0), keeps them (0) or loses the last
+ * -add[u] (a loss past zero empties it).  With P(x) = ceil(x / page), new = max(lens + add, 0):
+ *   cu_add[u]  = sum of max(add, 0) over the tables before u; cu_add[U] the total
+ *   a table that grows takes pages P(lens)..P(new)-1 of its block_table row from the ring's
+ *     head, in table order; one that shrinks returns pages P(new)..P(lens)-1 to its tail (other
+ *     entries of block_table are left as they were)
+ *   slot_map[cu_add[u] + i] = slot of row lens[u] + i, for i < add[u]
+ *   lens_out[u] = new
+ * Free pages are free_ring[i % num_pages] for free_state[0] <= i < free_state[1] (start with
+ * 0..num_pages-1 and {0, num_pages}); free_out gets the state after the call.  Pages returned by
+ * a call can be taken from the next call on.  Entries of slot_map from cu_add[U] on are left as
+ * they were.
+ *
+ * A table that cannot be served keeps its length and pages, its slots are -1, and the device
+ * error word is set:  7 a length below 0 or past max_pages * page; 8 no page left (in table
+ * order: from the first table whose pages do not fit, tables that need pages are refused; rows
+ * that fit in a table's last page are not); 9 its rows end past slot_capacity; 10 a page number
+ * taken or returned lies outside the pool (its slots are -1); 11 free_state is no ring of
+ * num_pages pages, or takes back more pages than it has room for (nothing is then taken, or
+ * returned).
+ *
+ * lens, add   [U] int32        lens_out [U] int32, may be lens
+ * free_ring   [num_pages] int32 in/out
+ * free_state  [2] int64        free_out [2] int64, may be free_state
+ * block_table [U][max_pages] int32 in/out
+ * cu_add      [U+1] int64 out  slot_map [slot_capacity] int64 out (slot_capacity < 2^31 - 1)
+ */
+KV_API kv_status kv_page_map(const kv_paged_shape* shape, const int32_t* lens, const int32_t* add,
+                             int32_t* free_ring, const int64_t* free_state, int64_t slot_capacity,
+                             int32_t* block_table, int32_t* lens_out, int64_t* free_out,
+                             int64_t* cu_add, int64_t* slot_map, void* ws, size_t ws_bytes,
+                             void* stream);
+
+/*
+ * kv_paged_write -- rows of K and V stored at their slots.
+ * For i < rows:  k_pages / v_pages [slot / page][h][slot % page][:] = k / v [i][h][:], h < Hp,
+ * with slot = slot_map[i].  Rows with slot -1 are skipped; any other slot outside the pool sets
+ * the device error word (10) and is skipped.  A slot may appear once per call.
+ *
+ * k, v     rows of [Hp][d] dtype, src_stride elements from a row to the next (>= Hp * d, so that
+ *          K and V may be parts of a fused projection's rows; 0 means dense).  kv_compact's
+ *          k_flat / v_flat with reserve = 0 are such rows for head tables (Hp = 1), in the order
+ *          of kv_page_map's slots.
+ * rows     the number of rows, or with n_rows (a device pointer, 8-byte aligned, nullable) the
+ *          most: rows from *n_rows on are not read (kv_page_map's cu_add + U fits)
+ */
+KV_API kv_status kv_paged_write(const kv_paged_shape* shape, const void* k, const void* v,
+                                int64_t src_stride, const int64_t* slot_map, int64_t rows,
+                                const int64_t* n_rows, void* k_pages, void* v_pages, void* ws,
+                                size_t ws_bytes, void* stream);
+
+/*
+ * paged_decode_attn -- one decode step of attention over the paged cache (flat_decode_attn's
+ * step; Ada-KV formal model: A = softmax(q K^T * scale), o = A V, over uneven lengths).
+ * For every sequence and query head q of KV head g, over the lens rows of its table:
+ *   out = sum_r softmax_r(q . k_r * softmax_scale) v_r,  zeros for a table with no rows.
+ * lens counts the new token's row: with k_new / v_new given, the last row (lens - 1) of each
+ * table that gained rows and was served (cu_add[u+1] > cu_add[u], slot_map[cu_add[u+1] - 1] >= 0)
+ * is taken from k_new / v_new and stored at that slot.  Tables that gained none (idle sequences of
+ * a batch) attend over the rows they hold.  A page number or slot outside the pool sets the device
+ * error word (10): rows of such a page are left out of the sums, and such a slot is not written.
+ * A length below 0 counts as 0, one past max_pages * page as max_pages * page (both set 7).
+ *
+ * q            [seqs][hq][d] dtype
+ * k_new, v_new [seqs][hkv][d] dtype, or both NULL (cu_add and slot_map are then not read)
+ * cu_add, slot_map, slot_capacity: as given to and written by kv_page_map
+ * block_table, lens (kv_page_map's lens_out), k_pages, v_pages: the cache
+ * out          [seqs][hq][d] dtype
+ * Sums, the softmax and out before its rounding are float32.  The K and V rows attended to have
+ * to be finite; anything may stand behind a table's last row and in pages of no table.
+ */
+KV_API kv_status paged_decode_attn(const kv_paged_shape* shape, const void* q, const void* k_new,
+                                   const void* v_new, const int64_t* cu_add,
+                                   const int64_t* slot_map, int64_t slot_capacity, void* k_pages,
+                                   void* v_pages, const int32_t* block_table, const int32_t* lens,
+                                   float softmax_scale, void* out, void* ws, size_t ws_bytes,
+                                   void* stream);
 
 /* Synchronises `stream`, reads the device error word of `ws` and clears it.
  * Returns KV_OK or KV_ERR_DEVICE_CHECK (KV_ERR_CUDA if the copy fails).

@@ -25,6 +25,9 @@ __all__ = [
     "KV_PROJ_CRIT_GQA", "KV_PROJ_LAPROX",
     "flat_decode_attn", "kv_check_device_status", "kv_status_string", "kv_kernel_launches",
     "flat_decode_attn_noalloc",
+    "KV_OP_PAGE_MAP", "KV_OP_PAGED_WRITE", "KV_OP_PAGED_DECODE", "KV_PAGE_MAP_MAX_TABLES",
+    "KvPagedShape", "kv_paged_workspace_size", "kv_page_map", "kv_paged_write",
+    "paged_decode_attn",
 ]
 
 KV_OK, KV_ERR_INVALID_ARG, KV_ERR_UNSUPPORTED, KV_ERR_WORKSPACE = 0, 1, 2, 3
@@ -33,6 +36,8 @@ KV_BF16, KV_F32 = 0, 1
 KV_SCORE_ADA, KV_SCORE_LAVA, KV_SCORE_CRITICAL = 0, 1, 2
 KV_GROUP_MEAN, KV_GROUP_MAX = 0, 1
 KV_OP_SCORE, KV_OP_ALLOCATE, KV_OP_COMPACT, KV_OP_DECODE = 0, 1, 2, 3
+KV_OP_PAGE_MAP, KV_OP_PAGED_WRITE, KV_OP_PAGED_DECODE = 4, 5, 6
+KV_PAGE_MAP_MAX_TABLES = 16384
 KV_TERMS_MEAN_POOLED, KV_TERMS_L2 = 0, 1
 KV_PROJ_CRIT_GQA, KV_PROJ_LAPROX = 0, 1
 
@@ -57,6 +62,20 @@ class KvShape(ctypes.Structure):
     def from_workload(cls, wl, batch: Optional[int] = None, layers: Optional[int] = None):
         return cls.of(wl.batch if batch is None else batch, wl.layers if layers is None else layers,
                       wl.hq, wl.hkv, wl.d, wl.n, wl.w, wl.pool, wl.dtype)
+
+
+class KvPagedShape(ctypes.Structure):
+    """Shape of a paged cache; ``page_stride`` (elements) 0 means dense pages."""
+    _fields_ = [(f, ctypes.c_int32) for f in
+                ("seqs", "hq", "hkv", "d", "tables", "page", "max_pages", "dtype")] + \
+               [("num_pages", ctypes.c_int64), ("page_stride", ctypes.c_int64)]
+
+    @classmethod
+    def of(cls, seqs, hq, hkv, d, tables, page, max_pages, dtype, num_pages,
+           page_stride=0) -> "KvPagedShape":
+        if isinstance(dtype, str):
+            dtype = KV_BF16 if dtype == "bf16" else KV_F32
+        return cls(seqs, hq, hkv, d, tables, page, max_pages, dtype, num_pages, page_stride)
 
 
 class KvError(RuntimeError):
@@ -99,6 +118,13 @@ _SIGS = {
     "kv_kernel_launches": (ctypes.c_uint64, []),
     "flat_decode_attn_noalloc": (ctypes.c_int, [ctypes.POINTER(KvShape), _vp, _vp, _vp, _vp, _vp,
                                                 _vp, _vp, _i64, _f32, _vp, _vp]),
+    "kv_paged_workspace_size": (_sz, [ctypes.c_int, ctypes.POINTER(KvPagedShape)]),
+    "kv_page_map": (ctypes.c_int, [ctypes.POINTER(KvPagedShape), _vp, _vp, _vp, _vp, _i64, _vp,
+                                   _vp, _vp, _vp, _vp, _vp, _sz, _vp]),
+    "kv_paged_write": (ctypes.c_int, [ctypes.POINTER(KvPagedShape), _vp, _vp, _i64, _vp, _i64,
+                                      _vp, _vp, _vp, _vp, _sz, _vp]),
+    "paged_decode_attn": (ctypes.c_int, [ctypes.POINTER(KvPagedShape), _vp, _vp, _vp, _vp, _vp,
+                                         _i64, _vp, _vp, _vp, _vp, _f32, _vp, _vp, _sz, _vp]),
 }
 
 
@@ -270,6 +296,114 @@ def flat_decode_attn_noalloc(shape: KvShape, q, k_new, v_new, k_flat, v_flat, cu
                                         _ptr(k_flat), _ptr(v_flat), _ptr(cu_off), _ptr(lens), cap,
                                         softmax_scale, _ptr(out), _stream(stream))
     _check("flat_decode_attn_noalloc", st)
+
+
+def kv_paged_workspace_size(op: int, shape: KvPagedShape) -> int:
+    return int(lib().kv_paged_workspace_size(op, ctypes.byref(shape)))
+
+
+def _need(t, dtype: str, count: int, what: str) -> None:
+    """A table's type and the entries the call may touch."""
+    if t is not None and not isinstance(t, int):
+        if str(t.dtype) != "torch." + dtype:
+            raise ValueError("%s must be %s" % (what, dtype))
+        if t.numel() < count:
+            raise ValueError("%s has %d entries, needs %d" % (what, t.numel(), count))
+
+
+def _rows_view(t, hp: int, d: int, what: str):
+    """Pointer and row stride (elements) of rows [n][hp][d] or [n][hp * d]; a row is contiguous,
+    rows may lie apart (parts of a fused projection)."""
+    if not t.is_cuda:
+        raise ValueError("tensor must be on a CUDA device")
+    if t.dim() < 2 or t.numel() != t.shape[0] * hp * d:
+        raise ValueError("%s must be rows of %d heads x %d" % (what, hp, d))
+    step = 1
+    for size, stride in zip(reversed(t.shape[1:]), reversed(t.stride()[1:])):
+        if size > 1 and stride != step:
+            raise ValueError("the rows of %s must be contiguous" % what)
+        step *= size
+    return t.data_ptr(), (t.stride(0) if t.shape[0] > 1 else hp * d)
+
+
+def _pool(shape: KvPagedShape, t, what: str) -> Optional[int]:
+    """Pointer of a page pool: its pages are dense, ``page_stride`` elements apart."""
+    if t is None or isinstance(t, int):
+        return t
+    if not t.is_cuda:
+        raise ValueError("tensor must be on a CUDA device")
+    if str(t.dtype) != ("torch.bfloat16" if shape.dtype == KV_BF16 else "torch.float32"):
+        raise ValueError("%s is not of the shape's dtype" % what)
+    inner = (shape.hkv // shape.tables) * shape.page * shape.d
+    stride = shape.page_stride or inner
+    if t.shape[0] < shape.num_pages or t[0].numel() != inner or not t[0].is_contiguous() or (
+            shape.num_pages > 1 and t.stride(0) != stride):
+        raise ValueError("%s must be [num_pages][heads][page][d], pages page_stride apart" % what)
+    return t.data_ptr()
+
+
+def kv_page_map(shape: KvPagedShape, lens, add, free_ring, free_state, block_table, lens_out,
+                free_out, cu_add, slot_map, ws, stream=None) -> None:
+    """Block tables, slots and lengths for the rows each table gains or loses.  ``lens_out`` may
+    be ``lens`` and ``free_out`` may be ``free_state``."""
+    n = shape.seqs * shape.tables
+    _need(lens, "int32", n, "lens")
+    _need(add, "int32", n, "add")
+    _need(free_ring, "int32", shape.num_pages, "free_ring")
+    _need(free_state, "int64", 2, "free_state")
+    _need(block_table, "int32", n * shape.max_pages, "block_table")
+    _need(lens_out, "int32", n, "lens_out")
+    _need(free_out, "int64", 2, "free_out")
+    _need(cu_add, "int64", n + 1, "cu_add")
+    _need(slot_map, "int64", 0, "slot_map")
+    st = lib().kv_page_map(ctypes.byref(shape), _ptr(lens), _ptr(add), _ptr(free_ring),
+                           _ptr(free_state), slot_map.numel(), _ptr(block_table), _ptr(lens_out),
+                           _ptr(free_out), _ptr(cu_add), _ptr(slot_map), _ptr(ws), _nbytes(ws),
+                           _stream(stream))
+    _check("kv_page_map", st)
+
+
+def kv_paged_write(shape: KvPagedShape, k, v, slot_map, n_rows, k_pages, v_pages, ws,
+                   stream=None) -> None:
+    """Rows of ``k`` and ``v`` ([n][heads per page][d], rows may lie apart) at their slots.
+    ``n_rows`` (a device int64, or None): rows from there on are left out."""
+    hp = shape.hkv // shape.tables
+    kp, ks = _rows_view(k, hp, shape.d, "k")
+    vp, vs = _rows_view(v, hp, shape.d, "v")
+    if k.dtype != k_pages.dtype or v.dtype != v_pages.dtype:
+        raise ValueError("rows and pages must have one dtype")
+    if ks != vs or k.shape[0] != v.shape[0]:
+        raise ValueError("k and v must have the same rows and row stride")
+    _need(slot_map, "int64", k.shape[0], "slot_map")
+    _need(n_rows, "int64", 1, "n_rows")
+    st = lib().kv_paged_write(ctypes.byref(shape), kp, vp, ks, _ptr(slot_map), k.shape[0],
+                              _ptr(n_rows), _pool(shape, k_pages, "k_pages"),
+                              _pool(shape, v_pages, "v_pages"), _ptr(ws), _nbytes(ws),
+                              _stream(stream))
+    _check("kv_paged_write", st)
+
+
+def paged_decode_attn(shape: KvPagedShape, q, k_new, v_new, cu_add, slot_map, k_pages, v_pages,
+                      block_table, lens, softmax_scale: float, out, ws, stream=None) -> None:
+    """One decode step over the paged cache; ``k_new`` / ``v_new`` / ``cu_add`` / ``slot_map``
+    None: no rows are stored."""
+    n = shape.seqs * shape.tables
+    _need(block_table, "int32", n * shape.max_pages, "block_table")
+    _need(lens, "int32", n, "lens")
+    _need(cu_add, "int64", n + 1, "cu_add")
+    _need(slot_map, "int64", 0, "slot_map")
+    el = "bfloat16" if shape.dtype == KV_BF16 else "float32"
+    for t, heads, what in ((q, shape.hq, "q"), (out, shape.hq, "out"), (k_new, shape.hkv, "k_new"),
+                           (v_new, shape.hkv, "v_new")):
+        _need(t, el, shape.seqs * heads * shape.d, what)
+    st = lib().paged_decode_attn(ctypes.byref(shape), _ptr(q), _ptr(k_new), _ptr(v_new),
+                                 _ptr(cu_add), _ptr(slot_map),
+                                 0 if slot_map is None else slot_map.numel(),
+                                 _pool(shape, k_pages, "k_pages"),
+                                 _pool(shape, v_pages, "v_pages"), _ptr(block_table), _ptr(lens),
+                                 softmax_scale, _ptr(out), _ptr(ws), _nbytes(ws),
+                                 _stream(stream))
+    _check("paged_decode_attn", st)
 
 
 def kv_check_device_status(ws, stream=None) -> int:

@@ -29,6 +29,11 @@ enum DevErr : unsigned int {
   DEV_HEAD_BUDGET = 4,      // head_budget outside [w, n] (clamped)
   DEV_WAIT_TIMEOUT = 5,     // a bounded wait gave up
   DEV_SELECT = 6,           // a selection invariant failed (should never happen)
+  DEV_PAGE_TABLE = 7,       // a length outside [0, max_pages * page]
+  DEV_NO_PAGES = 8,         // no free page left (table refused)
+  DEV_SLOT_CAPACITY = 9,    // rows past slot_capacity (table refused)
+  DEV_PAGE_ID = 10,         // a page number or slot outside the pool (skipped)
+  DEV_FREE_RING = 11,       // free_state is not a ring of num_pages pages
 };
 
 __device__ __forceinline__ void raise_dev(WsHeader* h, unsigned int code, unsigned int info = 0) {

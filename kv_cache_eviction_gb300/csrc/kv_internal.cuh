@@ -173,6 +173,32 @@ cudaError_t launch_decode_parts(const Shape& s, const void* q, const void* kn, c
                                 int64_t part_slots, uint32_t* tick, WsHeader* hdr,
                                 cudaStream_t st);
 
+// ----------------------------- paged cache ---------------------------------
+struct PagedShape {
+  int seqs, Hq, Hkv, d, tables, page, max_pages, dtype;
+  int64_t num_pages, page_stride;   // page_stride in elements
+  __host__ __device__ int G() const { return Hq / Hkv; }
+  __host__ __device__ int Hp() const { return Hkv / tables; }              // heads per page
+  __host__ __device__ int64_t U() const { return (int64_t)seqs * tables; }   // block tables
+  int esize() const { return dtype == KV_BF16 ? 2 : 4; }
+};
+
+// Workspace of kv_page_map: the header, then the count of CTAs that are done.
+constexpr size_t kPageMapWsBytes = kWsHeader + 256;
+cudaError_t launch_page_map(const PagedShape& s, const int32_t* lens, const int32_t* add,
+                            int32_t* ring, const int64_t* state, int64_t slot_capacity,
+                            int32_t* table, int32_t* lens_out, int64_t* state_out, int64_t* cu,
+                            int64_t* slots, char* ws, cudaStream_t st);
+cudaError_t launch_paged_write(const PagedShape& s, const void* k, const void* v,
+                               int64_t src_stride, const int64_t* slots, int64_t rows,
+                               const int64_t* n_rows, void* kp, void* vp, WsHeader* hdr,
+                               cudaStream_t st);
+size_t paged_decode_ws_bytes(const PagedShape& s);
+cudaError_t launch_paged_decode(const PagedShape& s, const void* q, const void* kn, const void* vn,
+                                const int64_t* cu, const int64_t* slots, int64_t slot_capacity,
+                                void* kp, void* vp, const int32_t* table, const int32_t* lens,
+                                float scale, void* out, char* ws, cudaStream_t st);
+
 int num_sms();
 // Largest dynamic + static shared memory one CTA may opt in to.
 size_t max_smem_optin();

@@ -68,6 +68,34 @@ static bool shape_supported(const Shape& s) {
   return true;
 }
 
+// Shape checks of the paged cache: KV_OK (with *out filled), invalid or unsupported.
+static kv_status paged_shape_check(const kv_paged_shape* sh, PagedShape* out) {
+  if (sh == nullptr) return KV_ERR_INVALID_ARG;
+  PagedShape s{sh->seqs, sh->hq, sh->hkv, sh->d, sh->tables, sh->page, sh->max_pages, sh->dtype,
+               sh->num_pages, sh->page_stride};
+  if (s.seqs < 0 || s.Hq <= 0 || s.Hkv <= 0 || s.d <= 0 || s.page <= 0 || s.max_pages <= 0 ||
+      s.num_pages <= 0 || s.page_stride < 0)
+    return KV_ERR_INVALID_ARG;
+  if (s.Hq % s.Hkv != 0 || s.d % 8 != 0) return KV_ERR_INVALID_ARG;
+  if (s.tables != 1 && s.tables != s.Hkv) return KV_ERR_INVALID_ARG;
+  if (s.dtype != KV_BF16 && s.dtype != KV_F32) return KV_ERR_INVALID_ARG;
+  if (s.G() > 8 || s.d > 128 || s.Hkv > 256) return KV_ERR_UNSUPPORTED;
+  if (s.page < 8 || s.page > 256 || (s.page & (s.page - 1)) != 0) return KV_ERR_UNSUPPORTED;
+  if ((int64_t)s.max_pages * s.page > INT32_MAX || s.num_pages > INT32_MAX)
+    return KV_ERR_UNSUPPORTED;
+  if (s.U() > INT32_MAX || (int64_t)s.seqs * s.Hkv > INT32_MAX) return KV_ERR_UNSUPPORTED;
+  const int64_t dense = (int64_t)s.Hp() * s.page * s.d;
+  if (s.page_stride == 0) s.page_stride = dense;
+  if (s.page_stride < dense || s.page_stride % (16 / s.esize()) != 0) return KV_ERR_INVALID_ARG;
+  if (s.page_stride >= ((int64_t)1 << 40) / s.esize()) return KV_ERR_UNSUPPORTED;
+  *out = s;
+  return KV_OK;
+}
+
+static bool aligned_to(const void* p, uintptr_t a) {
+  return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0;
+}
+
 static kv_status cuda_status(cudaError_t e) { return e == cudaSuccess ? KV_OK : KV_ERR_CUDA; }
 
 // The shape of a model-wide selection (kv_allocate layer_entropy_mode 2): the L layers of a
@@ -462,6 +490,101 @@ kv_status flat_decode_attn(const kv_shape* shape, const void* q, const void* k_n
   return cuda_status(launch_decode(s, q, k_new, v_new, k_flat, v_flat, cu_off, lens,
                                    flat_capacity_rows, softmax_scale, out,
                                    static_cast<char*>(ws), p, static_cast<cudaStream_t>(stream)));
+}
+
+size_t kv_paged_workspace_size(int op, const kv_paged_shape* shape) {
+  PagedShape s;
+  if (paged_shape_check(shape, &s) != KV_OK) return 0;
+  switch (op) {
+    case KV_OP_PAGE_MAP: return kPageMapWsBytes;
+    case KV_OP_PAGED_WRITE: return kWsHeader;
+    case KV_OP_PAGED_DECODE: return paged_decode_ws_bytes(s);
+    default: return 0;
+  }
+}
+
+kv_status kv_page_map(const kv_paged_shape* shape, const int32_t* lens, const int32_t* add,
+                      int32_t* free_ring, const int64_t* free_state, int64_t slot_capacity,
+                      int32_t* block_table, int32_t* lens_out, int64_t* free_out, int64_t* cu_add,
+                      int64_t* slot_map, void* ws, size_t ws_bytes, void* stream) {
+  PagedShape s;
+  const kv_status st = paged_shape_check(shape, &s);
+  if (st != KV_OK) return st;
+  if (ws == nullptr || !aligned16(ws)) return KV_ERR_INVALID_ARG;
+  if (slot_capacity < 0 || slot_capacity >= INT32_MAX) return KV_ERR_INVALID_ARG;
+  if (s.seqs == 0) return KV_OK;
+  if (lens == nullptr || add == nullptr || free_ring == nullptr || free_state == nullptr ||
+      block_table == nullptr || lens_out == nullptr || free_out == nullptr || cu_add == nullptr ||
+      (slot_map == nullptr && slot_capacity > 0))
+    return KV_ERR_INVALID_ARG;
+  if (!aligned_to(lens, 4) || !aligned_to(add, 4) || !aligned_to(free_ring, 4) ||
+      !aligned_to(free_state, 8) || !aligned_to(block_table, 4) || !aligned_to(lens_out, 4) ||
+      !aligned_to(free_out, 8) || !aligned_to(cu_add, 8) || !aligned_to(slot_map, 8))
+    return KV_ERR_INVALID_ARG;
+  if (lens_out == add) return KV_ERR_INVALID_ARG;
+  if (s.U() > KV_PAGE_MAP_MAX_TABLES) return KV_ERR_UNSUPPORTED;
+  if (ws_bytes < kPageMapWsBytes) return KV_ERR_WORKSPACE;
+  return cuda_status(launch_page_map(s, lens, add, free_ring, free_state, slot_capacity,
+                                     block_table, lens_out, free_out, cu_add, slot_map,
+                                     static_cast<char*>(ws), static_cast<cudaStream_t>(stream)));
+}
+
+kv_status kv_paged_write(const kv_paged_shape* shape, const void* k, const void* v,
+                         int64_t src_stride, const int64_t* slot_map, int64_t rows,
+                         const int64_t* n_rows, void* k_pages, void* v_pages, void* ws,
+                         size_t ws_bytes, void* stream) {
+  PagedShape s;
+  const kv_status st = paged_shape_check(shape, &s);
+  if (st != KV_OK) return st;
+  if (ws == nullptr || !aligned16(ws)) return KV_ERR_INVALID_ARG;
+  if (rows < 0 || rows > INT32_MAX || src_stride < 0) return KV_ERR_INVALID_ARG;
+  if (rows == 0) return KV_OK;
+  if (k == nullptr || v == nullptr || slot_map == nullptr || k_pages == nullptr ||
+      v_pages == nullptr)
+    return KV_ERR_INVALID_ARG;
+  if (!aligned16(k) || !aligned16(v) || !aligned16(k_pages) || !aligned16(v_pages) ||
+      !aligned_to(slot_map, 8) || !aligned_to(n_rows, 8))
+    return KV_ERR_INVALID_ARG;
+  const int64_t dense = (int64_t)s.Hp() * s.d;
+  if (src_stride == 0) src_stride = dense;
+  if (src_stride < dense || src_stride % (16 / s.esize()) != 0 ||
+      src_stride > ((int64_t)1 << 31))
+    return KV_ERR_INVALID_ARG;
+  if (ws_bytes < kWsHeader) return KV_ERR_WORKSPACE;
+  return cuda_status(launch_paged_write(s, k, v, src_stride, slot_map, rows, n_rows, k_pages,
+                                        v_pages, static_cast<WsHeader*>(ws),
+                                        static_cast<cudaStream_t>(stream)));
+}
+
+kv_status paged_decode_attn(const kv_paged_shape* shape, const void* q, const void* k_new,
+                            const void* v_new, const int64_t* cu_add, const int64_t* slot_map,
+                            int64_t slot_capacity, void* k_pages, void* v_pages,
+                            const int32_t* block_table, const int32_t* lens, float softmax_scale,
+                            void* out, void* ws, size_t ws_bytes, void* stream) {
+  PagedShape s;
+  const kv_status st = paged_shape_check(shape, &s);
+  if (st != KV_OK) return st;
+  if (ws == nullptr || !aligned16(ws)) return KV_ERR_INVALID_ARG;
+  if ((k_new == nullptr) != (v_new == nullptr)) return KV_ERR_INVALID_ARG;
+  if (!std::isfinite(softmax_scale)) return KV_ERR_INVALID_ARG;
+  if (slot_capacity < 0 || slot_capacity > INT32_MAX) return KV_ERR_INVALID_ARG;
+  if (s.seqs == 0) return KV_OK;
+  if (q == nullptr || k_pages == nullptr || v_pages == nullptr || block_table == nullptr ||
+      lens == nullptr || out == nullptr)
+    return KV_ERR_INVALID_ARG;
+  if (k_new != nullptr && (cu_add == nullptr || (slot_map == nullptr && slot_capacity > 0)))
+    return KV_ERR_INVALID_ARG;
+  const void* rows[] = {q, k_new, v_new, k_pages, v_pages, out};
+  for (const void* x : rows)
+    if (!aligned16(x)) return KV_ERR_INVALID_ARG;
+  if (!aligned_to(cu_add, 8) || !aligned_to(slot_map, 8) || !aligned_to(block_table, 4) ||
+      !aligned_to(lens, 4))
+    return KV_ERR_INVALID_ARG;
+  if (ws_bytes < paged_decode_ws_bytes(s)) return KV_ERR_WORKSPACE;
+  return cuda_status(launch_paged_decode(s, q, k_new, v_new, cu_add, slot_map, slot_capacity,
+                                         k_pages, v_pages, block_table, lens, softmax_scale, out,
+                                         static_cast<char*>(ws),
+                                         static_cast<cudaStream_t>(stream)));
 }
 
 kv_status kv_check_device_status(void* ws, void* stream, uint32_t* info) {
