@@ -1,0 +1,286 @@
+// One warp's online softmax over tiles of K and V rows in shared memory, on the warp matrix
+// instructions, for up to 8 query rows:  (m, l, o) := running maximum, sum and output of
+//   p_r = exp2(c2 q . k_r - m),  l = sum p_r,  o = sum p_r v_r.
+//
+// A tile is RT rows, K then V, each as NSEG segments of [RT][128 bytes] with the 16-byte
+// pieces of row r permuted by r & 7 (TMA's 128-byte swizzle): every access below touches 8
+// different pieces of the 32 banks.
+//
+// m16n8k16 (bf16) and m16n8k8 (tf32) have 16 rows where a KV head has at most 8 queries.  The
+// other 8 rows carry what is lost by holding the left operand in few bits: rows 0..7 hold the
+// high parts, rows 8..15 the rest, and their sums are added at the end, in the same lane.
+//   bf16: q and k are bf16, their products are exact.  p is held as two bf16 (16 bits).
+//   fp32: q and p are held as two tf32 (22 bits), and so are k and v, at one instruction each.
+// The sums are fp32.  Against one bf16 p this costs no instruction, and the error of p (2^-16)
+// stays far under that of the bf16 output.
+//
+// The score fragment of lane (4 g + c) holds query g and rows 2c, 2c + 1 of each 8; as left
+// operand of the second product the same lane holds the same rows (for tf32, whose lane holds
+// columns c and c + 4, the rows of each 8 are taken in the order 0, 2, 4, 6, 1, 3, 5, 7), so p
+// never leaves its lane.
+#pragma once
+
+#include "kv_internal.cuh"
+#include "tc_ptx.cuh"
+
+namespace kv {
+namespace pmma {
+
+__device__ __forceinline__ void mma_bf16_16816(float (&d)[4], uint32_t a0, uint32_t a1,
+                                               uint32_t a2, uint32_t a3, uint32_t b0,
+                                               uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+      "{%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void mma_tf32_1688(float (&d)[4], uint32_t a0, uint32_t a1,
+                                              uint32_t a2, uint32_t a3, uint32_t b0,
+                                              uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+      "{%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ void ldsm4_t(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ float lds_f(uint32_t addr) {
+  float v;
+  asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+  return v;
+}
+// The nearest tf32 (11 significant bits) to x, as fp32 bits.
+__device__ __forceinline__ uint32_t tf32_of(float x) {
+  uint32_t r;
+  asm("cvt.rna.tf32.f32 %0, %1;" : "=r"(r) : "f"(x));
+  return r;
+}
+// x = hi + lo to 22 bits (x - hi is exact).
+__device__ __forceinline__ void tf32_split(float x, uint32_t& hi, uint32_t& lo) {
+  hi = tf32_of(x);
+  lo = tf32_of(x - __uint_as_float(hi));
+}
+__device__ __forceinline__ uint32_t bf16x2_of(float x, float y) {   // x in the low half
+  const __nv_bfloat162 b = __floats2bfloat162_rn(x, y);
+  return *reinterpret_cast<const uint32_t*>(&b);
+}
+
+// Byte offset of 16-byte piece c of row r within a tile of RT rows.
+template <int RT>
+__device__ __forceinline__ uint32_t piece(int r, int c) {
+  return (uint32_t)((c >> 3) * (RT * 128) + r * 128 + (((c ^ r) & 7) << 4));
+}
+
+template <typename T, int NSEG>
+struct Tile;
+
+// What both types share: lane (4 g + c)'s running state for query g, and its part of o:
+// columns 8 t + 2 c and + 1 for every t < NT.
+template <int NT>
+struct State {
+  float m, l;        // l: this lane's share of the sum
+  float o[NT][4];    // [0..1] high rows, [2..3] low rows
+  __device__ __forceinline__ void begin() {
+    m = -INFINITY;
+    l = 0.f;
+#pragma unroll
+    for (int t = 0; t < NT; ++t)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) o[t][e] = 0.f;
+  }
+  // New maximum of this lane's query from the tile's scores; o and l follow.
+  __device__ __forceinline__ void raise(float mt) {
+    mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, 1));
+    mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, 2));
+    if (__any_sync(0xffffffffu, mt > m)) {
+      const float mn = fmaxf(m, mt);
+      const float a = mn > m ? ptx::ex2(m - mn) : 1.f;   // 0 while m is -inf
+      m = mn;
+      l *= a;
+#pragma unroll
+      for (int t = 0; t < NT; ++t)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[t][e] *= a;
+    }
+  }
+  __device__ __forceinline__ float base() const { return m == -INFINITY ? 0.f : m; }
+  // After the last tile: l whole in every lane of the query, o in [0..1].
+  __device__ __forceinline__ void finish() {
+    l += __shfl_xor_sync(0xffffffffu, l, 1);
+    l += __shfl_xor_sync(0xffffffffu, l, 2);
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+      o[t][0] += o[t][2];
+      o[t][1] += o[t][3];
+    }
+  }
+};
+
+template <int NSEG>
+struct Tile<__nv_bfloat16, NSEG> : State<NSEG * 8> {
+  static constexpr int RT = 16;
+  static constexpr int NT = NSEG * 8;
+  static constexpr int D = NSEG * 64;     // columns held (d rounded up; the rest is zero)
+  static constexpr int NQ = NSEG * 8;     // 32-bit words of q per lane
+  uint32_t q[NQ];
+
+  // Words of q for query g = lane / 4 (zero past d and for g >= G).
+  static __device__ __forceinline__ void load_q(const __nv_bfloat16* src, int G, int d,
+                                                uint32_t (&w)[NQ]) {
+    const int lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
+#pragma unroll
+    for (int i = 0; i < NQ; ++i) {
+      const int x = 8 * i + 2 * c;
+      w[i] = g < G && x < d ? *reinterpret_cast<const uint32_t*>(src + g * d + x) : 0u;
+    }
+  }
+  __device__ __forceinline__ void set_q(const uint32_t (&w)[NQ]) {
+#pragma unroll
+    for (int i = 0; i < NQ; ++i) q[i] = w[i];
+  }
+
+  // One tile at shared addresses ks, vs; bit r of `mask`: row r counts.
+  __device__ __forceinline__ void tile(uint32_t ks, uint32_t vs, uint32_t mask, float c2) {
+    const int lane = threadIdx.x & 31, c = lane & 3;
+    float s[2][4];
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) s[j][e] = 0.f;
+#pragma unroll
+    for (int kk = 0; kk < 2 * NSEG; ++kk) {
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        uint32_t b[4];
+        ldsm4(b, ks + piece<RT>(8 * j + (lane & 7), 4 * kk + (lane >> 3)));
+        mma_bf16_16816(s[j], q[4 * kk], 0u, q[4 * kk + 1], 0u, b[0], b[1]);
+        mma_bf16_16816(s[j], q[4 * kk + 2], 0u, q[4 * kk + 3], 0u, b[2], b[3]);
+      }
+    }
+    float z[2][2], mt = -INFINITY;
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        z[j][e] = mask >> (8 * j + 2 * c + e) & 1 ? s[j][e] * c2 : -INFINITY;
+        mt = fmaxf(mt, z[j][e]);
+      }
+    this->raise(mt);
+    const float base = this->base();
+    uint32_t hi[2], lo[2];
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const float p0 = ptx::ex2(z[j][0] - base), p1 = ptx::ex2(z[j][1] - base);
+      this->l += p0 + p1;
+      hi[j] = bf16x2_of(p0, p1);
+      lo[j] = bf16x2_of(p0 - __uint_as_float(hi[j] << 16),
+                        p1 - __uint_as_float(hi[j] & 0xFFFF0000u));
+    }
+    // rows that do not count may hold anything: zeros instead (0 * NaN is NaN)
+    uint32_t keep[2];
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const uint32_t two = mask >> (8 * j + 2 * c) & 3u;
+      keep[j] = (two & 1u ? 0xFFFFu : 0u) | (two & 2u ? 0xFFFF0000u : 0u);
+    }
+    const bool whole = mask == 0xFFFFu;
+#pragma unroll
+    for (int t = 0; t < NT; t += 2) {
+      uint32_t b[4];
+      ldsm4_t(b, vs + piece<RT>((lane & 7) + (lane & 8), t + (lane >> 4)));
+      if (!whole) {
+        b[0] &= keep[0];
+        b[1] &= keep[1];
+        b[2] &= keep[0];
+        b[3] &= keep[1];
+      }
+      mma_bf16_16816(this->o[t], hi[0], lo[0], hi[1], lo[1], b[0], b[1]);
+      mma_bf16_16816(this->o[t + 1], hi[0], lo[0], hi[1], lo[1], b[2], b[3]);
+    }
+  }
+};
+
+template <int NSEG>
+struct Tile<float, NSEG> : State<NSEG * 4> {
+  static constexpr int RT = NSEG > 2 ? 8 : 16;
+  static constexpr int NT = NSEG * 4;
+  static constexpr int D = NSEG * 32;
+  static constexpr int NQ = NSEG * 8;
+  uint32_t qh[NQ], ql[NQ];
+
+  static __device__ __forceinline__ void load_q(const float* src, int G, int d,
+                                                uint32_t (&w)[NQ]) {
+    const int lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
+#pragma unroll
+    for (int i = 0; i < NQ; ++i) {
+      const int x = 4 * i + c;
+      w[i] = g < G && x < d ? __float_as_uint(src[g * d + x]) : 0u;
+    }
+  }
+  __device__ __forceinline__ void set_q(const uint32_t (&w)[NQ]) {
+#pragma unroll
+    for (int i = 0; i < NQ; ++i) tf32_split(__uint_as_float(w[i]), qh[i], ql[i]);
+  }
+
+  __device__ __forceinline__ void tile(uint32_t ks, uint32_t vs, uint32_t mask, float c2) {
+    constexpr int NB = RT / 8;
+    const int lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
+    float z[NB][2], mt = -INFINITY;
+#pragma unroll
+    for (int j = 0; j < NB; ++j) {
+      float s[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int k = 0; k < NT; ++k) {
+        uint32_t h0, l0, h1, l1;
+        tf32_split(lds_f(ks + piece<RT>(8 * j + g, 2 * k) + 4 * c), h0, l0);
+        tf32_split(lds_f(ks + piece<RT>(8 * j + g, 2 * k + 1) + 4 * c), h1, l1);
+        mma_tf32_1688(s, qh[2 * k], ql[2 * k], qh[2 * k + 1], ql[2 * k + 1], h0, h1);
+        mma_tf32_1688(s, qh[2 * k], ql[2 * k], qh[2 * k + 1], ql[2 * k + 1], l0, l1);
+      }
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        z[j][e] = mask >> (8 * j + 2 * c + e) & 1 ? (s[e] + s[2 + e]) * c2 : -INFINITY;
+        mt = fmaxf(mt, z[j][e]);
+      }
+    }
+    this->raise(mt);
+    const float base = this->base();
+#pragma unroll
+    for (int j = 0; j < NB; ++j) {
+      const float p0 = ptx::ex2(z[j][0] - base), p1 = ptx::ex2(z[j][1] - base);
+      this->l += p0 + p1;
+      uint32_t h0, l0, h1, l1;
+      tf32_split(p0, h0, l0);
+      tf32_split(p1, h1, l1);
+      const bool k0 = mask >> (8 * j + 2 * c) & 1, k1 = mask >> (8 * j + 2 * c + 1) & 1;
+#pragma unroll
+      for (int t = 0; t < NT; ++t) {
+        const int cp = 2 * t + (g >> 2), w = 4 * (g & 3);
+        float v0 = lds_f(vs + piece<RT>(8 * j + 2 * c, cp) + w);
+        float v1 = lds_f(vs + piece<RT>(8 * j + 2 * c + 1, cp) + w);
+        if (!k0) v0 = 0.f;
+        if (!k1) v1 = 0.f;
+        uint32_t vh0, vl0, vh1, vl1;
+        tf32_split(v0, vh0, vl0);
+        tf32_split(v1, vh1, vl1);
+        mma_tf32_1688(this->o[t], h0, l0, h1, l1, vh0, vh1);
+        mma_tf32_1688(this->o[t], h0, l0, h1, l1, vl0, vl1);
+      }
+    }
+  }
+};
+
+}  // namespace pmma
+}  // namespace kv
