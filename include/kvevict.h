@@ -440,7 +440,8 @@ KV_API kv_status flat_decode_attn_noalloc(const kv_shape* shape, const void* q,
  *
  * Limits: page a power of two from 8 to 256, d <= 128 (a multiple of 8), hq / hkv <= 8,
  * hkv <= 256, max_pages * page and num_pages below 2^31, a page_stride below 2^40 bytes, and
- * for kv_page_map at most KV_PAGE_MAP_MAX_TABLES tables.
+ * for kv_page_map at most KV_PAGE_MAP_MAX_TABLES tables, for paged_decode_attn
+ * seqs * hkv * max_pages * page below 2^34.
  * Alignment: rows (k, v, q, out, k_pages, ...) 16 bytes, strides multiples of 16 bytes, tables
  * only their element's, so that slices can be passed.
  */

@@ -302,64 +302,109 @@ def kv_paged_workspace_size(op: int, shape: KvPagedShape) -> int:
     return int(lib().kv_paged_workspace_size(op, ctypes.byref(shape)))
 
 
-def _need(t, dtype: str, count: int, what: str) -> None:
-    """A table's type and the entries the call may touch."""
-    if t is not None and not isinstance(t, int):
-        if str(t.dtype) != "torch." + dtype:
-            raise ValueError("%s must be %s" % (what, dtype))
-        if t.numel() < count:
-            raise ValueError("%s has %d entries, needs %d" % (what, t.numel(), count))
+_DT = {}   # the torch dtypes of the paged calls, once torch is imported
 
 
-def _rows_view(t, hp: int, d: int, what: str):
-    """Pointer and row stride (elements) of rows [n][hp][d] or [n][hp * d]; a row is contiguous,
-    rows may lie apart (parts of a fused projection)."""
-    if not t.is_cuda:
-        raise ValueError("tensor must be on a CUDA device")
-    if t.dim() < 2 or t.numel() != t.shape[0] * hp * d:
-        raise ValueError("%s must be rows of %d heads x %d" % (what, hp, d))
-    step = 1
-    for size, stride in zip(reversed(t.shape[1:]), reversed(t.stride()[1:])):
-        if size > 1 and stride != step:
-            raise ValueError("the rows of %s must be contiguous" % what)
-        step *= size
-    return t.data_ptr(), (t.stride(0) if t.shape[0] > 1 else hp * d)
+def _dtypes():
+    if not _DT:
+        import torch
+        _DT.update(i32=torch.int32, i64=torch.int64, rows={KV_BF16: torch.bfloat16,
+                                                           KV_F32: torch.float32},
+                   device=torch.cuda.current_device,
+                   stream=getattr(torch._C, "_cuda_getCurrentRawStream", None) or
+                   (lambda dev: torch.cuda.current_stream(dev).cuda_stream))
+    return _DT
 
 
-def _pool(shape: KvPagedShape, t, what: str) -> Optional[int]:
-    """Pointer of a page pool: its pages are dense, ``page_stride`` elements apart."""
+def _device(t, what: str) -> int:
+    """The current device (a host tensor raises before CUDA is asked)."""
+    if not isinstance(t, int) and not t.is_cuda:
+        raise ValueError("%s must be on a CUDA device" % what)
+    return _dtypes()["device"]()
+
+
+def _buf(t, dtype, count: int, dev: int, what: str) -> Optional[int]:
+    """Device pointer of a contiguous tensor of the type and at least the entries that the call
+    may touch, on the current device (None stays NULL, an int is a pointer already)."""
     if t is None or isinstance(t, int):
         return t
     if not t.is_cuda:
-        raise ValueError("tensor must be on a CUDA device")
-    if str(t.dtype) != ("torch.bfloat16" if shape.dtype == KV_BF16 else "torch.float32"):
-        raise ValueError("%s is not of the shape's dtype" % what)
+        raise ValueError("%s must be on a CUDA device" % what)
+    if t.get_device() != dev:
+        raise ValueError("%s is on another device than the current one" % what)
+    if dtype is not None and t.dtype is not dtype:
+        raise ValueError("%s must be %s" % (what, dtype))
+    if t.numel() < count:
+        raise ValueError("%s has %d entries, needs %d" % (what, t.numel(), count))
+    if not t.is_contiguous():
+        raise ValueError("%s must be contiguous" % what)
+    return t.data_ptr()
+
+
+def _rows_view(t, dtype, hp: int, d: int, dev: int, what: str):
+    """Pointer, count and stride (elements) of rows [n][hp][d] or [n][hp * d]; a row is
+    contiguous, rows may lie apart (parts of a fused projection)."""
+    if not t.is_cuda or t.get_device() != dev:
+        raise ValueError("%s must be on the current CUDA device" % what)
+    if t.dtype is not dtype:
+        raise ValueError("%s must be %s" % (what, dtype))
+    size = t.shape
+    n = size[0]
+    if len(size) < 2 or t.numel() != n * hp * d:
+        raise ValueError("%s must be rows of %d heads x %d" % (what, hp, d))
+    if t.is_contiguous():
+        return t.data_ptr(), n, hp * d
+    stride, step = t.stride(), 1
+    for k in range(len(size) - 1, 0, -1):
+        if size[k] > 1 and stride[k] != step:
+            raise ValueError("the rows of %s must be contiguous" % what)
+        step *= size[k]
+    return t.data_ptr(), n, (stride[0] if n > 1 else hp * d)
+
+
+def _pool(shape: KvPagedShape, t, dtype, dev: int, what: str) -> Optional[int]:
+    """Pointer of a page pool: its pages are dense, ``page_stride`` elements apart."""
+    if t is None or isinstance(t, int):
+        return t
+    if not t.is_cuda or t.get_device() != dev:
+        raise ValueError("%s must be on the current CUDA device" % what)
+    if t.dtype is not dtype:
+        raise ValueError("%s must be %s" % (what, dtype))
     inner = (shape.hkv // shape.tables) * shape.page * shape.d
-    stride = shape.page_stride or inner
-    if t.shape[0] < shape.num_pages or t[0].numel() != inner or not t[0].is_contiguous() or (
-            shape.num_pages > 1 and t.stride(0) != stride):
+    want, pages, size = shape.page_stride or inner, shape.num_pages, t.shape
+    ok = size[0] >= pages and t.numel() == size[0] * inner
+    if ok and not (want == inner and t.is_contiguous()):
+        stride, step = t.stride(), 1
+        for k in range(len(size) - 1, 0, -1):
+            ok = ok and (size[k] == 1 or stride[k] == step)
+            step *= size[k]
+        ok = ok and (pages == 1 or stride[0] == want)
+    if not ok:
         raise ValueError("%s must be [num_pages][heads][page][d], pages page_stride apart" % what)
     return t.data_ptr()
+
+
+def _stream_on(stream, dev: int) -> Optional[int]:
+    if stream is None:
+        return _DT["stream"](dev)
+    return stream if isinstance(stream, int) else stream.cuda_stream
 
 
 def kv_page_map(shape: KvPagedShape, lens, add, free_ring, free_state, block_table, lens_out,
                 free_out, cu_add, slot_map, ws, stream=None) -> None:
     """Block tables, slots and lengths for the rows each table gains or loses.  ``lens_out`` may
     be ``lens`` and ``free_out`` may be ``free_state``."""
+    dev, dt = _device(lens, "lens"), _dtypes()
+    i32, i64 = dt["i32"], dt["i64"]
     n = shape.seqs * shape.tables
-    _need(lens, "int32", n, "lens")
-    _need(add, "int32", n, "add")
-    _need(free_ring, "int32", shape.num_pages, "free_ring")
-    _need(free_state, "int64", 2, "free_state")
-    _need(block_table, "int32", n * shape.max_pages, "block_table")
-    _need(lens_out, "int32", n, "lens_out")
-    _need(free_out, "int64", 2, "free_out")
-    _need(cu_add, "int64", n + 1, "cu_add")
-    _need(slot_map, "int64", 0, "slot_map")
-    st = lib().kv_page_map(ctypes.byref(shape), _ptr(lens), _ptr(add), _ptr(free_ring),
-                           _ptr(free_state), slot_map.numel(), _ptr(block_table), _ptr(lens_out),
-                           _ptr(free_out), _ptr(cu_add), _ptr(slot_map), _ptr(ws), _nbytes(ws),
-                           _stream(stream))
+    st = lib().kv_page_map(
+        ctypes.byref(shape), _buf(lens, i32, n, dev, "lens"), _buf(add, i32, n, dev, "add"),
+        _buf(free_ring, i32, shape.num_pages, dev, "free_ring"),
+        _buf(free_state, i64, 2, dev, "free_state"), slot_map.numel(),
+        _buf(block_table, i32, n * shape.max_pages, dev, "block_table"),
+        _buf(lens_out, i32, n, dev, "lens_out"), _buf(free_out, i64, 2, dev, "free_out"),
+        _buf(cu_add, i64, n + 1, dev, "cu_add"), _buf(slot_map, i64, 0, dev, "slot_map"),
+        _buf(ws, None, 0, dev, "ws"), _nbytes(ws), _stream_on(stream, dev))
     _check("kv_page_map", st)
 
 
@@ -367,19 +412,18 @@ def kv_paged_write(shape: KvPagedShape, k, v, slot_map, n_rows, k_pages, v_pages
                    stream=None) -> None:
     """Rows of ``k`` and ``v`` ([n][heads per page][d], rows may lie apart) at their slots.
     ``n_rows`` (a device int64, or None): rows from there on are left out."""
-    hp = shape.hkv // shape.tables
-    kp, ks = _rows_view(k, hp, shape.d, "k")
-    vp, vs = _rows_view(v, hp, shape.d, "v")
-    if k.dtype != k_pages.dtype or v.dtype != v_pages.dtype:
-        raise ValueError("rows and pages must have one dtype")
-    if ks != vs or k.shape[0] != v.shape[0]:
+    dev, dt = _device(k, "k"), _dtypes()
+    i64, el = dt["i64"], dt["rows"].get(shape.dtype)
+    hp, d = shape.hkv // shape.tables, shape.d
+    kp, n, ks = _rows_view(k, el, hp, d, dev, "k")
+    vp, nv, vs = _rows_view(v, el, hp, d, dev, "v")
+    if ks != vs or n != nv:
         raise ValueError("k and v must have the same rows and row stride")
-    _need(slot_map, "int64", k.shape[0], "slot_map")
-    _need(n_rows, "int64", 1, "n_rows")
-    st = lib().kv_paged_write(ctypes.byref(shape), kp, vp, ks, _ptr(slot_map), k.shape[0],
-                              _ptr(n_rows), _pool(shape, k_pages, "k_pages"),
-                              _pool(shape, v_pages, "v_pages"), _ptr(ws), _nbytes(ws),
-                              _stream(stream))
+    st = lib().kv_paged_write(
+        ctypes.byref(shape), kp, vp, ks, _buf(slot_map, i64, n, dev, "slot_map"), n,
+        _buf(n_rows, i64, 1, dev, "n_rows"), _pool(shape, k_pages, el, dev, "k_pages"),
+        _pool(shape, v_pages, el, dev, "v_pages"), _buf(ws, None, 0, dev, "ws"), _nbytes(ws),
+        _stream_on(stream, dev))
     _check("kv_paged_write", st)
 
 
@@ -387,22 +431,18 @@ def paged_decode_attn(shape: KvPagedShape, q, k_new, v_new, cu_add, slot_map, k_
                       block_table, lens, softmax_scale: float, out, ws, stream=None) -> None:
     """One decode step over the paged cache; ``k_new`` / ``v_new`` / ``cu_add`` / ``slot_map``
     None: no rows are stored."""
-    n = shape.seqs * shape.tables
-    _need(block_table, "int32", n * shape.max_pages, "block_table")
-    _need(lens, "int32", n, "lens")
-    _need(cu_add, "int64", n + 1, "cu_add")
-    _need(slot_map, "int64", 0, "slot_map")
-    el = "bfloat16" if shape.dtype == KV_BF16 else "float32"
-    for t, heads, what in ((q, shape.hq, "q"), (out, shape.hq, "out"), (k_new, shape.hkv, "k_new"),
-                           (v_new, shape.hkv, "v_new")):
-        _need(t, el, shape.seqs * heads * shape.d, what)
-    st = lib().paged_decode_attn(ctypes.byref(shape), _ptr(q), _ptr(k_new), _ptr(v_new),
-                                 _ptr(cu_add), _ptr(slot_map),
-                                 0 if slot_map is None else slot_map.numel(),
-                                 _pool(shape, k_pages, "k_pages"),
-                                 _pool(shape, v_pages, "v_pages"), _ptr(block_table), _ptr(lens),
-                                 softmax_scale, _ptr(out), _ptr(ws), _nbytes(ws),
-                                 _stream(stream))
+    dev, dt = _device(q, "q"), _dtypes()
+    i32, i64, el = dt["i32"], dt["i64"], dt["rows"].get(shape.dtype)
+    seqs = shape.seqs
+    n, nq, nk = seqs * shape.tables, seqs * shape.hq * shape.d, seqs * shape.hkv * shape.d
+    st = lib().paged_decode_attn(
+        ctypes.byref(shape), _buf(q, el, nq, dev, "q"), _buf(k_new, el, nk, dev, "k_new"),
+        _buf(v_new, el, nk, dev, "v_new"), _buf(cu_add, i64, n + 1, dev, "cu_add"),
+        _buf(slot_map, i64, 0, dev, "slot_map"), 0 if slot_map is None else slot_map.numel(),
+        _pool(shape, k_pages, el, dev, "k_pages"), _pool(shape, v_pages, el, dev, "v_pages"),
+        _buf(block_table, i32, n * shape.max_pages, dev, "block_table"),
+        _buf(lens, i32, n, dev, "lens"), softmax_scale, _buf(out, el, nq, dev, "out"),
+        _buf(ws, None, 0, dev, "ws"), _nbytes(ws), _stream_on(stream, dev))
     _check("paged_decode_attn", st)
 
 

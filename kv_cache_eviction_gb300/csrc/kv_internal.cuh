@@ -28,6 +28,15 @@ inline int per_device(std::atomic<int> (&slot)[kMaxDevices], F make) {
   return v;
 }
 
+// Launch attribute of a programmatic dependent launch: the kernel may start while the one
+// before it on the stream finishes, and waits (griddepcontrol.wait) before touching memory.
+inline cudaLaunchAttribute pdl_attribute() {
+  cudaLaunchAttribute a{};
+  a.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  a.val.programmaticStreamSerializationAllowed = 1;
+  return a;
+}
+
 struct Shape {
   int B, L, Hq, Hkv, d, n, w, pool, dtype;
   __host__ __device__ int G() const { return Hq / Hkv; }

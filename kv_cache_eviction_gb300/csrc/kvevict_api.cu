@@ -83,7 +83,7 @@ static kv_status paged_shape_check(const kv_paged_shape* sh, PagedShape* out) {
   if (s.page < 8 || s.page > 256 || (s.page & (s.page - 1)) != 0) return KV_ERR_UNSUPPORTED;
   if ((int64_t)s.max_pages * s.page > INT32_MAX || s.num_pages > INT32_MAX)
     return KV_ERR_UNSUPPORTED;
-  if (s.U() > INT32_MAX || (int64_t)s.seqs * s.Hkv > INT32_MAX) return KV_ERR_UNSUPPORTED;
+  if ((int64_t)s.seqs * s.Hkv > INT32_MAX) return KV_ERR_UNSUPPORTED;
   const int64_t dense = (int64_t)s.Hp() * s.page * s.d;
   if (s.page_stride == 0) s.page_stride = dense;
   if (s.page_stride < dense || s.page_stride % (16 / s.esize()) != 0) return KV_ERR_INVALID_ARG;
@@ -580,6 +580,9 @@ kv_status paged_decode_attn(const kv_paged_shape* shape, const void* q, const vo
   if (!aligned_to(cu_add, 8) || !aligned_to(slot_map, 8) || !aligned_to(block_table, 4) ||
       !aligned_to(lens, 4))
     return KV_ERR_INVALID_ARG;
+  // the kernel counts tiles of at least 8 rows in 31 bits
+  if ((int64_t)s.seqs * s.Hkv > (((int64_t)1 << 34) - 1) / ((int64_t)s.max_pages * s.page))
+    return KV_ERR_UNSUPPORTED;
   if (ws_bytes < paged_decode_ws_bytes(s)) return KV_ERR_WORKSPACE;
   return cuda_status(launch_paged_decode(s, q, k_new, v_new, cu_add, slot_map, slot_capacity,
                                          k_pages, v_pages, block_table, lens, softmax_scale, out,

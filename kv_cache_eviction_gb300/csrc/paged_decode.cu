@@ -75,55 +75,58 @@ struct Cfg {
 struct PagedSmem {
   unsigned char ring[kPWarps][kRingBytes];   // after the stream: the parts of the units
   unsigned char side[kPWarps][kSideBytes];
-  int64_t strip[kPThreads];                  // tiles before thread t's tables
-  int64_t wsum[kPWarps];
+  uint32_t strip[kPThreads];                 // tiles before thread t's tables
+  uint32_t wsum[kPWarps];
+  uint32_t bnd[2];                           // the CTA's first tile and its end
   uint64_t full[kPWarps][kMaxStages];
   // the parts warp w leaves: of a unit that began before its tiles (a), of one that goes on
   // after them (b); unit or -1, and whether the unit of part a goes on as well
   int32_t a_unit[kPWarps], b_unit[kPWarps], a_open[kPWarps];
   int32_t some[kPWarps];                     // warp w has tiles
-  int64_t start[kPWarps + 1], end[kPWarps + 1];   // units of warp 0's part a, of warps' parts b
+  uint32_t start[kPWarps + 1], end[kPWarps + 1];   // units of warp 0's part a, of warps' parts b
   int32_t win[2];
 };
 static_assert(2 * kPWarps * kPartFloats * 4 <= kPWarps * kRingBytes, "parts fit the rings");
 
 // 32 tables in a warp: lane i holds table w0 + i's rows and the end of its tiles (all heads).
+// (Tile numbers are 32 bits: the host refuses shapes that could hold 2^31 tiles.)
 struct Window {
-  int64_t w0, base;   // first table, tiles before it
-  int len;
-  int64_t end;
+  int w0, len;
+  uint32_t end;
 };
 
 template <int RT>
-__device__ __forceinline__ int tiles_of(int len) { return (len + RT - 1) / RT; }
+__device__ __forceinline__ int tiles_of(int len) { return (int)(((uint32_t)len + RT - 1) / RT); }
 
-__device__ __forceinline__ int clamp_len(int len, int64_t most) {
-  return len < 0 ? 0 : len > most ? (int)most : len;
+__device__ __forceinline__ int clamp_len(int len, int most) {
+  return len < 0 ? 0 : len > most ? most : len;
 }
 
-template <int RT>
-__device__ __forceinline__ void load_window(Window& w, int64_t w0, int64_t base,
-                                            const PagedArgs& a) {
+__device__ __forceinline__ uint32_t warp_incl_scan(uint32_t x) {
   const int lane = threadIdx.x & 31;
-  w.w0 = w0;
-  w.base = base;
-  w.len = w0 + lane < a.U ? clamp_len(a.lens[w0 + lane], (int64_t)a.max_pages << a.shift) : 0;
-  int64_t x = (int64_t)tiles_of<RT>(w.len) * a.Hp;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const int64_t y = __shfl_up_sync(0xffffffffu, (long long)x, o);
+    const uint32_t y = __shfl_up_sync(0xffffffffu, x, o);
     if (lane >= o) x += y;
   }
-  w.end = base + x;
+  return x;
 }
-__device__ __forceinline__ int64_t window_end(const Window& w) {
-  return __shfl_sync(0xffffffffu, (long long)w.end, 31);
-}
-// Moves the window to the one that holds tile x (0 <= x < total; x not before it).
+// `base`: the tiles before table w0.
 template <int RT>
-__device__ __forceinline__ void seek(Window& w, int64_t x, const PagedArgs& a) {
+__device__ __forceinline__ void load_window(Window& w, int w0, uint32_t base, const PagedArgs& a) {
+  const int lane = threadIdx.x & 31;
+  w.w0 = w0;
+  w.len = w0 + lane < a.U ? clamp_len(a.lens[w0 + lane], a.max_pages << a.shift) : 0;
+  w.end = base + warp_incl_scan((uint32_t)tiles_of<RT>(w.len) * a.Hp);
+}
+__device__ __forceinline__ uint32_t window_end(const Window& w) {
+  return __shfl_sync(0xffffffffu, w.end, 31);
+}
+// Moves the window to the one that holds tile x (x < total, and not before the window).
+template <int RT>
+__device__ __forceinline__ void seek(Window& w, uint32_t x, const PagedArgs& a) {
   for (;;) {
-    const int64_t e = window_end(w);
+    const uint32_t e = window_end(w);
     if (x < e || w.w0 + 32 >= a.U) return;
     load_window<RT>(w, w.w0 + 32, e, a);
   }
@@ -194,7 +197,7 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap kmap,
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int N = (int)gridDim.x, c = (int)blockIdx.x;
   const int page = 1 << a.shift, d = a.d, G = a.G;
-  const int64_t most = (int64_t)a.max_pages << a.shift;
+  const int most = a.max_pages << a.shift;
   if (lane == 0) {
     for (int s = 0; s < S; ++s) ptx::mbar_init(&sm.full[warp][s], 1);
     ptx::fence_mbar_init();
@@ -204,82 +207,111 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap kmap,
     }
   }
 
-  // ---- 1. tiles of all tables
-  const int K = (a.U + kPThreads - 1) / kPThreads;   // tables per thread
-  int64_t sum = 0;
-  for (int i = 0; i < K; ++i) {
-    const int64_t u = (int64_t)tid * K + i;
-    int len = 1;
-    if (u < a.U) {
-      const int raw = a.lens[u];
-      len = clamp_len(raw, most);
-      if (raw != len && c == 0) raise_dev(a.hdr, DEV_PAGE_TABLE, (unsigned)u);
-      sum += tiles_of<RT>(len);
+  // a programmatic dependent launch: nothing of the call before is read or written until it ends
+  ptx::griddep_launch_dependents();
+  ptx::griddep_wait();
+
+  // ---- 1. tiles of all tables.  Up to 32 tables fit a warp's window: every warp finds its
+  // tiles by itself.  More: each thread sums a strip of K tables, the CTA their prefix.
+  const bool few = a.U <= 32;
+  const int K = few ? 1 : (a.U + kPThreads - 1) / kPThreads;
+  Window w;
+  uint32_t total;
+  {
+    uint32_t sum = 0;
+    for (int i = 0; i < K; ++i) {
+      const int u = (few ? lane : tid) * K + i;
+      int len = 1;
+      if (u < a.U) {
+        const int raw = a.lens[u];
+        len = clamp_len(raw, most);
+        if (raw != len && c == 0) raise_dev(a.hdr, DEV_PAGE_TABLE, (unsigned)u);
+        sum += tiles_of<RT>(len);
+      } else if (few) {
+        len = 0;
+      }
+      if (few) {
+        w.w0 = 0;
+        w.len = len;
+      }
+      // tables with no rows: zeros, table u by CTA u % N
+      uint32_t todo = __ballot_sync(0xffffffffu, u < a.U && len == 0);
+      while (todo) {
+        const int src = __ffs(todo) - 1;
+        todo &= todo - 1;
+        const int ut = ((few ? 0 : warp * 32) + src) * K + i;
+        if (ut % N != c || (few && warp != (src & (kPWarps - 1)))) continue;
+        T* dst = (T*)a.out + (int64_t)ut * a.Hp * G * d;
+        const int n16 = a.Hp * G * d * (int)sizeof(T) / 16;
+        for (int x = lane; x < n16; x += 32)
+          reinterpret_cast<uint4*>(dst)[x] = make_uint4(0u, 0u, 0u, 0u);
+      }
     }
-    // tables with no rows: zeros, table u by CTA u % N
-    const bool zero = u < a.U && len == 0 && (int)(u % N) == c;
-    uint32_t todo = __ballot_sync(0xffffffffu, zero);
-    while (todo) {
-      const int src = __ffs(todo) - 1;
-      todo &= todo - 1;
-      const int64_t ut = (int64_t)(warp * 32 + src) * K + i;
-      T* dst = (T*)a.out + ut * a.Hp * G * d;
-      const int n16 = a.Hp * G * d * (int)sizeof(T) / 16;
-      for (int x = lane; x < n16; x += 32)
-        reinterpret_cast<uint4*>(dst)[x] = make_uint4(0u, 0u, 0u, 0u);
+    if (few) {
+      w.end = warp_incl_scan(sum * a.Hp);
+      total = window_end(w);
+    } else {
+      const uint32_t incl = warp_incl_scan(sum);
+      if (lane == 31) sm.wsum[warp] = incl;
+      __syncthreads();
+      uint32_t before = 0;
+      total = 0;
+#pragma unroll
+      for (int k = 0; k < kPWarps; ++k) {
+        if (k == warp) before = total;
+        total += sm.wsum[k];
+      }
+      sm.strip[tid] = before + incl - sum;
+      total *= a.Hp;
+      __syncthreads();
     }
   }
-  int64_t incl = sum;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int64_t y = __shfl_up_sync(0xffffffffu, (long long)incl, o);
-    if (lane >= o) incl += y;
-  }
-  if (lane == 31) sm.wsum[warp] = incl;
-  __syncthreads();
-  int64_t total = 0, before = 0;
-#pragma unroll
-  for (int w = 0; w < kPWarps; ++w) {
-    if (w == warp) before = total;
-    total += sm.wsum[w];
-  }
-  sm.strip[tid] = before + incl - sum;
-  total *= a.Hp;
-  __syncthreads();
-  const int64_t want = (total + kMinTiles - 1) / kMinTiles;
-  const int Ne = (int)(want > N ? N : want);   // CTAs that take tiles
-  if (c >= Ne) return;
+  const uint32_t want = (total + kMinTiles - 1) / kMinTiles;
+  const uint32_t Ne = want > (uint32_t)N ? N : want;   // CTAs that take tiles
+  if (c >= (int)Ne) return;
 
   // the window of tables that holds tile x
-  auto find = [&](int64_t x, Window& w) {
+  auto find = [&](uint32_t x) {
+    if (few) return;
     int lo = 0, hi = kPThreads;
     while (hi - lo > 1) {
       const int mid = (lo + hi) >> 1;
       if (sm.strip[mid] * a.Hp <= x) lo = mid;
       else hi = mid;
     }
-    load_window<RT>(w, (int64_t)lo * K, sm.strip[lo] * a.Hp, a);
+    load_window<RT>(w, lo * K, sm.strip[lo] * a.Hp, a);
     seek<RT>(w, x, a);
   };
   // CTA k's first tile: total k / Ne, moved to the nearer end of a short unit it falls in
-  auto bound = [&](int64_t k) -> int64_t {
-    const int64_t x = total * k / Ne;
-    if (x <= 0 || x >= total) return x;
-    Window w;
-    find(x, w);
+  auto bound = [&](uint32_t k) -> uint32_t {
+    const uint32_t x = total / Ne * k + total % Ne * k / Ne;
+    if (x == 0 || x >= total) return x;
+    find(x);
     const int j = __popc(__ballot_sync(0xffffffffu, w.end <= x));
-    const int nt = tiles_of<RT>(__shfl_sync(0xffffffffu, w.len, j));
-    const int64_t tb = __shfl_sync(0xffffffffu, (long long)w.end, j) - (int64_t)nt * a.Hp;
-    const int64_t lo = tb + (x - tb) / nt * nt;
+    const uint32_t nt = tiles_of<RT>(__shfl_sync(0xffffffffu, w.len, j));
+    const uint32_t tb = __shfl_sync(0xffffffffu, w.end, j) - nt * a.Hp;
+    const uint32_t lo = tb + (x - tb) / nt * nt;
     if (nt > kSnapTiles) return x;
     return x - lo <= lo + nt - x ? lo : lo + nt;
   };
-  const int64_t b0 = bound(c), b1 = bound(c + 1);
-  const int64_t span = b1 - b0;
-  if (span <= 0) return;   // uniform in the CTA
+  uint32_t b0, b1;
+  if (few) {
+    b0 = bound(c);
+    b1 = bound(c + 1);
+  } else {
+    if (warp < 2) {
+      const uint32_t b = bound(c + warp);
+      if (lane == 0) sm.bnd[warp] = b;
+    }
+    __syncthreads();
+    b0 = sm.bnd[0];
+    b1 = sm.bnd[1];
+  }
+  const uint32_t span = b1 - b0;
+  if (span == 0) return;   // uniform in the CTA
   // (rounded up: warp 0 has the CTA's first tile)
-  const int64_t xs = b0 + (span * warp + kPWarps - 1) / kPWarps;
-  const int64_t xe = b0 + (span * (warp + 1) + kPWarps - 1) / kPWarps;
+  const uint32_t xs = b0 + (uint32_t)(((uint64_t)span * warp + kPWarps - 1) / kPWarps);
+  const uint32_t xe = b0 + (uint32_t)(((uint64_t)span * (warp + 1) + kPWarps - 1) / kPWarps);
 
   // ---- 2. this warp's tiles
   unsigned char* ring = sm.ring[warp];
@@ -294,86 +326,81 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap kmap,
   float am = -INFINITY, al = 0.f, ao[NT][2];   // part a
   int32_t unit_a = -1, unit_b = -1;
   bool open_a = false;
-  int64_t start_a = 0, end_a = 0, start_b = 0, end_b = 0;
+  uint32_t start_a = 0, end_a = 0, start_b = 0, end_b = 0;
   int issued = 0, consumed = 0;   // stage uses
   bool ok = true;
   if (xs < xe) {
-    Window w;
-    find(xs, w);
+    find(xs);
     // lane i's tile x0 + i (nothing past xe)
-    auto describe = [&](int64_t x0) -> Desc {
+    auto describe = [&](uint32_t x0) -> Desc {
       Desc t{-1, 0, 0, 0, 0, 0, 0u, -1};
-      const int64_t x = x0 + lane;
+      const uint32_t x = x0 + lane;
       bool open = x < xe;
-      seek<RT>(w, x0 < xe ? x0 : xe - 1, a);
-      while (__any_sync(0xffffffffu, open)) {
-        const int64_t wend = window_end(w);
+      for (;;) {
+        const uint32_t wend = window_end(w);
         // tables whose tiles end at or before x
         int j = 0;
 #pragma unroll
-        for (int step = 16; step > 0; step >>= 1) {
-          const int64_t e = __shfl_sync(0xffffffffu, (long long)w.end, j + step - 1);
-          if (e <= x) j += step;
-        }
-        const int jj = j < 31 ? j : 31;
-        const int len = __shfl_sync(0xffffffffu, w.len, jj);
-        const int64_t e = __shfl_sync(0xffffffffu, (long long)w.end, jj);
+        for (int step = 16; step > 0; step >>= 1)
+          if (__shfl_sync(0xffffffffu, w.end, j + step - 1) <= x) j += step;
+        const int len = __shfl_sync(0xffffffffu, w.len, j & 31);
+        const uint32_t e = __shfl_sync(0xffffffffu, w.end, j & 31);
         if (open && x < wend) {
           open = false;
-          const int nt = tiles_of<RT>(len);
-          const int64_t y = x - (e - (int64_t)nt * a.Hp);
-          const int h = (int)(y / nt), tt = (int)(y - (int64_t)h * nt);
-          const int64_t u = w.w0 + jj;
+          const uint32_t nt = tiles_of<RT>(len);
+          const uint32_t y = x - (e - nt * a.Hp);
+          const int h = (int)(y / nt), tt = (int)(y - h * nt);
+          const int u = w.w0 + j;
           const int r0 = tt * RT, nv = len - r0 < RT ? len - r0 : RT;
-          const int32_t* entry = a.table + u * a.max_pages + (r0 >> a.shift);
-          t.unit = (int32_t)(u * a.Hp + h);
+          const int32_t* entry = a.table + (int64_t)u * a.max_pages + (r0 >> a.shift);
+          t.unit = u * a.Hp + h;
           t.row = h * page + (r0 & (page - 1));
           t.tt = tt;
           t.nt = nt;
           t.mask = (1u << nv) - 1u;
-          t.page = entry[0];
-          bool bad = t.page < 0 || t.page >= a.num_pages;
-          if (bad) {
-            t.page = 0;
-            t.mask &= page < RT ? ~0xFFu : 0u;
-          }
-          if (page < RT && nv > page) {
-            t.page2 = entry[1];
-            if (t.page2 < 0 || t.page2 >= a.num_pages) {
-              t.page2 = 0;
-              t.mask &= 0xFFu;
-              bad = true;
-            }
-          }
           if (tt == 0) t.mask |= kFirst;
-          if (tt == nt - 1) {
-            t.mask |= kLast;
-            if (has_new) {
-              const int64_t c0 = a.cu[u], c1 = a.cu[u + 1];
-              if (c1 > c0 && c1 > 0 && c1 <= a.slot_cap) t.slot = a.slots[c1 - 1];
-              if (t.slot < -1 || t.slot >= (a.num_pages << a.shift)) {
-                t.slot = -1;
-                bad = true;
-              }
-              if (t.slot >= 0) t.mask |= 1u << (nv - 1);
-            }
-          }
-          if (bad) raise_dev(a.hdr, DEV_PAGE_ID, (unsigned)u);
+          if (tt == (int)nt - 1) t.mask |= kLast;
+          t.page = entry[0];
+          if (page < RT && nv > page) t.page2 = entry[1];
         }
-        if (__any_sync(0xffffffffu, open)) {
-          if (w.w0 + 32 >= a.U) break;
-          load_window<RT>(w, w.w0 + 32, wend, a);
-        }
+        if (!__any_sync(0xffffffffu, open) || w.w0 + 32 >= a.U) break;
+        load_window<RT>(w, w.w0 + 32, wend, a);
       }
       return t;
     };
-    const int64_t count = xe - xs;
-    Desc cur = describe(xs), nxt = describe(xs + 32);
-    int64_t cur0 = 0;   // index of cur's lane 0
+    // pages outside the pool: their rows do not count (page 0 is read in their place)
+    auto check_pages = [&](Desc& t) {
+      bool bad = t.page < 0 || t.page >= a.num_pages;
+      if (bad) {
+        t.page = 0;
+        t.mask &= page < RT ? ~0xFFu : ~0xFFFFu;
+      }
+      if (t.page2 < 0 || t.page2 >= a.num_pages) {
+        t.page2 = 0;
+        t.mask &= ~0xFF00u;
+        bad = true;
+      }
+      if (bad) raise_dev(a.hdr, DEV_PAGE_ID, (unsigned)t.unit);
+    };
+    // where the new row of a unit's last tile goes
+    auto look_up_slot = [&](Desc& t) {
+      if (!has_new || !(t.mask & kLast)) return;
+      const int u = t.unit / a.Hp;
+      const int64_t c0 = a.cu[u], c1 = a.cu[u + 1];
+      if (c1 > c0 && c1 > 0 && c1 <= a.slot_cap) t.slot = a.slots[c1 - 1];
+      if (t.slot < -1 || t.slot >= (a.num_pages << a.shift)) {
+        t.slot = -1;
+        raise_dev(a.hdr, DEV_PAGE_ID, (unsigned)t.unit);
+      }
+    };
+    const int count = (int)(xe - xs);
+    Desc cur = describe(xs), nxt{-1, 0, 0, 0, 0, 0, 0u, -1};
+    check_pages(cur);
+    int cur0 = 0;   // index of cur's lane 0
 
     // tile i (of this warp) into the ring: the lane that knows it issues
-    auto issue = [&](int64_t i) {
-      const int src = (int)(i - cur0);   // 0..63
+    auto issue = [&](int i) {
+      const int src = i - cur0;   // 0..63
       const Desc& t = src < 32 ? cur : nxt;
       const int s = issued % S;
       if (lane == (src & 31)) {
@@ -408,20 +435,31 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap kmap,
       ++issued;
     };
     __syncwarp();   // the barriers are initialised
-    int64_t next = 0;
+    int next = 0;
     for (; next < S && next < count; ++next) issue(next);
+    // (with the first copies under way)
+    look_up_slot(cur);
+    if (count > 32) {
+      nxt = describe(xs + 32);
+      check_pages(nxt);
+      look_up_slot(nxt);
+    }
 
     uint32_t qw[Tl::NQ];
     int32_t q_unit = -1;   // unit whose q words qw holds
     bool whole = false;    // the warp has the unit from its first tile on
-    for (int64_t i = 0; i < count; ++i) {
+    for (int i = 0; i < count; ++i) {
       if (i - cur0 == 32) {
         cur = nxt;
         cur0 += 32;
-        nxt = describe(xs + cur0 + 32);
+        if (count - cur0 > 32) {
+          nxt = describe(xs + cur0 + 32);
+          check_pages(nxt);
+          look_up_slot(nxt);
+        }
       }
-      const int src = (int)(i - cur0);
-      const uint32_t mask = __shfl_sync(0xffffffffu, cur.mask, src);
+      const int src = i - cur0;
+      uint32_t mask = __shfl_sync(0xffffffffu, cur.mask, src);
       const int32_t unit = __shfl_sync(0xffffffffu, cur.unit, src);
       if (i == 0 || (mask & kFirst)) {
         if (q_unit != unit) Tl::load_q(qp + (int64_t)unit * G * d, G, d, qw);
@@ -450,8 +488,10 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap kmap,
           cp_async_wait_all();
           __syncwarp();
           if (slot >= 0) {
-            // the new row is the highest that counts: to its place in the tile and to its slot
-            const int r = 31 - __clz((int)(mask & 0xFFFFu));
+            // to its place in the tile, the unit's last row, and to its slot
+            const int u = unit / a.Hp;
+            const int r = (clamp_len(a.lens[u], most) - 1) & (RT - 1);
+            mask |= 1u << r;
             const int64_t at = (slot >> a.shift) * a.page_stride +
                                (((int64_t)(unit % a.Hp) << a.shift) + (slot & (page - 1))) * d;
             for (int p = lane; p < pieces; p += 32) {
@@ -479,8 +519,8 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap kmap,
       // ---- the end of a unit, or of the warp's tiles
       if ((mask & kLast) || i == count - 1) {
         att.finish();
-        const int64_t start = xs + i - __shfl_sync(0xffffffffu, cur.tt, src);
-        const int64_t end = start + __shfl_sync(0xffffffffu, cur.nt, src);
+        const uint32_t start = xs + i - __shfl_sync(0xffffffffu, cur.tt, src);
+        const uint32_t end = start + __shfl_sync(0xffffffffu, cur.nt, src);
         if (whole && (mask & kLast)) {
           const int g = lane >> 2, col = 2 * (lane & 3);
           if (g < G) {
@@ -600,14 +640,16 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap kmap,
   if (cross_a < 0 && cross_b < 0) return;   // uniform in the CTA
 
   // units that cross CTAs: the CTA that holds tile x, and the last of a unit's CTAs merges
-  auto cta_of = [&](int64_t x) { return ((x + 1) * Ne + total - 1) / total - 1; };
+  auto cta_of = [&](uint32_t x) {
+    return (int)((((uint64_t)x + 1) * Ne + total - 1) / total) - 1;
+  };
   __threadfence();
   __syncthreads();
   if (tid < 2) {
     const int cand = tid == 0 ? cross_a : cross_b;
     int won = -1;
     if (cand >= 0) {
-      const int64_t ca = cta_of(sm.start[cand]), cb = cta_of(sm.end[cand] - 1);
+      const int ca = cta_of(sm.start[cand]), cb = cta_of(sm.end[cand] - 1);
       const uint32_t old = atomicAdd(&a.tick[ca], 1u);
       if (old == (uint32_t)(cb - ca)) {
         atomicExch(&a.tick[ca], 0u);
@@ -622,7 +664,7 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap kmap,
     const int cand = sm.win[y];
     if (cand < 0) continue;
     const int32_t unit = cand == 0 ? sm.a_unit[0] : sm.b_unit[cand - 1];
-    const int ca = (int)cta_of(sm.start[cand]), cb = (int)cta_of(sm.end[cand] - 1);
+    const int ca = cta_of(sm.start[cand]), cb = cta_of(sm.end[cand] - 1);
     for (int idx = tid; idx < nsl; idx += kPThreads) {
       const int g = idx / (D / 4), col = (idx - g * (D / 4)) * 4;
       float M = -INFINITY, L = 0.f;
@@ -714,8 +756,15 @@ cudaError_t launch_t(const PagedShape& s, const PagedArgs& a, cudaStream_t st) {
   int64_t grid = cdiv(tiles, kMinTiles);
   if (grid > num_sms()) grid = num_sms();
   if (grid > kMaxCtas) grid = kMaxCtas;
-  paged_decode_kernel<T, NSEG><<<(unsigned)grid, kPThreads, smem, st>>>(km, vm, a);
-  const cudaError_t e = cudaGetLastError();
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3((unsigned)grid);
+  cfg.blockDim = dim3(kPThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1] = {pdl_attribute()};
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, paged_decode_kernel<T, NSEG>, km, vm, a);
   if (e == cudaSuccess) count_launches(1);
   return e;
 }

@@ -69,6 +69,13 @@ def test_unsupported_shapes(L, far):
     assert call_decode(L, s) == kv.KV_ERR_UNSUPPORTED
 
 
+def test_decode_counts_its_tiles_in_31_bits(L):
+    s = shape(seqs=1 << 11, max_pages=(1 << 16) - 1, page=16)     # 2^14 heads of 2^20 - 16 rows
+    n = kv.kv_paged_workspace_size(kv.KV_OP_PAGED_DECODE, s)
+    assert call_decode(L, s, n=n - 1) == kv.KV_ERR_WORKSPACE
+    assert call_decode(L, shape(seqs=1 << 11, max_pages=1 << 16)) == kv.KV_ERR_UNSUPPORTED
+
+
 def test_workspace_sizes(L):
     for op in OPS:
         n = kv.kv_paged_workspace_size(op, shape())
