@@ -2,12 +2,11 @@
 //   z_r = scale * q . k_r,  p = softmax(z) over the rows of the table,  o = sum_r p_r v_r.
 //
 // The step reads every K and V row once and little else: it is bound by that stream, or by
-// latency when the cache is small.  So the rows are split evenly, whatever the lengths, and
-// every SM keeps close to 200 KB of loads in flight.
+// latency when the cache is small.  So the rows are split evenly, whatever the lengths.
 //
-//   1. Every CTA (one per SM, 8 warps) reads the tables' lengths.  In tiles of RT rows, the
-//      units (table, head) laid one after the other are one range [0, total): CTA c takes
-//      [total c / Ne, total (c + 1) / Ne) and a warp an eighth of that.  A CTA boundary inside a
+//   1. Every CTA reads the tables' lengths.  In tiles of RT rows, the units (table, head) laid
+//      one after the other are one range [0, total): CTA c takes [total c / Ne, total (c + 1) /
+//      Ne) and each of its warps an equal part of that.  A CTA boundary that falls inside a
 //      short unit moves to the nearer end of it, so only long units cross CTAs.
 //   2. A warp walks its tiles 32 at a time: lane i works out tile i (its table by a search
 //      over 32 tables' running sums, then the page number) and later issues its TMA boxes.
@@ -25,6 +24,9 @@
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
+#include <cfloat>
+#include <cmath>
+
 #include <mutex>
 
 #include "paged_mma.cuh"
@@ -32,17 +34,17 @@
 namespace kv {
 namespace {
 
-constexpr int kPWarps = 8;
+constexpr int kPWarps = 4;
+constexpr int kCtasPerSm = 2;
 constexpr int kPThreads = kPWarps * 32;
-constexpr int kMaxCtas = 160;
-constexpr int kRingBytes = 24 * 1024;   // of a warp
-constexpr int kSideBytes = 3 * 1024;    // of a warp: the new rows of its stages
+constexpr int kMaxCtas = 320;
+constexpr int kRingBytes = 16 * 1024;   // of a warp
 constexpr int kMaxStages = 6;
 // Tiles per CTA at least: a small call runs on as few CTAs as that allows.
-constexpr int kMinTiles = 16;
-// A CTA boundary inside a unit of at most this many tiles moves to the unit's nearer end.
+constexpr int kMinTiles = 8;
+// A boundary inside a unit of at most this many tiles moves to the unit's nearer end.
 constexpr int kSnapTiles = 16;
-// Part of a unit in the workspace or in shared memory: max[8], sum[8], then o[G][D].
+// Part of a unit in the workspace: max[8], sum[8], then o[G][D].
 constexpr int kPartHead = 16;
 constexpr int kPartFloats = kPartHead + 8 * 128;
 
@@ -54,11 +56,12 @@ struct PagedArgs {
   const int32_t *table, *lens;
   void* out;
   WsHeader* hdr;
-  uint32_t* tick;
-  float* part;
+  uint32_t* tick;   // [k]: parts done of the unit that crosses CTA k's end
+  float* part;      // two parts a CTA
+  float* far;       // a part a for each warp
   int U, Hp, G, d, shift, max_pages;
   int64_t num_pages, page_stride;
-  float c2;   // softmax scale * log2 e
+  pmma::Scale scale;
 };
 
 template <typename T, int NSEG>
@@ -68,25 +71,31 @@ struct Cfg {
   static constexpr int kRow = NSEG * 128;                  // bytes of a row in a stage
   static constexpr int kHalf = RT * kRow;                  // K, then V
   static constexpr int kStages = kRingBytes / (2 * kHalf);
-  static_assert(kStages >= 3 && kStages <= kMaxStages, "ring");
-  static_assert(kStages * 2 * kRow <= kSideBytes, "new rows");
+  static_assert(kStages >= 2 && kStages <= kMaxStages, "ring");
+  static constexpr int kSide = kStages * 2 * kRow;         // of a warp: its stages' new rows
+  static_assert(2 * 8 * Tl::D * 4 <= 2 * kHalf, "a warp's two parts fit one stage");
 };
 
+template <typename C>
 struct PagedSmem {
-  unsigned char ring[kPWarps][kRingBytes];   // after the stream: the parts of the units
-  unsigned char side[kPWarps][kSideBytes];
+  unsigned char ring[kPWarps][kRingBytes];
+  unsigned char side[kPWarps][C::kSide];
   uint32_t strip[kPThreads];                 // tiles before thread t's tables
+  int32_t lens[kPThreads];                   // rows per table, where a thread has one table
   uint32_t wsum[kPWarps];
-  uint32_t bnd[2];                           // the CTA's first tile and its end
   uint64_t full[kPWarps][kMaxStages];
-  // the parts warp w leaves: of a unit that began before its tiles (a), of one that goes on
-  // after them (b); unit or -1, and whether the unit of part a goes on as well
+  // the parts warp w leaves in one of its stages (at byte `at`): of a unit that began before
+  // its tiles (a), of one that goes on after them (b); unit or -1, and whether the unit of
+  // part a goes on as well
+  float ml[kPWarps][2][16];                  // max[8], sum[8] of parts a and b
+  int32_t at[kPWarps];
   int32_t a_unit[kPWarps], b_unit[kPWarps], a_open[kPWarps];
+  int32_t far[kPWarps];                      // part a is in the workspace
   int32_t some[kPWarps];                     // warp w has tiles
-  uint32_t start[kPWarps + 1], end[kPWarps + 1];   // units of warp 0's part a, of warps' parts b
-  int32_t win[2];
+  uint2 ends[kPWarps][2];                    // first tile and end of the units of warp w's
+                                             // first and last tiles
+  int32_t won[2];                            // this CTA's part of a crossing unit was the last
 };
-static_assert(2 * kPWarps * kPartFloats * 4 <= kPWarps * kRingBytes, "parts fit the rings");
 
 // 32 tables in a warp: lane i holds table w0 + i's rows and the end of its tiles (all heads).
 // (Tile numbers are 32 bits: the host refuses shapes that could hold 2^31 tiles.)
@@ -111,24 +120,26 @@ __device__ __forceinline__ uint32_t warp_incl_scan(uint32_t x) {
   }
   return x;
 }
-// `base`: the tiles before table w0.
-template <int RT>
-__device__ __forceinline__ void load_window(Window& w, int w0, uint32_t base, const PagedArgs& a) {
+// `base`: the tiles before table w0; `lens`: the lengths, cut to the table.
+template <int RT, typename Lens>
+__device__ __forceinline__ void load_window(Window& w, int w0, uint32_t base, const PagedArgs& a,
+                                            Lens lens) {
   const int lane = threadIdx.x & 31;
   w.w0 = w0;
-  w.len = w0 + lane < a.U ? clamp_len(a.lens[w0 + lane], a.max_pages << a.shift) : 0;
+  w.len = w0 + lane < a.U ? lens(w0 + lane) : 0;
   w.end = base + warp_incl_scan((uint32_t)tiles_of<RT>(w.len) * a.Hp);
 }
 __device__ __forceinline__ uint32_t window_end(const Window& w) {
   return __shfl_sync(0xffffffffu, w.end, 31);
 }
 // Moves the window to the one that holds tile x (x < total, and not before the window).
-template <int RT>
-__device__ __forceinline__ void seek(Window& w, uint32_t x, const PagedArgs& a) {
+template <int RT, typename Lens>
+__device__ __forceinline__ void seek(Window& w, uint32_t x, const PagedArgs& a, Lens lens) {
+#pragma unroll 1
   for (;;) {
     const uint32_t e = window_end(w);
     if (x < e || w.w0 + 32 >= a.U) return;
-    load_window<RT>(w, w.w0 + 32, e, a);
+    load_window<RT>(w, w.w0 + 32, e, a, lens);
   }
 }
 
@@ -137,8 +148,8 @@ struct Desc {
   int32_t unit;
   int32_t page, page2;   // page2: of the tile's second 8 rows, when a page holds 8
   int32_t row;           // row of the pool's page: head * page + first row within the page
-  int32_t tt, nt;        // the tile within its unit, and the unit's tiles
-  uint32_t mask;         // rows that count; kFirst / kLast: the unit's first / last tile
+  uint32_t mask;         // bits 0..15: rows that count; kFirst / kLast: the unit's first / last
+                         // tile; bits 24..27: its last row
   int64_t slot;          // where the new row (the unit's last) goes, or -1
 };
 constexpr uint32_t kFirst = 1u << 16, kLast = 1u << 17;
@@ -169,22 +180,32 @@ __device__ __forceinline__ void cp_async_wait_all() {
   asm volatile("cp.async.wait_all;" ::: "memory");
 }
 
-// Running merge of parts: (M, L, acc) with one part's (m, l, o).
-__device__ __forceinline__ void merge_part(float m, float l, const float4& o, float& M, float& L,
-                                           float4& acc) {
-  if (m == -INFINITY) return;
-  const float mn = fmaxf(M, m);
-  const float f = ptx::ex2(M - mn), w = ptx::ex2(m - mn);   // f is 0 while M is -inf
+// Merge of up to kB parts (max, sum, 4 outputs each; max -inf: none) into (M, L, acc).
+template <int kB>
+__device__ __forceinline__ void merge_parts(const float (&m)[kB], const float (&l)[kB],
+                                            const float4 (&o)[kB], float& M, float& L,
+                                            float4& acc) {
+  float mn = M;
+#pragma unroll
+  for (int b = 0; b < kB; ++b) mn = fmaxf(mn, m[b]);
+  if (mn == -INFINITY) return;
+  const float f = ptx::ex2(M - mn);   // 0 while M is -inf
   M = mn;
-  L = fmaf(L, f, l * w);
-  acc.x = fmaf(acc.x, f, o.x * w);
-  acc.y = fmaf(acc.y, f, o.y * w);
-  acc.z = fmaf(acc.z, f, o.z * w);
-  acc.w = fmaf(acc.w, f, o.w * w);
+  L *= f;
+  acc = make_float4(acc.x * f, acc.y * f, acc.z * f, acc.w * f);
+#pragma unroll
+  for (int b = 0; b < kB; ++b) {
+    const float w = ptx::ex2(m[b] - mn);
+    L = fmaf(l[b], w, L);
+    acc.x = fmaf(o[b].x, w, acc.x);
+    acc.y = fmaf(o[b].y, w, acc.y);
+    acc.z = fmaf(o[b].z, w, acc.z);
+    acc.w = fmaf(o[b].w, w, acc.w);
+  }
 }
 
 template <typename T, int NSEG>
-__global__ void __launch_bounds__(kPThreads, 1)
+__global__ void __launch_bounds__(kPThreads, kCtasPerSm)
 paged_decode_kernel(const __grid_constant__ CUtensorMap kmap,
                     const __grid_constant__ CUtensorMap vmap, const PagedArgs a) {
   using C = Cfg<T, NSEG>;
@@ -192,7 +213,7 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap kmap,
   constexpr int RT = C::RT, S = C::kStages, NT = Tl::NT, D = Tl::D;
   constexpr int kSegElems = 128 / (int)sizeof(T);
   extern __shared__ unsigned char dsm_raw[];
-  PagedSmem& sm = *reinterpret_cast<PagedSmem*>(
+  PagedSmem<C>& sm = *reinterpret_cast<PagedSmem<C>*>(
       (reinterpret_cast<uintptr_t>(dsm_raw) + 1023) & ~(uintptr_t)1023);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int N = (int)gridDim.x, c = (int)blockIdx.x;
@@ -227,6 +248,7 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap kmap,
         len = clamp_len(raw, most);
         if (raw != len && c == 0) raise_dev(a.hdr, DEV_PAGE_TABLE, (unsigned)u);
         sum += tiles_of<RT>(len);
+        if (K == 1 && !few) sm.lens[u] = len;
       } else if (few) {
         len = 0;
       }
@@ -266,23 +288,24 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap kmap,
       __syncthreads();
     }
   }
+  if (total == 0) return;
   const uint32_t want = (total + kMinTiles - 1) / kMinTiles;
   const uint32_t Ne = want > (uint32_t)N ? N : want;   // CTAs that take tiles
   if (c >= (int)Ne) return;
 
+  auto rows_of = [&](int u) { return K == 1 ? sm.lens[u] : clamp_len(a.lens[u], most); };
   // the window of tables that holds tile x
   auto find = [&](uint32_t x) {
     if (few) return;
-    int lo = 0, hi = kPThreads;
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) >> 1;
-      if (sm.strip[mid] * a.Hp <= x) lo = mid;
-      else hi = mid;
-    }
-    load_window<RT>(w, lo * K, sm.strip[lo] * a.Hp, a);
-    seek<RT>(w, x, a);
+    // the strip: the last one that starts at or before x, by 32nds, then among one's strips
+    constexpr int kPer = kPThreads / 32;
+    const int hi = __popc(__ballot_sync(0xffffffffu, sm.strip[lane * kPer] * a.Hp <= x)) - 1;
+    const uint32_t at = sm.strip[hi * kPer + lane % kPer] * a.Hp;
+    const int st = hi * kPer + __popc(__ballot_sync(0xffffffffu, lane < kPer && at <= x)) - 1;
+    load_window<RT>(w, st * K, sm.strip[st] * a.Hp, a, rows_of);
+    seek<RT>(w, x, a, rows_of);
   };
-  // CTA k's first tile: total k / Ne, moved to the nearer end of a short unit it falls in
+  // CTA k's first tile, moved to the nearer end of a short unit it falls in
   auto bound = [&](uint32_t k) -> uint32_t {
     const uint32_t x = total / Ne * k + total % Ne * k / Ne;
     if (x == 0 || x >= total) return x;
@@ -294,24 +317,16 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap kmap,
     if (nt > kSnapTiles) return x;
     return x - lo <= lo + nt - x ? lo : lo + nt;
   };
-  uint32_t b0, b1;
-  if (few) {
-    b0 = bound(c);
-    b1 = bound(c + 1);
-  } else {
-    if (warp < 2) {
-      const uint32_t b = bound(c + warp);
-      if (lane == 0) sm.bnd[warp] = b;
-    }
-    __syncthreads();
-    b0 = sm.bnd[0];
-    b1 = sm.bnd[1];
-  }
-  const uint32_t span = b1 - b0;
+  // the CTA that holds tile x of a unit that crosses CTAs
+  auto cta_of = [&](uint32_t x) {
+    return (int)((((uint64_t)x + 1) * Ne + total - 1) / total) - 1;
+  };
+  const uint32_t b0 = bound(c), span = bound(c + 1) - b0;
   if (span == 0) return;   // uniform in the CTA
   // (rounded up: warp 0 has the CTA's first tile)
   const uint32_t xs = b0 + (uint32_t)(((uint64_t)span * warp + kPWarps - 1) / kPWarps);
   const uint32_t xe = b0 + (uint32_t)(((uint64_t)span * (warp + 1) + kPWarps - 1) / kPWarps);
+  const int count = (int)(xe - xs);
 
   // ---- 2. this warp's tiles
   unsigned char* ring = sm.ring[warp];
@@ -321,176 +336,186 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap kmap,
   const int pieces = d * (int)sizeof(T) / 16;   // 16-byte pieces of a row
   const bool has_new = a.kn != nullptr;
   const T* qp = (const T*)a.q;
-
   Tl att;
-  float am = -INFINITY, al = 0.f, ao[NT][2];   // part a
-  int32_t unit_a = -1, unit_b = -1;
-  bool open_a = false;
-  uint32_t start_a = 0, end_a = 0, start_b = 0, end_b = 0;
-  int issued = 0, consumed = 0;   // stage uses
   bool ok = true;
-  if (xs < xe) {
-    find(xs);
-    // lane i's tile x0 + i (nothing past xe)
-    auto describe = [&](uint32_t x0) -> Desc {
-      Desc t{-1, 0, 0, 0, 0, 0, 0u, -1};
-      const uint32_t x = x0 + lane;
-      bool open = x < xe;
-      for (;;) {
-        const uint32_t wend = window_end(w);
-        // tables whose tiles end at or before x
-        int j = 0;
-#pragma unroll
-        for (int step = 16; step > 0; step >>= 1)
-          if (__shfl_sync(0xffffffffu, w.end, j + step - 1) <= x) j += step;
-        const int len = __shfl_sync(0xffffffffu, w.len, j & 31);
-        const uint32_t e = __shfl_sync(0xffffffffu, w.end, j & 31);
-        if (open && x < wend) {
-          open = false;
-          const uint32_t nt = tiles_of<RT>(len);
-          const uint32_t y = x - (e - nt * a.Hp);
-          const int h = (int)(y / nt), tt = (int)(y - h * nt);
-          const int u = w.w0 + j;
-          const int r0 = tt * RT, nv = len - r0 < RT ? len - r0 : RT;
-          const int32_t* entry = a.table + (int64_t)u * a.max_pages + (r0 >> a.shift);
-          t.unit = u * a.Hp + h;
-          t.row = h * page + (r0 & (page - 1));
-          t.tt = tt;
-          t.nt = nt;
-          t.mask = (1u << nv) - 1u;
-          if (tt == 0) t.mask |= kFirst;
-          if (tt == (int)nt - 1) t.mask |= kLast;
-          t.page = entry[0];
-          if (page < RT && nv > page) t.page2 = entry[1];
-        }
-        if (!__any_sync(0xffffffffu, open) || w.w0 + 32 >= a.U) break;
-        load_window<RT>(w, w.w0 + 32, wend, a);
-      }
-      return t;
-    };
-    // pages outside the pool: their rows do not count (page 0 is read in their place)
-    auto check_pages = [&](Desc& t) {
-      bool bad = t.page < 0 || t.page >= a.num_pages;
-      if (bad) {
-        t.page = 0;
-        t.mask &= page < RT ? ~0xFFu : ~0xFFFFu;
-      }
-      if (t.page2 < 0 || t.page2 >= a.num_pages) {
-        t.page2 = 0;
-        t.mask &= ~0xFF00u;
-        bad = true;
-      }
-      if (bad) raise_dev(a.hdr, DEV_PAGE_ID, (unsigned)t.unit);
-    };
-    // where the new row of a unit's last tile goes
-    auto look_up_slot = [&](Desc& t) {
-      if (!has_new || !(t.mask & kLast)) return;
-      const int u = t.unit / a.Hp;
-      const int64_t c0 = a.cu[u], c1 = a.cu[u + 1];
-      if (c1 > c0 && c1 > 0 && c1 <= a.slot_cap) t.slot = a.slots[c1 - 1];
-      if (t.slot < -1 || t.slot >= (a.num_pages << a.shift)) {
-        t.slot = -1;
-        raise_dev(a.hdr, DEV_PAGE_ID, (unsigned)t.unit);
-      }
-    };
-    const int count = (int)(xe - xs);
-    Desc cur = describe(xs), nxt{-1, 0, 0, 0, 0, 0, 0u, -1};
-    check_pages(cur);
-    int cur0 = 0;   // index of cur's lane 0
+  // cur holds tiles cur0..cur0 + 31, nxt the 32 behind them
+  Desc cur, nxt;
+  int cur0 = 0;
+  // loads on nxt's account that have not been looked at: its pages, and cu of the last tile's
+  // table and the next
+  int32_t p_page = 0, p_page2 = 0;
+  int64_t p_c0 = 0, p_c1 = 0;
+  bool ready = true;     // there are none
 
-    // tile i (of this warp) into the ring: the lane that knows it issues
-    auto issue = [&](int i) {
-      const int src = i - cur0;   // 0..63
-      const Desc& t = src < 32 ? cur : nxt;
-      const int s = issued % S;
-      if (lane == (src & 31)) {
-        ptx::mbar_arrive_expect_tx(&full[s], 2u * C::kHalf);
-        unsigned char* st = ring + s * 2 * C::kHalf;
+  // lane i's tile x0 + i (nothing past xe)
+  auto describe = [&](uint32_t x0) {
+    const uint32_t x = x0 + lane;
+    bool open = x < xe;
+    nxt.unit = -1;
+    nxt.mask = 0;
+    p_page = p_page2 = 0;
+    p_c0 = p_c1 = 0;
+#pragma unroll 1
+    for (;;) {
+      const uint32_t wend = window_end(w);
+      // tables whose tiles end at or before x
+      int j = 0;
 #pragma unroll
-        for (int g = 0; g < NSEG; ++g) {
-          if (page >= RT) {
-            ptx::tma_load_3d(st + g * RT * 128, &kmap, &full[s], g * kSegElems, t.row, t.page);
-            ptx::tma_load_3d(st + C::kHalf + g * RT * 128, &vmap, &full[s], g * kSegElems, t.row,
-                             t.page);
-          } else {
-            ptx::tma_load_3d(st + g * RT * 128, &kmap, &full[s], g * kSegElems, t.row, t.page);
-            ptx::tma_load_3d(st + g * RT * 128 + 1024, &kmap, &full[s], g * kSegElems, t.row,
-                             t.page2);
-            ptx::tma_load_3d(st + C::kHalf + g * RT * 128, &vmap, &full[s], g * kSegElems, t.row,
-                             t.page);
-            ptx::tma_load_3d(st + C::kHalf + g * RT * 128 + 1024, &vmap, &full[s],
-                             g * kSegElems, t.row, t.page2);
+      for (int step = 16; step > 0; step >>= 1)
+        if (__shfl_sync(0xffffffffu, w.end, j + step - 1) <= x) j += step;
+      const int len = __shfl_sync(0xffffffffu, w.len, j & 31);
+      const uint32_t e = __shfl_sync(0xffffffffu, w.end, j & 31);
+      if (open && x < wend) {
+        open = false;
+        const int u = w.w0 + j;
+        const uint32_t nt = tiles_of<RT>(len);
+        const uint32_t y = x - (e - nt * a.Hp);
+        const int h = (int)(y / nt), tt = (int)(y - h * nt);
+        const int r0 = tt * RT, nv = len - r0 < RT ? len - r0 : RT;
+        const int32_t* entry = a.table + (int64_t)u * a.max_pages + (r0 >> a.shift);
+        p_page = entry[0];
+        if (page < RT && nv > page) p_page2 = entry[1];
+        nxt.mask = ((1u << nv) - 1u) | (uint32_t)(nv - 1) << 24;
+        if (tt == 0) nxt.mask |= kFirst;
+        if (tt == (int)nt - 1) {
+          nxt.mask |= kLast;
+          if (has_new) {
+            p_c0 = a.cu[u];
+            p_c1 = a.cu[u + 1];
           }
         }
+        nxt.unit = u * a.Hp + h;
+        nxt.row = h * page + (r0 & (page - 1));
+        // the units of the warp's first and last tiles, for the merges
+        const uint32_t first = x - tt;
+        if (x == xs) sm.ends[warp][0] = make_uint2(first, first + nt);
+        if (x == xe - 1) sm.ends[warp][1] = make_uint2(first, first + nt);
       }
-      const uint32_t flags = __shfl_sync(0xffffffffu, src < 32 ? cur.mask : nxt.mask, src & 31);
-      if (has_new && (flags & kLast)) {
-        const int64_t u = __shfl_sync(0xffffffffu, src < 32 ? cur.unit : nxt.unit, src & 31);
-        for (int p = lane; p < pieces; p += 32) {
-          cp_async16(side_u + s * 2 * C::kRow + p * 16, (const T*)a.kn + u * d + p * kSegElems / 8);
-          cp_async16(side_u + s * 2 * C::kRow + C::kRow + p * 16,
-                     (const T*)a.vn + u * d + p * kSegElems / 8);
-        }
-      }
-      ++issued;
-    };
-    __syncwarp();   // the barriers are initialised
-    int next = 0;
-    for (; next < S && next < count; ++next) issue(next);
-    // (with the first copies under way)
-    look_up_slot(cur);
-    if (count > 32) {
-      nxt = describe(xs + 32);
-      check_pages(nxt);
-      look_up_slot(nxt);
+      if (!__any_sync(0xffffffffu, open) || w.w0 + 32 >= a.U) break;
+      load_window<RT>(w, w.w0 + 32, wend, a, rows_of);
     }
-
-    uint32_t qw[Tl::NQ];
-    int32_t q_unit = -1;   // unit whose q words qw holds
-    bool whole = false;    // the warp has the unit from its first tile on
-    for (int i = 0; i < count; ++i) {
-      if (i - cur0 == 32) {
-        cur = nxt;
-        cur0 += 32;
-        if (count - cur0 > 32) {
-          nxt = describe(xs + cur0 + 32);
-          check_pages(nxt);
-          look_up_slot(nxt);
+    ready = false;
+  };
+  // What describe() asked for, once it is there.  Pages outside the pool: their rows do not
+  // count (page 0 is read in their place).  The slot of a unit's new row is only asked for here.
+  auto settle = [&]() {
+    if (ready) return;
+    ready = true;
+    const bool bad = p_page < 0 || p_page >= a.num_pages;
+    const bool bad2 = p_page2 < 0 || p_page2 >= a.num_pages;
+    nxt.page = bad ? 0 : p_page;
+    nxt.page2 = bad2 ? 0 : p_page2;
+    if (bad) nxt.mask &= page < RT ? ~0xFFu : ~0xFFFFu;
+    if (bad2) nxt.mask &= ~0xFF00u;
+    if (bad || bad2) raise_dev(a.hdr, DEV_PAGE_ID, (unsigned)nxt.unit);
+    nxt.slot = -1;
+    if (p_c1 > p_c0 && p_c1 > 0 && p_c1 <= a.slot_cap) nxt.slot = a.slots[p_c1 - 1];
+  };
+  // lane src's tile of t into stage s: that lane issues it
+  auto issue = [&](const Desc& t, int src, int s) {
+    if (lane == src) {
+      ptx::mbar_arrive_expect_tx(&full[s], 2u * C::kHalf);
+      unsigned char* st = ring + s * 2 * C::kHalf;
+#pragma unroll
+      for (int g = 0; g < NSEG; ++g) {
+        ptx::tma_load_3d(st + g * RT * 128, &kmap, &full[s], g * kSegElems, t.row, t.page);
+        ptx::tma_load_3d(st + C::kHalf + g * RT * 128, &vmap, &full[s], g * kSegElems, t.row,
+                         t.page);
+        if (page < RT) {
+          ptx::tma_load_3d(st + g * RT * 128 + 1024, &kmap, &full[s], g * kSegElems, t.row,
+                           t.page2);
+          ptx::tma_load_3d(st + C::kHalf + g * RT * 128 + 1024, &vmap, &full[s], g * kSegElems,
+                           t.row, t.page2);
         }
       }
-      const int src = i - cur0;
-      uint32_t mask = __shfl_sync(0xffffffffu, cur.mask, src);
+    }
+    if (has_new && (__shfl_sync(0xffffffffu, t.mask, src) & kLast)) {
+      const int64_t u = __shfl_sync(0xffffffffu, t.unit, src);
+      for (int p = lane; p < pieces; p += 32) {
+        cp_async16(side_u + s * 2 * C::kRow + p * 16, (const T*)a.kn + u * d + p * kSegElems / 8);
+        cp_async16(side_u + s * 2 * C::kRow + C::kRow + p * 16,
+                   (const T*)a.vn + u * d + p * kSegElems / 8);
+      }
+    }
+  };
+  __syncwarp();   // the barriers are initialised
+  int32_t unit_a = -1, unit_b = -1;
+  bool open_a = false, far = false;
+  if (count > 0) {
+    find(xs);
+    describe(xs);
+    settle();
+    cur = nxt;
+    for (int i = 0; i < S && i < count; ++i) issue(cur, i, i);
+  }
+  if (count > 32) describe(xs + 32);
+  uint32_t qw[Tl::NQ];
+  int32_t q_unit = -1;   // unit whose q words qw holds
+  bool whole = false;    // the warp has the unit from its first tile on
+  int s = 0;             // stage of tile i
+  uint32_t phase = 0;    // of its barrier
+  uint32_t firsts = 0, lasts = 0, cuts = 0;   // cur's tiles: units' first, last; not all rows
+  for (int i = 0; i < count; ++i) {
+    if (i - cur0 == 32) {
+      settle();
+      cur = nxt;
+      cur0 += 32;
+      if (count - cur0 > 32) describe(xs + cur0 + 32);
+    }
+    const int src = i - cur0;
+    if (src == 0) {
+      firsts = __ballot_sync(0xffffffffu, cur.mask & kFirst);
+      lasts = __ballot_sync(0xffffffffu, cur.mask & kLast);
+      cuts = __ballot_sync(0xffffffffu, (cur.mask & ((1u << RT) - 1u)) != (1u << RT) - 1u);
+    }
+    const bool last = lasts >> src & 1;
+    if (i == 0 || (firsts >> src & 1)) {
       const int32_t unit = __shfl_sync(0xffffffffu, cur.unit, src);
-      if (i == 0 || (mask & kFirst)) {
-        if (q_unit != unit) Tl::load_q(qp + (int64_t)unit * G * d, G, d, qw);
-        att.set_q(qw);
-        att.begin();
-        whole = (mask & kFirst) != 0;
-        // the next unit's q, while this one streams
-        q_unit = -1;
-        if (unit + 1 < a.U * a.Hp && i + 1 < count) {
-          q_unit = unit + 1;
-          Tl::load_q(qp + (int64_t)q_unit * G * d, G, d, qw);
-        }
+      if (q_unit != unit) Tl::load_q(qp + (int64_t)unit * G * d, G, d, qw);
+      att.set_q(qw, a.scale);
+      att.begin();
+      whole = firsts >> src & 1;
+      // the next unit's q, while this one streams
+      q_unit = -1;
+      if (unit + 1 < a.U * a.Hp && i + 1 < count) {
+        q_unit = unit + 1;
+        Tl::load_q(qp + (int64_t)q_unit * G * d, G, d, qw);
       }
-      const int s = consumed % S;
-      if (ok) {
-        const bool landed = ptx::mbar_wait(&full[s], (uint32_t)((consumed / S) & 1));
-        if (__any_sync(0xffffffffu, !landed)) {
-          ok = false;
-          if (lane == 0) raise_dev(a.hdr, DEV_WAIT_TIMEOUT, 0x800u + (unsigned)s);
+    }
+    if (ok) {
+      const bool landed = ptx::mbar_wait(&full[s], phase);
+      if (__any_sync(0xffffffffu, !landed)) {
+        ok = false;
+        if (lane == 0) {
+          raise_dev(a.hdr, DEV_WAIT_TIMEOUT, 0x800u + (unsigned)s);
+          // a wait gave up: let what is in flight land before the memory is reused
+          int t = s;
+          uint32_t ph = phase;
+          for (int k = i; k < count && k < i + S; ++k) {
+            (void)ptx::mbar_wait(&full[t], ph, 20000000ull);
+            if (++t == S) t = 0, ph ^= 1;
+          }
         }
+        __syncwarp();
       }
-      if (ok) {
-        const uint32_t ks = ring_u + s * 2 * C::kHalf, vs = ks + C::kHalf;
-        if (has_new && (mask & kLast)) {
+    }
+    if (ok) {
+      const uint32_t ks = ring_u + s * 2 * C::kHalf, vs = ks + C::kHalf;
+      uint32_t mask = (1u << RT) - 1u;
+      if ((cuts >> src & 1) || (has_new && last)) {
+        mask = __shfl_sync(0xffffffffu, cur.mask, src);
+        const int r = mask >> 24 & 15;   // the unit's last row, if this is its last tile
+        mask &= (1u << RT) - 1u;
+        unsigned char* st = ring + s * 2 * C::kHalf;
+        if (has_new && last) {
           const int64_t slot = __shfl_sync(0xffffffffu, (long long)cur.slot, src);
+          const int32_t unit = __shfl_sync(0xffffffffu, cur.unit, src);
+          const bool in_pool = slot >= 0 && slot < (a.num_pages << a.shift);
+          if (slot != -1 && !in_pool && lane == 0) raise_dev(a.hdr, DEV_PAGE_ID, (unsigned)unit);
           cp_async_wait_all();
           __syncwarp();
-          if (slot >= 0) {
-            // to its place in the tile, the unit's last row, and to its slot
-            const int u = unit / a.Hp;
-            const int r = (clamp_len(a.lens[u], most) - 1) & (RT - 1);
+          if (in_pool) {
+            // the new row, to its place in the tile and to its slot
             mask |= 1u << r;
             const int64_t at = (slot >> a.shift) * a.page_stride +
                                (((int64_t)(unit % a.Hp) << a.shift) + (slot & (page - 1))) * d;
@@ -498,133 +523,122 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap kmap,
               const uint4 kx = *reinterpret_cast<const uint4*>(side + s * 2 * C::kRow + p * 16);
               const uint4 vx =
                   *reinterpret_cast<const uint4*>(side + s * 2 * C::kRow + C::kRow + p * 16);
-              unsigned char* st = ring + s * 2 * C::kHalf + pmma::piece<RT>(r, p);
-              *reinterpret_cast<uint4*>(st) = kx;
-              *reinterpret_cast<uint4*>(st + C::kHalf) = vx;
+              *reinterpret_cast<uint4*>(st + pmma::piece<RT>(r, p)) = kx;
+              *reinterpret_cast<uint4*>(st + C::kHalf + pmma::piece<RT>(r, p)) = vx;
               *reinterpret_cast<uint4*>((T*)a.kp + at + p * (16 / (int)sizeof(T))) = kx;
               *reinterpret_cast<uint4*>((T*)a.vp + at + p * (16 / (int)sizeof(T))) = vx;
             }
-            ptx::fence_proxy_async_smem();   // before the stage is refilled
-            __syncwarp();
           }
         }
-        att.tile(ks, vs, mask & 0xFFFFu, a.c2);
-        __syncwarp();   // every lane is done with stage s
-        ++consumed;
-        if (next < count) {
-          issue(next);
-          ++next;
-        }
+        pmma::clear_rows<RT>(st + C::kHalf, mask, NSEG);
+        ptx::fence_proxy_async_smem();   // before the stage is refilled
+        __syncwarp();
       }
-      // ---- the end of a unit, or of the warp's tiles
-      if ((mask & kLast) || i == count - 1) {
-        att.finish();
-        const uint32_t start = xs + i - __shfl_sync(0xffffffffu, cur.tt, src);
-        const uint32_t end = start + __shfl_sync(0xffffffffu, cur.nt, src);
-        if (whole && (mask & kLast)) {
-          const int g = lane >> 2, col = 2 * (lane & 3);
-          if (g < G) {
-            const float inv = att.l > 0.f ? 1.f / att.l : 0.f;
-            T* dst = (T*)a.out + ((int64_t)unit * G + g) * d + col;
-#pragma unroll
-            for (int t = 0; t < NT; ++t)
-              if (8 * t < d) store2(dst + 8 * t, att.o[t][0] * inv, att.o[t][1] * inv);
-          }
-        } else if (!whole) {
-          am = att.m;
-          al = att.l;
-#pragma unroll
-          for (int t = 0; t < NT; ++t) {
-            ao[t][0] = att.o[t][0];
-            ao[t][1] = att.o[t][1];
-          }
-          unit_a = unit;
-          open_a = (mask & kLast) == 0;
-          start_a = start;
-          end_a = end;
-        } else {
-          unit_b = unit;
-          start_b = start;
-          end_b = end;
-        }
+      att.tile(ks, vs, mask, a.scale.c2);
+      __syncwarp();   // every lane is done with stage s
+      const int n = src + S;
+      if (i + S < count) {
+        if (n >= 32) settle();
+        issue(n < 32 ? cur : nxt, n & 31, s);
       }
     }
-    if (!ok && lane == 0)   // a wait gave up: let what is in flight land before the memory is reused
-      for (int i = consumed; i < issued; ++i)
-        (void)ptx::mbar_wait(&full[i % S], (uint32_t)((i / S) & 1), 20000000ull);
+    // ---- the end of a unit, or of the warp's tiles
+    if (last || i == count - 1) {
+      const int32_t unit = __shfl_sync(0xffffffffu, cur.unit, src);
+      att.finish(a.scale.c2);
+      const int g = lane >> 2, col = 2 * (lane & 3);
+      if (whole && last) {
+        if (g < G) {
+          const float inv = att.l > 0.f ? 1.f / att.l : 0.f;
+          T* dst = (T*)a.out + ((int64_t)unit * G + g) * d + col;
+#pragma unroll
+          for (int t = 0; t < NT; ++t)
+            if (8 * t < d) store2(dst + 8 * t, att.o[t][0] * inv, att.o[t][1] * inv);
+        }
+      } else {
+        // A part of the unit.  Its place is the stage that the warp reads last; a part a that
+        // ends before the warp's tiles do waits in the workspace.
+        if (whole) {
+          unit_b = unit;
+        } else {
+          unit_a = unit;
+          open_a = !last;
+          far = i < count - 1;
+        }
+        if (col == 0) {
+          sm.ml[warp][whole][g] = att.m;
+          sm.ml[warp][whole][8 + g] = att.l;
+        }
+        float* dst = far && !whole
+            ? a.far + (int64_t)(c * kPWarps + warp) * 8 * 128
+            : reinterpret_cast<float*>(ring + s * 2 * C::kHalf) + (whole ? 8 * D : 0);
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+          *reinterpret_cast<float2*>(dst + g * D + 8 * t + col) =
+              make_float2(att.o[t][0], att.o[t][1]);
+      }
+    }
+    if (i < count - 1 && ++s == S) s = 0, phase ^= 1;
   }
+
+  // ---- 3. what the warps leave
   if (lane == 0) {
+    sm.at[warp] = s * 2 * C::kHalf;
+    sm.far[warp] = far ? 1 : 0;
     sm.a_unit[warp] = unit_a;
     sm.a_open[warp] = open_a ? 1 : 0;
     sm.b_unit[warp] = unit_b;
-    sm.some[warp] = xs < xe ? 1 : 0;
-    sm.start[1 + warp] = start_b;
-    sm.end[1 + warp] = end_b;
-    if (warp == 0) {
-      sm.start[0] = start_a;
-      sm.end[0] = end_a;
-    }
-  }
-  __syncthreads();   // every ring is idle: its memory holds the parts now
-
-  // ---- 3. merges
-  float* wp = reinterpret_cast<float*>(&sm.ring[0][0]);   // part a of warp w: 2 w, part b: 2 w + 1
-  const int g4 = lane >> 2, c4 = lane & 3;
-  if (unit_a >= 0) {
-    float* P = wp + (2 * warp) * kPartFloats;
-    if (c4 == 0) {
-      P[g4] = am;
-      P[8 + g4] = al;
-    }
-#pragma unroll
-    for (int t = 0; t < NT; ++t)
-      *reinterpret_cast<float2*>(P + kPartHead + g4 * D + 8 * t + 2 * c4) =
-          make_float2(ao[t][0], ao[t][1]);
-  }
-  if (unit_b >= 0) {
-    float* P = wp + (2 * warp + 1) * kPartFloats;
-    if (c4 == 0) {
-      P[g4] = att.m;
-      P[8 + g4] = att.l;
-    }
-#pragma unroll
-    for (int t = 0; t < NT; ++t)
-      *reinterpret_cast<float2*>(P + kPartHead + g4 * D + 8 * t + 2 * c4) =
-          make_float2(att.o[t][0], att.o[t][1]);
+    sm.some[warp] = count > 0 ? 1 : 0;
   }
   __syncthreads();
-  const int nsl = G * (D / 4);   // 16-byte slices of a part's output
-  int cross_a = -1, cross_b = -1;   // units that began before this CTA / go on after it: the
-                                    // candidate (0: warp 0's part a, 1 + w: warp w's part b)
-  for (int cand = 0; cand <= kPWarps; ++cand) {
-    const int32_t unit = cand == 0 ? sm.a_unit[0] : sm.b_unit[cand - 1];
-    if (unit < 0) continue;
-    const int first = cand == 0 ? 0 : 2 * cand - 1;
-    uint32_t members = 0;   // warps whose part a goes on with the unit
-    bool open = cand == 0 ? sm.a_open[0] != 0 : true;
-    for (int k = cand == 0 ? 1 : cand; k < kPWarps && open; ++k) {
-      if (!sm.some[k]) continue;
-      if (sm.a_unit[k] != unit) break;
-      members |= 1u << k;
-      open = sm.a_open[k] != 0;
-    }
-    const bool crosses = cand == 0 || open;
-    if (cand == 0) cross_a = 0;
-    else if (open) cross_b = cand;
+  // Heads: lane 0 stands for the unit of warp 0's part a, lane i > 0 for that of warp
+  // i - 1's part b.  A head's unit goes on in the parts a of the warps from `from` on, up to
+  // the first warp with tiles whose part a (if any) ends there; if there is none it crosses
+  // the CTA's end.
+  int32_t unit = -1;
+  uint32_t part_a, stops;
+  {
+    const bool in = lane < kPWarps;
+    const int32_t ua = in ? sm.a_unit[lane] : -1, ub = in ? sm.b_unit[lane] : -1;
+    part_a = __ballot_sync(0xffffffffu, ua >= 0);
+    stops = __ballot_sync(0xffffffffu, in && sm.some[lane] && !sm.a_open[lane]);
+    const int32_t before = __shfl_up_sync(0xffffffffu, ub, 1);
+    unit = lane == 0 ? ua : lane <= kPWarps ? before : -1;
+  }
+  const uint32_t from = ~0u << (lane == 0 ? 1 : lane & 15), stop = stops & from;
+  uint32_t members = part_a & from & (stop ? (stop ^ (stop - 1)) : ~0u);
+  if (lane == 0 && (stops & 1)) members = 0;
+  const uint32_t heads = __ballot_sync(0xffffffffu, unit >= 0);
+  const uint32_t cross = __ballot_sync(0xffffffffu, unit >= 0 && (lane == 0 || stop == 0));
+
+  const int nsl = G * (D / 4);   // 4-float slices of a part's output
+  for (uint32_t todo = heads; todo; todo &= todo - 1) {
+    const int i = __ffs(todo) - 1;
+    const int32_t un = __shfl_sync(0xffffffffu, unit, i);
+    uint32_t mem = __shfl_sync(0xffffffffu, members, i);
     for (int idx = tid; idx < nsl; idx += kPThreads) {
       const int g = idx / (D / 4), col = (idx - g * (D / 4)) * 4;
-      const float* P = wp + first * kPartFloats;
+      float m[kPWarps], l[kPWarps];
+      float4 o[kPWarps];
+#pragma unroll
+      for (int k = 0; k < kPWarps; ++k) {
+        // warp k's part: b where the unit begins with it, else a
+        const bool b = i == k + 1, in = b || (mem >> k & 1) || (i == 0 && k == 0);
+        m[k] = in ? sm.ml[k][b][g] : -INFINITY;
+        l[k] = in ? sm.ml[k][b][8 + g] : 0.f;
+        o[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (in && !b && sm.far[k])
+          o[k] = __ldcg(reinterpret_cast<const float4*>(
+              a.far + (int64_t)(c * kPWarps + k) * 8 * 128 + g * D + col));
+        else if (in)
+          o[k] = *reinterpret_cast<const float4*>(sm.ring[k] + sm.at[k] +
+                                                  ((b ? 8 * D : 0) + g * D + col) * 4);
+      }
       float M = -INFINITY, L = 0.f;
       float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-      merge_part(P[g], P[8 + g], *reinterpret_cast<const float4*>(P + kPartHead + g * D + col), M,
-                 L, acc);
-      for (uint32_t m = members; m; m &= m - 1) {
-        P = wp + 2 * (__ffs(m) - 1) * kPartFloats;
-        merge_part(P[g], P[8 + g], *reinterpret_cast<const float4*>(P + kPartHead + g * D + col),
-                   M, L, acc);
-      }
-      if (crosses) {
-        float* Q = a.part + (int64_t)(cand == 0 ? 2 * c : 2 * c + 1) * kPartFloats;
+      merge_parts<kPWarps>(m, l, o, M, L, acc);
+      if (cross >> i & 1) {
+        float* Q = a.part + (int64_t)(2 * c + (i == 0 ? 0 : 1)) * kPartFloats;
         if (col == 0) {
           Q[g] = M;
           Q[8 + g] = L;
@@ -632,66 +646,90 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap kmap,
         *reinterpret_cast<float4*>(Q + kPartHead + g * D + col) = acc;
       } else if (col < d) {
         const float inv = L > 0.f ? 1.f / L : 0.f;
-        store4((T*)a.out + ((int64_t)unit * G + g) * d + col,
+        store4((T*)a.out + ((int64_t)un * G + g) * d + col,
                make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv));
       }
     }
   }
-  if (cross_a < 0 && cross_b < 0) return;   // uniform in the CTA
 
-  // units that cross CTAs: the CTA that holds tile x, and the last of a unit's CTAs merges
-  auto cta_of = [&](uint32_t x) {
-    return (int)((((uint64_t)x + 1) * Ne + total - 1) / total) - 1;
-  };
-  __threadfence();
-  __syncthreads();
-  if (tid < 2) {
-    const int cand = tid == 0 ? cross_a : cross_b;
-    int won = -1;
-    if (cand >= 0) {
-      const int ca = cta_of(sm.start[cand]), cb = cta_of(sm.end[cand] - 1);
-      const uint32_t old = atomicAdd(&a.tick[ca], 1u);
-      if (old == (uint32_t)(cb - ca)) {
-        atomicExch(&a.tick[ca], 0u);
-        won = cand;
-      }
+  if (cross == 0) return;   // uniform in the CTA
+
+  // units that cross CTAs (at most the one that began before this CTA and the one that goes on
+  // after it): the last of a unit's CTAs to get here merges its parts
+  const int i1 = 31 - __clz((int)cross);   // the second's head, if it is not 0
+  const int32_t units[2] = {cross & 1 ? __shfl_sync(0xffffffffu, unit, 0) : -1,
+                            i1 > 0 ? __shfl_sync(0xffffffffu, unit, i1) : -1};
+  int first[2], parts[2];
+#pragma unroll
+  for (int y = 0; y < 2; ++y) {
+    const uint2 ends = y == 0 ? sm.ends[0][0] : sm.ends[i1 > 0 ? i1 - 1 : 0][1];
+    first[y] = units[y] >= 0 ? cta_of(ends.x) : 0;
+    parts[y] = units[y] >= 0 ? cta_of(ends.y - 1) - first[y] + 1 : 0;
+  }
+  __syncthreads();   // the CTA's parts are written
+  if (tid == 0) {
+    __threadfence();
+    uint32_t drawn[2] = {0, 0};
+#pragma unroll
+    for (int y = 0; y < 2; ++y)
+      if (units[y] >= 0) drawn[y] = atomicAdd(&a.tick[first[y]], 1u);
+#pragma unroll
+    for (int y = 0; y < 2; ++y) {
+      sm.won[y] = units[y] >= 0 && drawn[y] == (uint32_t)parts[y] - 1;
+      if (sm.won[y]) atomicExch(&a.tick[first[y]], 0u);
     }
-    sm.win[tid] = won;
+    __threadfence();
   }
   __syncthreads();
-  __threadfence();
+  // groups of threads take the parts in turn, and their sums are added in order
+  const int groups = nsl < kPThreads ? kPThreads / nsl : 1;
+#pragma unroll 1
   for (int y = 0; y < 2; ++y) {
-    const int cand = sm.win[y];
-    if (cand < 0) continue;
-    const int32_t unit = cand == 0 ? sm.a_unit[0] : sm.b_unit[cand - 1];
-    const int ca = cta_of(sm.start[cand]), cb = cta_of(sm.end[cand] - 1);
-    for (int idx = tid; idx < nsl; idx += kPThreads) {
+    if (!sm.won[y]) continue;
+#pragma unroll 1
+    for (int sl = 0; sl < nsl; sl += kPThreads) {
+      const int grp = nsl < kPThreads ? tid / nsl : 0, idx = sl + tid - grp * nsl;
       const int g = idx / (D / 4), col = (idx - g * (D / 4)) * 4;
+      const bool in_part = grp < groups && idx < nsl;
       float M = -INFINITY, L = 0.f;
       float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
       constexpr int kB = 8;   // parts per round of loads
-      for (int c0 = ca; c0 <= cb; c0 += kB) {
+#pragma unroll 1
+      for (int k0 = grp; in_part && k0 < parts[y]; k0 += kB * groups) {
         float m[kB], l[kB];
         float4 o[kB];
 #pragma unroll
         for (int b = 0; b < kB; ++b) {
-          m[b] = -INFINITY;
-          l[b] = 0.f;
-          o[b] = make_float4(0.f, 0.f, 0.f, 0.f);
-          if (c0 + b <= cb) {
-            const int k = c0 + b;
-            const float* P = a.part + (int64_t)(k == ca ? 2 * k + 1 : 2 * k) * kPartFloats;
-            m[b] = __ldcg(P + g);
-            l[b] = __ldcg(P + 8 + g);
-            o[b] = __ldcg(reinterpret_cast<const float4*>(P + kPartHead + g * D + col));
-          }
+          const int k = k0 + b * groups;
+          // (the unit is the second of its first CTA)
+          const float* P = a.part + (int64_t)(2 * (first[y] + k) + (k == 0 ? 1 : 0)) * kPartFloats;
+          const bool in = k < parts[y];
+          m[b] = in ? __ldcg(P + g) : -INFINITY;
+          l[b] = in ? __ldcg(P + 8 + g) : 0.f;
+          o[b] = in ? __ldcg(reinterpret_cast<const float4*>(P + kPartHead + g * D + col))
+                    : make_float4(0.f, 0.f, 0.f, 0.f);
         }
-#pragma unroll
-        for (int b = 0; b < kB; ++b) merge_part(m[b], l[b], o[b], M, L, acc);
+        merge_parts<kB>(m, l, o, M, L, acc);
       }
-      if (col < d) {
+      if (groups > 1) {
+        // (in the stage that held the warp's parts)
+        float* mine = reinterpret_cast<float*>(ring + sm.at[warp]) + lane * 8;
+        *reinterpret_cast<float4*>(mine) = acc;
+        *reinterpret_cast<float2*>(mine + 4) = make_float2(M, L);
+        __syncthreads();
+        for (int k = 1; grp == 0 && k < groups; ++k) {
+          const int t = tid + k * nsl;
+          const float* p = reinterpret_cast<const float*>(sm.ring[t >> 5] + sm.at[t >> 5]) +
+                           (t & 31) * 8;
+          const float m[1] = {p[4]}, l[1] = {p[5]};
+          const float4 o[1] = {*reinterpret_cast<const float4*>(p)};
+          merge_parts<1>(m, l, o, M, L, acc);
+        }
+        __syncthreads();
+      }
+      if (in_part && grp == 0 && col < d) {
         const float inv = L > 0.f ? 1.f / L : 0.f;
-        store4((T*)a.out + ((int64_t)unit * G + g) * d + col,
+        store4((T*)a.out + ((int64_t)units[y] * G + g) * d + col,
                make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv));
       }
     }
@@ -732,14 +770,14 @@ bool pool_map(CUtensorMap* map, const void* base, const PagedShape& s, int rows)
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-constexpr size_t kTickBytes = 1024;
+constexpr size_t kTickBytes = 2048;
 static_assert(kMaxCtas * sizeof(uint32_t) <= kTickBytes, "tickets");
 
 template <typename T, int NSEG>
 cudaError_t launch_t(const PagedShape& s, const PagedArgs& a, cudaStream_t st) {
   using C = Cfg<T, NSEG>;
-  constexpr size_t smem = sizeof(PagedSmem) + 1024;
-  static_assert(smem <= 227 * 1024, "one CTA per SM");
+  constexpr size_t smem = sizeof(PagedSmem<C>) + 1024;
+  static_assert(kCtasPerSm * (smem + 1024) <= 228 * 1024, "CTAs per SM");
   static std::atomic<int> slot[kMaxDevices];
   const int ok = per_device(slot, []() {
     return cudaFuncSetAttribute(paged_decode_kernel<T, NSEG>,
@@ -754,7 +792,7 @@ cudaError_t launch_t(const PagedShape& s, const PagedArgs& a, cudaStream_t st) {
   // no more CTAs than the tables could ever fill
   const int64_t tiles = (int64_t)s.seqs * s.Hkv * cdiv((int64_t)s.max_pages * s.page, C::RT);
   int64_t grid = cdiv(tiles, kMinTiles);
-  if (grid > num_sms()) grid = num_sms();
+  if (grid > kCtasPerSm * num_sms()) grid = kCtasPerSm * num_sms();
   if (grid > kMaxCtas) grid = kMaxCtas;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3((unsigned)grid);
@@ -771,7 +809,8 @@ cudaError_t launch_t(const PagedShape& s, const PagedArgs& a, cudaStream_t st) {
 }  // namespace
 
 size_t paged_decode_ws_bytes(const PagedShape&) {
-  return kWsHeader + kTickBytes + (size_t)2 * kMaxCtas * kPartFloats * sizeof(float);
+  return kWsHeader + kTickBytes + (size_t)2 * kMaxCtas * kPartFloats * sizeof(float) +
+         (size_t)kMaxCtas * kPWarps * 8 * 128 * sizeof(float);
 }
 
 cudaError_t launch_paged_decode(const PagedShape& s, const void* q, const void* kn, const void* vn,
@@ -780,11 +819,16 @@ cudaError_t launch_paged_decode(const PagedShape& s, const void* q, const void* 
                                 float scale, void* out, char* ws, cudaStream_t st) {
   int shift = 0;
   while ((1 << shift) < s.page) ++shift;
+  const float c2 = fabsf(scale) * 1.4426950408889634f;   // times log2 e
+  const uint32_t flip = scale >= 0.f ? 0u : s.dtype == KV_BF16 ? 0x80008000u : 0x80000000u;
   const PagedArgs a{q, kn, vn, cu, slots, slot_capacity, kp, vp, table, lens, out,
                     reinterpret_cast<WsHeader*>(ws), reinterpret_cast<uint32_t*>(ws + kWsHeader),
-                    reinterpret_cast<float*>(ws + kWsHeader + kTickBytes), (int)s.U(), s.Hp(),
+                    reinterpret_cast<float*>(ws + kWsHeader + kTickBytes),
+                    reinterpret_cast<float*>(ws + kWsHeader + kTickBytes) +
+                        (size_t)2 * kMaxCtas * kPartFloats,
+                    (int)s.U(), s.Hp(),
                     s.G(), s.d, shift, s.max_pages, s.num_pages, s.page_stride,
-                    scale * 1.4426950408889634f};
+                    pmma::Scale{c2 > FLT_MIN ? c2 : FLT_MIN, flip}};
   if (s.dtype == KV_BF16)
     return s.d <= 64 ? launch_t<__nv_bfloat16, 1>(s, a, st) : launch_t<__nv_bfloat16, 2>(s, a, st);
   switch ((s.d + 31) / 32) {

@@ -1,6 +1,6 @@
 // One warp's online softmax over tiles of K and V rows in shared memory, on the warp matrix
 // instructions, for up to 8 query rows:  (m, l, o) := running maximum, sum and output of
-//   p_r = exp2(c2 q . k_r - m),  l = sum p_r,  o = sum p_r v_r.
+//   p_r = exp2(c2 (q . k_r - m)),  l = sum p_r,  o = sum p_r v_r,   c2 > 0.
 //
 // A tile is RT rows, K then V, each as NSEG segments of [RT][128 bytes] with the 16-byte
 // pieces of row r permuted by r & 7 (TMA's 128-byte swizzle): every access below touches 8
@@ -18,6 +18,10 @@
 // operand of the second product the same lane holds the same rows (for tf32, whose lane holds
 // columns c and c + 4, the rows of each 8 are taken in the order 0, 2, 4, 6, 1, 3, 5, 7), so p
 // never leaves its lane.
+//
+// The scale is no factor of its own: p = exp2(fma(s, c2, -m c2)).  A negative scale is taken
+// into q's sign, and a zero one is the smallest positive number, so that masked scores (-inf)
+// give zeros (Scale).
 #pragma once
 
 #include "kv_internal.cuh"
@@ -83,6 +87,19 @@ __device__ __forceinline__ uint32_t piece(int r, int c) {
   return (uint32_t)((c >> 3) * (RT * 128) + r * 128 + (((c ^ r) & 7) << 4));
 }
 
+struct Scale {
+  float c2;        // > 0
+  uint32_t flip;   // sign bits of q to flip (bf16: of both halves)
+};
+
+// Rows of a tile's V that do not count may hold anything, and 0 * NaN is NaN: zeros instead.
+// (Before tile(), when `mask` is not all ones; all lanes, with a __syncwarp behind it.)
+template <int RT>
+__device__ __forceinline__ void clear_rows(unsigned char* v, uint32_t mask, int nseg) {
+  for (int i = threadIdx.x & 31; i < nseg * RT * 8; i += 32)
+    if (!(mask >> (i / 8 % RT) & 1)) reinterpret_cast<uint4*>(v)[i] = make_uint4(0u, 0u, 0u, 0u);
+}
+
 template <typename T, int NSEG>
 struct Tile;
 
@@ -101,12 +118,12 @@ struct State {
       for (int e = 0; e < 4; ++e) o[t][e] = 0.f;
   }
   // New maximum of this lane's query from the tile's scores; o and l follow.
-  __device__ __forceinline__ void raise(float mt) {
+  __device__ __forceinline__ void raise(float mt, float c2) {
     mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, 1));
     mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, 2));
     if (__any_sync(0xffffffffu, mt > m)) {
       const float mn = fmaxf(m, mt);
-      const float a = mn > m ? ptx::ex2(m - mn) : 1.f;   // 0 while m is -inf
+      const float a = mn > m ? ptx::ex2((m - mn) * c2) : 1.f;   // 0 while m is -inf
       m = mn;
       l *= a;
 #pragma unroll
@@ -115,9 +132,10 @@ struct State {
         for (int e = 0; e < 4; ++e) o[t][e] *= a;
     }
   }
-  __device__ __forceinline__ float base() const { return m == -INFINITY ? 0.f : m; }
-  // After the last tile: l whole in every lane of the query, o in [0..1].
-  __device__ __forceinline__ void finish() {
+  __device__ __forceinline__ float base(float c2) const { return m == -INFINITY ? 0.f : -m * c2; }
+  // After the last tile: m in units of log2, l whole in every lane of the query, o in [0..1].
+  __device__ __forceinline__ void finish(float c2) {
+    m *= c2;
     l += __shfl_xor_sync(0xffffffffu, l, 1);
     l += __shfl_xor_sync(0xffffffffu, l, 2);
 #pragma unroll
@@ -146,66 +164,61 @@ struct Tile<__nv_bfloat16, NSEG> : State<NSEG * 8> {
       w[i] = g < G && x < d ? *reinterpret_cast<const uint32_t*>(src + g * d + x) : 0u;
     }
   }
-  __device__ __forceinline__ void set_q(const uint32_t (&w)[NQ]) {
+  __device__ __forceinline__ void set_q(const uint32_t (&w)[NQ], const Scale& sc) {
 #pragma unroll
-    for (int i = 0; i < NQ; ++i) q[i] = w[i];
+    for (int i = 0; i < NQ; ++i) q[i] = w[i] ^ sc.flip;
   }
 
-  // One tile at shared addresses ks, vs; bit r of `mask`: row r counts.
+  // One tile at shared addresses ks, vs (1024-byte aligned); bit r of `mask`: row r counts.
+  // A piece's address is its row's with piece bits under xor (r & 7) * 16, so the pieces of a
+  // lane's row are one address xor a constant.
   __device__ __forceinline__ void tile(uint32_t ks, uint32_t vs, uint32_t mask, float c2) {
     const int lane = threadIdx.x & 31, c = lane & 3;
-    float s[2][4];
+    // scores: two sums per 8 rows (even and odd k-steps), short chains
+    float s[2][2][4];
 #pragma unroll
     for (int j = 0; j < 2; ++j)
 #pragma unroll
-      for (int e = 0; e < 4; ++e) s[j][e] = 0.f;
+      for (int e = 0; e < 4; ++e) s[j][0][e] = s[j][1][e] = 0.f;
+    const uint32_t ka = ks + (lane & 7) * 128 + (((lane >> 3) ^ (lane & 7)) << 4);
 #pragma unroll
     for (int kk = 0; kk < 2 * NSEG; ++kk) {
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
         uint32_t b[4];
-        ldsm4(b, ks + piece<RT>(8 * j + (lane & 7), 4 * kk + (lane >> 3)));
-        mma_bf16_16816(s[j], q[4 * kk], 0u, q[4 * kk + 1], 0u, b[0], b[1]);
-        mma_bf16_16816(s[j], q[4 * kk + 2], 0u, q[4 * kk + 3], 0u, b[2], b[3]);
+        ldsm4(b, (ka ^ ((kk & 1) * 64)) + (kk >> 1) * (RT * 128) + j * 1024);
+        mma_bf16_16816(s[j][0], q[4 * kk], 0u, q[4 * kk + 1], 0u, b[0], b[1]);
+        mma_bf16_16816(s[j][1], q[4 * kk + 2], 0u, q[4 * kk + 3], 0u, b[2], b[3]);
       }
     }
-    float z[2][2], mt = -INFINITY;
+    float z[2][2];
 #pragma unroll
     for (int j = 0; j < 2; ++j)
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        z[j][e] = mask >> (8 * j + 2 * c + e) & 1 ? s[j][e] * c2 : -INFINITY;
-        mt = fmaxf(mt, z[j][e]);
-      }
-    this->raise(mt);
-    const float base = this->base();
+      for (int e = 0; e < 2; ++e) z[j][e] = s[j][0][e] + s[j][1][e];
+    if (mask != 0xFFFFu) {
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+          if (!(mask >> (8 * j + 2 * c + e) & 1)) z[j][e] = -INFINITY;
+    }
+    this->raise(fmaxf(fmaxf(z[0][0], z[0][1]), fmaxf(z[1][0], z[1][1])), c2);
+    const float base = this->base(c2);
     uint32_t hi[2], lo[2];
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
-      const float p0 = ptx::ex2(z[j][0] - base), p1 = ptx::ex2(z[j][1] - base);
+      const float p0 = ptx::ex2(fmaf(z[j][0], c2, base)), p1 = ptx::ex2(fmaf(z[j][1], c2, base));
       this->l += p0 + p1;
       hi[j] = bf16x2_of(p0, p1);
       lo[j] = bf16x2_of(p0 - __uint_as_float(hi[j] << 16),
                         p1 - __uint_as_float(hi[j] & 0xFFFF0000u));
     }
-    // rows that do not count may hold anything: zeros instead (0 * NaN is NaN)
-    uint32_t keep[2];
-#pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      const uint32_t two = mask >> (8 * j + 2 * c) & 3u;
-      keep[j] = (two & 1u ? 0xFFFFu : 0u) | (two & 2u ? 0xFFFF0000u : 0u);
-    }
-    const bool whole = mask == 0xFFFFu;
+    const uint32_t va = vs + (lane & 15) * 128 + (((lane >> 4) ^ (lane & 7)) << 4);
 #pragma unroll
     for (int t = 0; t < NT; t += 2) {
       uint32_t b[4];
-      ldsm4_t(b, vs + piece<RT>((lane & 7) + (lane & 8), t + (lane >> 4)));
-      if (!whole) {
-        b[0] &= keep[0];
-        b[1] &= keep[1];
-        b[2] &= keep[0];
-        b[3] &= keep[1];
-      }
+      ldsm4_t(b, (va ^ ((t & 6) * 16)) + (t >> 3) * (RT * 128));
       mma_bf16_16816(this->o[t], hi[0], lo[0], hi[1], lo[1], b[0], b[1]);
       mma_bf16_16816(this->o[t + 1], hi[0], lo[0], hi[1], lo[1], b[2], b[3]);
     }
@@ -229,52 +242,54 @@ struct Tile<float, NSEG> : State<NSEG * 4> {
       w[i] = g < G && x < d ? __float_as_uint(src[g * d + x]) : 0u;
     }
   }
-  __device__ __forceinline__ void set_q(const uint32_t (&w)[NQ]) {
+  __device__ __forceinline__ void set_q(const uint32_t (&w)[NQ], const Scale& sc) {
 #pragma unroll
-    for (int i = 0; i < NQ; ++i) tf32_split(__uint_as_float(w[i]), qh[i], ql[i]);
+    for (int i = 0; i < NQ; ++i) tf32_split(__uint_as_float(w[i] ^ sc.flip), qh[i], ql[i]);
   }
 
   __device__ __forceinline__ void tile(uint32_t ks, uint32_t vs, uint32_t mask, float c2) {
     constexpr int NB = RT / 8;
     const int lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
+    // scores: the high and the low parts of k in sums of their own
     float z[NB][2], mt = -INFINITY;
+    const uint32_t ka = ks + g * 128 + (g << 4) + 4 * c;
 #pragma unroll
     for (int j = 0; j < NB; ++j) {
-      float s[4] = {0.f, 0.f, 0.f, 0.f};
+      float s[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
 #pragma unroll
       for (int k = 0; k < NT; ++k) {
+        const uint32_t at = (k >> 2) * (RT * 128) + j * 1024;
         uint32_t h0, l0, h1, l1;
-        tf32_split(lds_f(ks + piece<RT>(8 * j + g, 2 * k) + 4 * c), h0, l0);
-        tf32_split(lds_f(ks + piece<RT>(8 * j + g, 2 * k + 1) + 4 * c), h1, l1);
-        mma_tf32_1688(s, qh[2 * k], ql[2 * k], qh[2 * k + 1], ql[2 * k + 1], h0, h1);
-        mma_tf32_1688(s, qh[2 * k], ql[2 * k], qh[2 * k + 1], ql[2 * k + 1], l0, l1);
+        tf32_split(lds_f((ka ^ ((2 * k & 7) << 4)) + at), h0, l0);
+        tf32_split(lds_f((ka ^ ((2 * k + 1 & 7) << 4)) + at), h1, l1);
+        mma_tf32_1688(s[0], qh[2 * k], ql[2 * k], qh[2 * k + 1], ql[2 * k + 1], h0, h1);
+        mma_tf32_1688(s[1], qh[2 * k], ql[2 * k], qh[2 * k + 1], ql[2 * k + 1], l0, l1);
       }
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        z[j][e] = mask >> (8 * j + 2 * c + e) & 1 ? (s[e] + s[2 + e]) * c2 : -INFINITY;
+        z[j][e] = (s[0][e] + s[0][2 + e]) + (s[1][e] + s[1][2 + e]);
+        if (mask != (1u << RT) - 1u && !(mask >> (8 * j + 2 * c + e) & 1)) z[j][e] = -INFINITY;
         mt = fmaxf(mt, z[j][e]);
       }
     }
-    this->raise(mt);
-    const float base = this->base();
+    this->raise(mt, c2);
+    const float base = this->base(c2);
+    // rows 2 c and 2 c + 1 of each 8, pieces under xor their row
+    const uint32_t v0 = vs + 2 * c * 128 + (((g >> 2) ^ (2 * c)) << 4) + 4 * (g & 3);
+    const uint32_t v1 = v0 + 128 - (((g >> 2) ^ (2 * c)) << 4) + (((g >> 2) ^ (2 * c + 1)) << 4);
 #pragma unroll
     for (int j = 0; j < NB; ++j) {
-      const float p0 = ptx::ex2(z[j][0] - base), p1 = ptx::ex2(z[j][1] - base);
+      const float p0 = ptx::ex2(fmaf(z[j][0], c2, base)), p1 = ptx::ex2(fmaf(z[j][1], c2, base));
       this->l += p0 + p1;
       uint32_t h0, l0, h1, l1;
       tf32_split(p0, h0, l0);
       tf32_split(p1, h1, l1);
-      const bool k0 = mask >> (8 * j + 2 * c) & 1, k1 = mask >> (8 * j + 2 * c + 1) & 1;
 #pragma unroll
       for (int t = 0; t < NT; ++t) {
-        const int cp = 2 * t + (g >> 2), w = 4 * (g & 3);
-        float v0 = lds_f(vs + piece<RT>(8 * j + 2 * c, cp) + w);
-        float v1 = lds_f(vs + piece<RT>(8 * j + 2 * c + 1, cp) + w);
-        if (!k0) v0 = 0.f;
-        if (!k1) v1 = 0.f;
+        const uint32_t x = (2 * t & 7) << 4, at = (t >> 2) * (RT * 128) + j * 1024;
         uint32_t vh0, vl0, vh1, vl1;
-        tf32_split(v0, vh0, vl0);
-        tf32_split(v1, vh1, vl1);
+        tf32_split(lds_f((v0 ^ x) + at), vh0, vl0);
+        tf32_split(lds_f((v1 ^ x) + at), vh1, vl1);
         mma_tf32_1688(this->o[t], h0, l0, h1, l1, vh0, vh1);
         mma_tf32_1688(this->o[t], h0, l0, h1, l1, vl0, vl1);
       }

@@ -344,6 +344,21 @@ def test_decode_head_tables_skewed():
     c.check_pools()
 
 
+@pytest.mark.parametrize("lens", [[30000, 9000, 100, 26001], [1] * 50 + [20000, 45000],
+                                  [65001]])
+@pytest.mark.parametrize("dtype,d,G", [("bf16", 128, 1), ("bf16", 64, 3), ("f32", 40, 1)])
+def test_decode_many_tiles_a_warp(dtype, d, G, lens):
+    """Calls large enough that CTAs take further segments and a warp has over 32 tiles."""
+    c = Cache(len(lens), 8, G, d, 1, 64, lens, dtype, 12)
+    out, ws = c.run()
+    torch.cuda.synchronize()
+    assert kv.kv_check_device_status(ws) == 0
+    c.check(out)
+    c.check_pools()
+    for _ in range(5):
+        assert torch.equal(out, c.run(ws=ws)[0])
+
+
 @pytest.mark.parametrize("extra", [8, 64, 4096])
 def test_decode_page_stride(extra):
     c = Cache(3, 2, 4, 128, 1, 16, [100, 0, 333], "bf16", 5, page_stride=2 * 16 * 128 + extra)
