@@ -9,9 +9,9 @@
 //      Ne) and each of its warps an equal part of that.  A CTA boundary that falls inside a
 //      short unit moves to the nearer end of it, so only long units cross CTAs.
 //   2. A warp walks its tiles 32 at a time: lane i works out tile i (its table by a search
-//      over 32 tables' running sums, then the page number) and later issues its TMA boxes.
-//      K and V tiles land, swizzled, in the warp's own ring of stages; the warp runs the
-//      online softmax of paged_mma.cuh over them.  No CTA barrier in the loop.
+//      over 32 tables' running sums, then the page number).  Tiles are copied 16 bytes a lane
+//      (cp.async), swizzled, into the warp's own ring of stages; the warp runs the online
+//      softmax of paged_mma.cuh over them.  No CTA barrier in the loop.
 //   3. A unit held by one warp is written out by it.  The parts of a unit split between warps
 //      are merged in shared memory; of one that crosses CTAs, each CTA leaves one part in the
 //      workspace, and the last of them to finish (a ticket) merges those in order, so the
@@ -21,13 +21,8 @@
 // place, put there when the stage has landed, and stored to its slot.
 // Rows past a table's last one, and rows of pages outside the pool, are masked: their scores
 // are -inf and their values zeros.  No CTA waits for another.
-#include <cuda.h>
-#include <cudaTypedefs.h>
-
 #include <cfloat>
 #include <cmath>
-
-#include <mutex>
 
 #include "paged_mma.cuh"
 
@@ -39,7 +34,6 @@ constexpr int kCtasPerSm = 2;
 constexpr int kPThreads = kPWarps * 32;
 constexpr int kMaxCtas = 320;
 constexpr int kRingBytes = 16 * 1024;   // of a warp
-constexpr int kMaxStages = 6;
 // Tiles per CTA at least: a small call runs on as few CTAs as that allows.
 constexpr int kMinTiles = 8;
 // A boundary inside a unit of at most this many tiles moves to the unit's nearer end.
@@ -71,8 +65,11 @@ struct Cfg {
   static constexpr int kRow = NSEG * 128;                  // bytes of a row in a stage
   static constexpr int kHalf = RT * kRow;                  // K, then V
   static constexpr int kStages = kRingBytes / (2 * kHalf);
-  static_assert(kStages >= 2 && kStages <= kMaxStages, "ring");
+  static_assert(kStages >= 2, "ring");
   static constexpr int kSide = kStages * 2 * kRow;         // of a warp: its stages' new rows
+  // a copy instruction of a warp: kRows rows of kLanes 16-byte pieces
+  static constexpr int kLanes = NSEG <= 2 ? NSEG * 8 : 32;
+  static constexpr int kRows = 32 / kLanes;
   static_assert(2 * 8 * Tl::D * 4 <= 2 * kHalf, "a warp's two parts fit one stage");
 };
 
@@ -83,7 +80,6 @@ struct PagedSmem {
   uint32_t strip[kPThreads];                 // tiles before thread t's tables
   int32_t lens[kPThreads];                   // rows per table, where a thread has one table
   uint32_t wsum[kPWarps];
-  uint64_t full[kPWarps][kMaxStages];
   // the parts warp w leaves in one of its stages (at byte `at`): of a unit that began before
   // its tiles (a), of one that goes on after them (b); unit or -1, and whether the unit of
   // part a goes on as well
@@ -146,8 +142,9 @@ __device__ __forceinline__ void seek(Window& w, uint32_t x, const PagedArgs& a, 
 // What a lane knows of one tile.
 struct Desc {
   int32_t unit;
-  int32_t page, page2;   // page2: of the tile's second 8 rows, when a page holds 8
-  int32_t row;           // row of the pool's page: head * page + first row within the page
+  int64_t at;            // element of the pool where the tile's first row begins; in pages of 8
+                         // rows, of its first 8
+  int64_t at2;           // of its second 8 rows
   uint32_t mask;         // bits 0..15: rows that count; kFirst / kLast: the unit's first / last
                          // tile; bits 24..27: its last row
   int64_t slot;          // where the new row (the unit's last) goes, or -1
@@ -173,11 +170,17 @@ __device__ __forceinline__ void store4(__nv_bfloat16* p, const float4& v) {
   w.y = pmma::bf16x2_of(v.z, v.w);
   *reinterpret_cast<uint2*>(p) = w;
 }
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+// 16 bytes from global to shared memory; `bytes` of them are read, the rest is zero.
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, int bytes = 16) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes)
+               : "memory");
 }
-__device__ __forceinline__ void cp_async_wait_all() {
-  asm volatile("cp.async.wait_all;" ::: "memory");
+__device__ __forceinline__ void cp_async_commit() {
+  asm volatile("cp.async.commit_group;" ::: "memory");
+}
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {   // all groups but the last N
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
 // Merge of up to kB parts (max, sum, 4 outputs each; max -inf: none) into (M, L, acc).
@@ -206,12 +209,11 @@ __device__ __forceinline__ void merge_parts(const float (&m)[kB], const float (&
 
 template <typename T, int NSEG>
 __global__ void __launch_bounds__(kPThreads, kCtasPerSm)
-paged_decode_kernel(const __grid_constant__ CUtensorMap kmap,
-                    const __grid_constant__ CUtensorMap vmap, const PagedArgs a) {
+paged_decode_kernel(const __grid_constant__ PagedArgs a) {
   using C = Cfg<T, NSEG>;
   using Tl = typename C::Tl;
   constexpr int RT = C::RT, S = C::kStages, NT = Tl::NT, D = Tl::D;
-  constexpr int kSegElems = 128 / (int)sizeof(T);
+  constexpr int VE = 16 / (int)sizeof(T);   // elements of a piece
   extern __shared__ unsigned char dsm_raw[];
   PagedSmem<C>& sm = *reinterpret_cast<PagedSmem<C>*>(
       (reinterpret_cast<uintptr_t>(dsm_raw) + 1023) & ~(uintptr_t)1023);
@@ -219,15 +221,6 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap kmap,
   const int N = (int)gridDim.x, c = (int)blockIdx.x;
   const int page = 1 << a.shift, d = a.d, G = a.G;
   const int most = a.max_pages << a.shift;
-  if (lane == 0) {
-    for (int s = 0; s < S; ++s) ptx::mbar_init(&sm.full[warp][s], 1);
-    ptx::fence_mbar_init();
-    if (warp == 0) {
-      ptx::tma_prefetch_desc(&kmap);
-      ptx::tma_prefetch_desc(&vmap);
-    }
-  }
-
   // a programmatic dependent launch: nothing of the call before is read or written until it ends
   ptx::griddep_launch_dependents();
   ptx::griddep_wait();
@@ -331,19 +324,17 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap kmap,
   // ---- 2. this warp's tiles
   unsigned char* ring = sm.ring[warp];
   unsigned char* side = sm.side[warp];
-  uint64_t* full = sm.full[warp];
   const uint32_t ring_u = ptx::smem_u32(ring), side_u = ptx::smem_u32(side);
-  const int pieces = d * (int)sizeof(T) / 16;   // 16-byte pieces of a row
+  const int pieces = d / VE;   // 16-byte pieces of a row
   const bool has_new = a.kn != nullptr;
   const T* qp = (const T*)a.q;
   Tl att;
-  bool ok = true;
   // cur holds tiles cur0..cur0 + 31, nxt the 32 behind them
   Desc cur, nxt;
   int cur0 = 0;
   // loads on nxt's account that have not been looked at: its pages, and cu of the last tile's
   // table and the next
-  int32_t p_page = 0, p_page2 = 0;
+  int32_t p_page = 0, p_page2 = 0, p_row = 0;   // p_row: head * page + row within the page
   int64_t p_c0 = 0, p_c1 = 0;
   bool ready = true;     // there are none
 
@@ -385,7 +376,7 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap kmap,
           }
         }
         nxt.unit = u * a.Hp + h;
-        nxt.row = h * page + (r0 & (page - 1));
+        p_row = h * page + (r0 & (page - 1));
         // the units of the warp's first and last tiles, for the merges
         const uint32_t first = x - tt;
         if (x == xs) sm.ends[warp][0] = make_uint2(first, first + nt);
@@ -396,49 +387,65 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap kmap,
     }
     ready = false;
   };
-  // What describe() asked for, once it is there.  Pages outside the pool: their rows do not
-  // count (page 0 is read in their place).  The slot of a unit's new row is only asked for here.
+  // What describe() asked for, once it is there.  Rows of pages outside the pool do not count.
+  // The slot of a unit's new row is only asked for here.
   auto settle = [&]() {
     if (ready) return;
     ready = true;
     const bool bad = p_page < 0 || p_page >= a.num_pages;
     const bool bad2 = p_page2 < 0 || p_page2 >= a.num_pages;
-    nxt.page = bad ? 0 : p_page;
-    nxt.page2 = bad2 ? 0 : p_page2;
+    nxt.at = (bad ? 0 : p_page) * a.page_stride + p_row * (int64_t)d;
+    nxt.at2 = (bad2 ? 0 : p_page2) * a.page_stride + p_row * (int64_t)d;
     if (bad) nxt.mask &= page < RT ? ~0xFFu : ~0xFFFFu;
     if (bad2) nxt.mask &= ~0xFF00u;
     if (bad || bad2) raise_dev(a.hdr, DEV_PAGE_ID, (unsigned)nxt.unit);
     nxt.slot = -1;
     if (p_c1 > p_c0 && p_c1 > 0 && p_c1 <= a.slot_cap) nxt.slot = a.slots[p_c1 - 1];
   };
-  // lane src's tile of t into stage s: that lane issues it
+  // Lane src's tile of t into stage s: rows `i kRows + lr`, piece `pc` of each is this lane's.
+  // (A piece's address is xor its row's low bits, and kRows divides 8: one address per lane, xor
+  // and plus constants.)
+  const int pc = lane % C::kLanes, lr = lane / C::kLanes;
+  const uint32_t to = ring_u + (pc >> 3) * (RT * 128) + lr * 128 + (((pc & 7) ^ lr) << 4);
+  const int64_t from = (int64_t)lr * d + pc * VE;
   auto issue = [&](const Desc& t, int src, int s) {
-    if (lane == src) {
-      ptx::mbar_arrive_expect_tx(&full[s], 2u * C::kHalf);
-      unsigned char* st = ring + s * 2 * C::kHalf;
+    constexpr uint32_t kAll = (1u << RT) - 1u;
+    const int64_t at = __shfl_sync(0xffffffffu, (long long)t.at, src) + from;
+    const uint32_t mask = __shfl_sync(0xffffffffu, t.mask, src);
+    const uint32_t dst = to + s * 2 * C::kHalf;
+    const T* ks = (const T*)a.kp + at;
+    const T* vs = (const T*)a.vp + at;
+    // in pages of 8 rows: from a row of the first 8 to one of the second
+    int64_t skip = 0;
+    if (page < RT) skip = __shfl_sync(0xffffffffu, (long long)(t.at2 - t.at), src) - 8 * (int64_t)d;
+    if (pc < pieces) {
+      if ((mask & kAll) == kAll && page >= RT) {
 #pragma unroll
-      for (int g = 0; g < NSEG; ++g) {
-        ptx::tma_load_3d(st + g * RT * 128, &kmap, &full[s], g * kSegElems, t.row, t.page);
-        ptx::tma_load_3d(st + C::kHalf + g * RT * 128, &vmap, &full[s], g * kSegElems, t.row,
-                         t.page);
-        if (page < RT) {
-          ptx::tma_load_3d(st + g * RT * 128 + 1024, &kmap, &full[s], g * kSegElems, t.row,
-                           t.page2);
-          ptx::tma_load_3d(st + C::kHalf + g * RT * 128 + 1024, &vmap, &full[s], g * kSegElems,
-                           t.row, t.page2);
+        for (int i = 0; i < RT / C::kRows; ++i) {
+          const uint32_t x = (dst ^ (((i * C::kRows) & 7) << 4)) + i * C::kRows * 128;
+          cp_async16(x, ks + i * C::kRows * d);
+          cp_async16(x + C::kHalf, vs + i * C::kRows * d);
+        }
+      } else {
+        // rows that do not count are not read: zeros
+#pragma unroll
+        for (int i = 0; i < RT / C::kRows; ++i) {
+          const uint32_t x = (dst ^ (((i * C::kRows) & 7) << 4)) + i * C::kRows * 128;
+          const int r = i * C::kRows + lr, n = mask >> r & 1 ? 16 : 0;
+          const int64_t o = n == 0 ? -at : i * C::kRows * d + (page < RT && r >= 8 ? skip : (int64_t)0);
+          cp_async16(x, ks + o, n);
+          cp_async16(x + C::kHalf, vs + o, n);
         }
       }
     }
-    if (has_new && (__shfl_sync(0xffffffffu, t.mask, src) & kLast)) {
+    if (has_new && (mask & kLast)) {
       const int64_t u = __shfl_sync(0xffffffffu, t.unit, src);
       for (int p = lane; p < pieces; p += 32) {
-        cp_async16(side_u + s * 2 * C::kRow + p * 16, (const T*)a.kn + u * d + p * kSegElems / 8);
-        cp_async16(side_u + s * 2 * C::kRow + C::kRow + p * 16,
-                   (const T*)a.vn + u * d + p * kSegElems / 8);
+        cp_async16(side_u + s * 2 * C::kRow + p * 16, (const T*)a.kn + u * d + p * VE);
+        cp_async16(side_u + s * 2 * C::kRow + C::kRow + p * 16, (const T*)a.vn + u * d + p * VE);
       }
     }
   };
-  __syncwarp();   // the barriers are initialised
   int32_t unit_a = -1, unit_b = -1;
   bool open_a = false, far = false;
   if (count > 0) {
@@ -446,14 +453,22 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap kmap,
     describe(xs);
     settle();
     cur = nxt;
-    for (int i = 0; i < S && i < count; ++i) issue(cur, i, i);
+  }
+  if (pieces < NSEG * 8) {   // columns past d: zeros, for good
+    for (int i = lane; i < kRingBytes / 16; i += 32)
+      reinterpret_cast<uint4*>(ring)[i] = make_uint4(0u, 0u, 0u, 0u);
+    __syncwarp();
+  }
+#pragma unroll
+  for (int i = 0; i < S; ++i) {   // one group of copies a tile, empty past the last
+    if (i < count) issue(cur, i, i);
+    cp_async_commit();
   }
   if (count > 32) describe(xs + 32);
   uint32_t qw[Tl::NQ];
   int32_t q_unit = -1;   // unit whose q words qw holds
   bool whole = false;    // the warp has the unit from its first tile on
   int s = 0;             // stage of tile i
-  uint32_t phase = 0;    // of its barrier
   uint32_t firsts = 0, lasts = 0, cuts = 0;   // cur's tiles: units' first, last; not all rows
   for (int i = 0; i < count; ++i) {
     if (i - cur0 == 32) {
@@ -482,24 +497,9 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap kmap,
         Tl::load_q(qp + (int64_t)q_unit * G * d, G, d, qw);
       }
     }
-    if (ok) {
-      const bool landed = ptx::mbar_wait(&full[s], phase);
-      if (__any_sync(0xffffffffu, !landed)) {
-        ok = false;
-        if (lane == 0) {
-          raise_dev(a.hdr, DEV_WAIT_TIMEOUT, 0x800u + (unsigned)s);
-          // a wait gave up: let what is in flight land before the memory is reused
-          int t = s;
-          uint32_t ph = phase;
-          for (int k = i; k < count && k < i + S; ++k) {
-            (void)ptx::mbar_wait(&full[t], ph, 20000000ull);
-            if (++t == S) t = 0, ph ^= 1;
-          }
-        }
-        __syncwarp();
-      }
-    }
-    if (ok) {
+    cp_async_wait<S - 1>();
+    __syncwarp();
+    {
       const uint32_t ks = ring_u + s * 2 * C::kHalf, vs = ks + C::kHalf;
       uint32_t mask = (1u << RT) - 1u;
       if ((cuts >> src & 1) || (has_new && last)) {
@@ -512,8 +512,6 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap kmap,
           const int32_t unit = __shfl_sync(0xffffffffu, cur.unit, src);
           const bool in_pool = slot >= 0 && slot < (a.num_pages << a.shift);
           if (slot != -1 && !in_pool && lane == 0) raise_dev(a.hdr, DEV_PAGE_ID, (unsigned)unit);
-          cp_async_wait_all();
-          __syncwarp();
           if (in_pool) {
             // the new row, to its place in the tile and to its slot
             mask |= 1u << r;
@@ -530,8 +528,6 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap kmap,
             }
           }
         }
-        pmma::clear_rows<RT>(st + C::kHalf, mask, NSEG);
-        ptx::fence_proxy_async_smem();   // before the stage is refilled
         __syncwarp();
       }
       att.tile(ks, vs, mask, a.scale.c2);
@@ -541,6 +537,7 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap kmap,
         if (n >= 32) settle();
         issue(n < 32 ? cur : nxt, n & 31, s);
       }
+      cp_async_commit();
     }
     // ---- the end of a unit, or of the warp's tiles
     if (last || i == count - 1) {
@@ -578,7 +575,7 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap kmap,
               make_float2(att.o[t][0], att.o[t][1]);
       }
     }
-    if (i < count - 1 && ++s == S) s = 0, phase ^= 1;
+    if (i < count - 1 && ++s == S) s = 0;
   }
 
   // ---- 3. what the warps leave
@@ -592,7 +589,7 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap kmap,
   }
   __syncthreads();
   // Heads: lane 0 stands for the unit of warp 0's part a, lane i > 0 for that of warp
-  // i - 1's part b.  A head's unit goes on in the parts a of the warps from `from` on, up to
+  // i - 1's part b.  A head's unit goes on in the parts a of the warps behind it, up to
   // the first warp with tiles whose part a (if any) ends there; if there is none it crosses
   // the CTA's end.
   int32_t unit = -1;
@@ -605,8 +602,8 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap kmap,
     const int32_t before = __shfl_up_sync(0xffffffffu, ub, 1);
     unit = lane == 0 ? ua : lane <= kPWarps ? before : -1;
   }
-  const uint32_t from = ~0u << (lane == 0 ? 1 : lane & 15), stop = stops & from;
-  uint32_t members = part_a & from & (stop ? (stop ^ (stop - 1)) : ~0u);
+  const uint32_t after = ~0u << (lane == 0 ? 1 : lane & 15), stop = stops & after;
+  uint32_t members = part_a & after & (stop ? (stop ^ (stop - 1)) : ~0u);
   if (lane == 0 && (stops & 1)) members = 0;
   const uint32_t heads = __ballot_sync(0xffffffffu, unit >= 0);
   const uint32_t cross = __ballot_sync(0xffffffffu, unit >= 0 && (lane == 0 || stop == 0));
@@ -738,38 +735,6 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap kmap,
 
 // ------------------------------------- host side ----------------------------------------
 
-PFN_cuTensorMapEncodeTiled_v12000 paged_encode_fn() {
-  static std::once_flag once;
-  static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
-  std::call_once(once, [] {
-    void* ptr = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &ptr, 12000,
-                                         cudaEnableDefault, &q) == cudaSuccess &&
-        q == cudaDriverEntryPointSuccess)
-      fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(ptr);
-  });
-  return fn;
-}
-
-// The pool as [num_pages][Hp * page rows][d], in boxes of 128 bytes of `rows` rows of one page,
-// swizzled; columns past d read as zero.
-bool pool_map(CUtensorMap* map, const void* base, const PagedShape& s, int rows) {
-  auto fn = paged_encode_fn();
-  if (fn == nullptr) return false;
-  const uint64_t e = (uint64_t)s.esize();
-  const cuuint64_t dims[3] = {(cuuint64_t)s.d, (cuuint64_t)s.Hp() * s.page,
-                              (cuuint64_t)s.num_pages};
-  const cuuint64_t strides[2] = {(cuuint64_t)s.d * e, (cuuint64_t)s.page_stride * e};
-  const cuuint32_t box[3] = {(cuuint32_t)(128 / e), (cuuint32_t)rows, 1};
-  const cuuint32_t estr[3] = {1, 1, 1};
-  return fn(map,
-            s.dtype == KV_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32,
-            3, const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-            CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
 constexpr size_t kTickBytes = 2048;
 static_assert(kMaxCtas * sizeof(uint32_t) <= kTickBytes, "tickets");
 
@@ -785,10 +750,6 @@ cudaError_t launch_t(const PagedShape& s, const PagedArgs& a, cudaStream_t st) {
                                 (int)smem) == cudaSuccess ? 1 : 0;
   });
   if (!ok) return cudaErrorInvalidConfiguration;
-  CUtensorMap km, vm;
-  const int rows = s.page < C::RT ? s.page : C::RT;
-  if (!pool_map(&km, a.kp, s, rows) || !pool_map(&vm, a.vp, s, rows))
-    return cudaErrorInvalidValue;
   // no more CTAs than the tables could ever fill
   const int64_t tiles = (int64_t)s.seqs * s.Hkv * cdiv((int64_t)s.max_pages * s.page, C::RT);
   int64_t grid = cdiv(tiles, kMinTiles);
@@ -802,7 +763,7 @@ cudaError_t launch_t(const PagedShape& s, const PagedArgs& a, cudaStream_t st) {
   cudaLaunchAttribute attr[1] = {pdl_attribute()};
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, paged_decode_kernel<T, NSEG>, km, vm, a);
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, paged_decode_kernel<T, NSEG>, a);
   if (e == cudaSuccess) count_launches(1);
   return e;
 }

@@ -3,7 +3,7 @@
 //   p_r = exp2(c2 (q . k_r - m)),  l = sum p_r,  o = sum p_r v_r,   c2 > 0.
 //
 // A tile is RT rows, K then V, each as NSEG segments of [RT][128 bytes] with the 16-byte
-// pieces of row r permuted by r & 7 (TMA's 128-byte swizzle): every access below touches 8
+// pieces of row r permuted by r & 7, so that every access below touches 8
 // different pieces of the 32 banks.
 //
 // m16n8k16 (bf16) and m16n8k8 (tf32) have 16 rows where a KV head has at most 8 queries.  The
@@ -92,14 +92,6 @@ struct Scale {
   uint32_t flip;   // sign bits of q to flip (bf16: of both halves)
 };
 
-// Rows of a tile's V that do not count may hold anything, and 0 * NaN is NaN: zeros instead.
-// (Before tile(), when `mask` is not all ones; all lanes, with a __syncwarp behind it.)
-template <int RT>
-__device__ __forceinline__ void clear_rows(unsigned char* v, uint32_t mask, int nseg) {
-  for (int i = threadIdx.x & 31; i < nseg * RT * 8; i += 32)
-    if (!(mask >> (i / 8 % RT) & 1)) reinterpret_cast<uint4*>(v)[i] = make_uint4(0u, 0u, 0u, 0u);
-}
-
 template <typename T, int NSEG>
 struct Tile;
 
@@ -169,7 +161,8 @@ struct Tile<__nv_bfloat16, NSEG> : State<NSEG * 8> {
     for (int i = 0; i < NQ; ++i) q[i] = w[i] ^ sc.flip;
   }
 
-  // One tile at shared addresses ks, vs (1024-byte aligned); bit r of `mask`: row r counts.
+  // One tile at shared addresses ks, vs (1024-byte aligned); bit r of `mask`: row r counts
+  // (others hold zeros: 0 * NaN is NaN).
   // A piece's address is its row's with piece bits under xor (r & 7) * 16, so the pieces of a
   // lane's row are one address xor a constant.
   __device__ __forceinline__ void tile(uint32_t ks, uint32_t vs, uint32_t mask, float c2) {
