@@ -302,91 +302,100 @@ def kv_paged_workspace_size(op: int, shape: KvPagedShape) -> int:
     return int(lib().kv_paged_workspace_size(op, ctypes.byref(shape)))
 
 
-_DT = {}   # the torch dtypes of the paged calls, once torch is imported
+# torch's dtypes and lookups for the paged calls, set when the first of them runs
+_I32 = _I64 = _device_now = _stream_now = None
+_ROWS = {}
 
 
-def _dtypes():
-    if not _DT:
-        import torch
-        _DT.update(i32=torch.int32, i64=torch.int64, rows={KV_BF16: torch.bfloat16,
-                                                           KV_F32: torch.float32},
-                   device=torch.cuda.current_device,
-                   stream=getattr(torch._C, "_cuda_getCurrentRawStream", None) or
-                   (lambda dev: torch.cuda.current_stream(dev).cuda_stream))
-    return _DT
+def _init_torch() -> None:
+    global _I32, _I64, _device_now, _stream_now
+    import torch
+    _I32, _I64 = torch.int32, torch.int64
+    _ROWS.update({KV_BF16: torch.bfloat16, KV_F32: torch.float32})
+    _stream_now = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+        lambda dev: torch.cuda.current_stream(dev).cuda_stream)
+    _device_now = torch.cuda.current_device
 
 
 def _device(t, what: str) -> int:
     """The current device (a host tensor raises before CUDA is asked)."""
     if not isinstance(t, int) and not t.is_cuda:
         raise ValueError("%s must be on a CUDA device" % what)
-    return _dtypes()["device"]()
+    if _device_now is None:
+        _init_torch()
+    return _device_now()
 
 
 def _buf(t, dtype, count: int, dev: int, what: str) -> Optional[int]:
     """Device pointer of a contiguous tensor of the type and at least the entries that the call
     may touch, on the current device (None stays NULL, an int is a pointer already)."""
-    if t is None or isinstance(t, int):
-        return t
-    if not t.is_cuda:
-        raise ValueError("%s must be on a CUDA device" % what)
+    try:
+        if t.dtype is dtype and t.get_device() == dev and t.numel() >= count and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:
+        if t is None or isinstance(t, int):
+            return t
+        raise
     if t.get_device() != dev:
-        raise ValueError("%s is on another device than the current one" % what)
-    if dtype is not None and t.dtype is not dtype:
+        raise ValueError("%s must be on the current CUDA device" % what)
+    if t.dtype is not dtype:
         raise ValueError("%s must be %s" % (what, dtype))
     if t.numel() < count:
         raise ValueError("%s has %d entries, needs %d" % (what, t.numel(), count))
-    if not t.is_contiguous():
-        raise ValueError("%s must be contiguous" % what)
-    return t.data_ptr()
+    raise ValueError("%s must be contiguous" % what)
 
 
-def _rows_view(t, dtype, hp: int, d: int, dev: int, what: str):
-    """Pointer, count and stride (elements) of rows [n][hp][d] or [n][hp * d]; a row is
+def _work(ws, dev: int):
+    """Pointer and bytes of a workspace (of any type)."""
+    return _buf(ws, ws.dtype, 0, dev, "ws"), ws.numel() * ws.element_size()
+
+
+def _rows_view(t, dtype, row: int, dev: int, what: str):
+    """Pointer, count and stride (elements) of rows of `row` elements, [n][...]; a row is
     contiguous, rows may lie apart (parts of a fused projection)."""
-    if not t.is_cuda or t.get_device() != dev:
-        raise ValueError("%s must be on the current CUDA device" % what)
-    if t.dtype is not dtype:
-        raise ValueError("%s must be %s" % (what, dtype))
+    if t.get_device() != dev or t.dtype is not dtype:
+        raise ValueError("%s must be %s on the current CUDA device" % (what, dtype))
     size = t.shape
     n = size[0]
-    if len(size) < 2 or t.numel() != n * hp * d:
-        raise ValueError("%s must be rows of %d heads x %d" % (what, hp, d))
-    if t.is_contiguous():
-        return t.data_ptr(), n, hp * d
-    stride, step = t.stride(), 1
-    for k in range(len(size) - 1, 0, -1):
-        if size[k] > 1 and stride[k] != step:
-            raise ValueError("the rows of %s must be contiguous" % what)
-        step *= size[k]
-    return t.data_ptr(), n, (stride[0] if n > 1 else hp * d)
-
-
-def _pool(shape: KvPagedShape, t, dtype, dev: int, what: str) -> Optional[int]:
-    """Pointer of a page pool: its pages are dense, ``page_stride`` elements apart."""
-    if t is None or isinstance(t, int):
-        return t
-    if not t.is_cuda or t.get_device() != dev:
-        raise ValueError("%s must be on the current CUDA device" % what)
-    if t.dtype is not dtype:
-        raise ValueError("%s must be %s" % (what, dtype))
-    inner = (shape.hkv // shape.tables) * shape.page * shape.d
-    want, pages, size = shape.page_stride or inner, shape.num_pages, t.shape
-    ok = size[0] >= pages and t.numel() == size[0] * inner
-    if ok and not (want == inner and t.is_contiguous()):
-        stride, step = t.stride(), 1
+    if len(size) < 2 or t.numel() != n * row:
+        raise ValueError("%s must be rows of %d elements" % (what, row))
+    stride = row
+    if not t.is_contiguous():
+        strides, step = t.stride(), 1
         for k in range(len(size) - 1, 0, -1):
-            ok = ok and (size[k] == 1 or stride[k] == step)
+            if size[k] > 1 and strides[k] != step:
+                raise ValueError("the rows of %s must be contiguous" % what)
             step *= size[k]
-        ok = ok and (pages == 1 or stride[0] == want)
-    if not ok:
-        raise ValueError("%s must be [num_pages][heads][page][d], pages page_stride apart" % what)
-    return t.data_ptr()
+        if n > 1:
+            stride = strides[0]
+    return t.data_ptr(), n, stride
+
+
+def _pool(t, dtype, inner: int, pages: int, page_stride: int, dev: int, what: str):
+    """Pointer of a page pool: pages of `inner` elements, dense, ``page_stride`` apart."""
+    try:
+        if t.dtype is dtype and t.get_device() == dev:
+            n = t.shape[0]
+            if n >= pages and t.numel() == n * inner:
+                if t.is_contiguous() and (page_stride == inner or pages == 1):
+                    return t.data_ptr()
+                size, strides, step, ok = t.shape, t.stride(), 1, True
+                for k in range(len(size) - 1, 0, -1):
+                    ok = ok and (size[k] == 1 or strides[k] == step)
+                    step *= size[k]
+                if ok and (pages == 1 or strides[0] == page_stride):
+                    return t.data_ptr()
+    except AttributeError:
+        if t is None or isinstance(t, int):
+            return t
+        raise
+    raise ValueError("%s must be [num_pages][heads][page][d] %s on the current CUDA device, pages "
+                     "page_stride apart" % (what, dtype))
 
 
 def _stream_on(stream, dev: int) -> Optional[int]:
     if stream is None:
-        return _DT["stream"](dev)
+        return _stream_now(dev)
     return stream if isinstance(stream, int) else stream.cuda_stream
 
 
@@ -394,56 +403,63 @@ def kv_page_map(shape: KvPagedShape, lens, add, free_ring, free_state, block_tab
                 free_out, cu_add, slot_map, ws, stream=None) -> None:
     """Block tables, slots and lengths for the rows each table gains or loses.  ``lens_out`` may
     be ``lens`` and ``free_out`` may be ``free_state``."""
-    dev, dt = _device(lens, "lens"), _dtypes()
-    i32, i64 = dt["i32"], dt["i64"]
-    n = shape.seqs * shape.tables
+    dev = _device(lens, "lens")
+    i32, i64, n = _I32, _I64, shape.seqs * shape.tables
+    wp, wn = _work(ws, dev)
     st = lib().kv_page_map(
         ctypes.byref(shape), _buf(lens, i32, n, dev, "lens"), _buf(add, i32, n, dev, "add"),
         _buf(free_ring, i32, shape.num_pages, dev, "free_ring"),
         _buf(free_state, i64, 2, dev, "free_state"), slot_map.numel(),
         _buf(block_table, i32, n * shape.max_pages, dev, "block_table"),
         _buf(lens_out, i32, n, dev, "lens_out"), _buf(free_out, i64, 2, dev, "free_out"),
-        _buf(cu_add, i64, n + 1, dev, "cu_add"), _buf(slot_map, i64, 0, dev, "slot_map"),
-        _buf(ws, None, 0, dev, "ws"), _nbytes(ws), _stream_on(stream, dev))
-    _check("kv_page_map", st)
+        _buf(cu_add, i64, n + 1, dev, "cu_add"), _buf(slot_map, i64, 0, dev, "slot_map"), wp, wn,
+        _stream_on(stream, dev))
+    if st:
+        raise KvError("kv_page_map", st)
 
 
 def kv_paged_write(shape: KvPagedShape, k, v, slot_map, n_rows, k_pages, v_pages, ws,
                    stream=None) -> None:
     """Rows of ``k`` and ``v`` ([n][heads per page][d], rows may lie apart) at their slots.
     ``n_rows`` (a device int64, or None): rows from there on are left out."""
-    dev, dt = _device(k, "k"), _dtypes()
-    i64, el = dt["i64"], dt["rows"].get(shape.dtype)
-    hp, d = shape.hkv // shape.tables, shape.d
-    kp, n, ks = _rows_view(k, el, hp, d, dev, "k")
-    vp, nv, vs = _rows_view(v, el, hp, d, dev, "v")
+    dev = _device(k, "k")
+    el, row, pages = _ROWS.get(shape.dtype), shape.hkv // shape.tables * shape.d, shape.num_pages
+    inner = row * shape.page
+    apart = shape.page_stride or inner
+    kp, n, ks = _rows_view(k, el, row, dev, "k")
+    vp, nv, vs = _rows_view(v, el, row, dev, "v")
     if ks != vs or n != nv:
         raise ValueError("k and v must have the same rows and row stride")
+    wp, wn = _work(ws, dev)
     st = lib().kv_paged_write(
-        ctypes.byref(shape), kp, vp, ks, _buf(slot_map, i64, n, dev, "slot_map"), n,
-        _buf(n_rows, i64, 1, dev, "n_rows"), _pool(shape, k_pages, el, dev, "k_pages"),
-        _pool(shape, v_pages, el, dev, "v_pages"), _buf(ws, None, 0, dev, "ws"), _nbytes(ws),
-        _stream_on(stream, dev))
-    _check("kv_paged_write", st)
+        ctypes.byref(shape), kp, vp, ks, _buf(slot_map, _I64, n, dev, "slot_map"), n,
+        _buf(n_rows, _I64, 1, dev, "n_rows"), _pool(k_pages, el, inner, pages, apart, dev, "k_pages"),
+        _pool(v_pages, el, inner, pages, apart, dev, "v_pages"), wp, wn, _stream_on(stream, dev))
+    if st:
+        raise KvError("kv_paged_write", st)
 
 
 def paged_decode_attn(shape: KvPagedShape, q, k_new, v_new, cu_add, slot_map, k_pages, v_pages,
                       block_table, lens, softmax_scale: float, out, ws, stream=None) -> None:
     """One decode step over the paged cache; ``k_new`` / ``v_new`` / ``cu_add`` / ``slot_map``
     None: no rows are stored."""
-    dev, dt = _device(q, "q"), _dtypes()
-    i32, i64, el = dt["i32"], dt["i64"], dt["rows"].get(shape.dtype)
-    seqs = shape.seqs
-    n, nq, nk = seqs * shape.tables, seqs * shape.hq * shape.d, seqs * shape.hkv * shape.d
+    dev = _device(q, "q")
+    el, seqs, hkv, d, tables = _ROWS.get(shape.dtype), shape.seqs, shape.hkv, shape.d, shape.tables
+    n, nq, nk, pages = seqs * tables, seqs * shape.hq * d, seqs * hkv * d, shape.num_pages
+    inner = hkv // tables * shape.page * d
+    apart = shape.page_stride or inner
+    wp, wn = _work(ws, dev)
     st = lib().paged_decode_attn(
         ctypes.byref(shape), _buf(q, el, nq, dev, "q"), _buf(k_new, el, nk, dev, "k_new"),
-        _buf(v_new, el, nk, dev, "v_new"), _buf(cu_add, i64, n + 1, dev, "cu_add"),
-        _buf(slot_map, i64, 0, dev, "slot_map"), 0 if slot_map is None else slot_map.numel(),
-        _pool(shape, k_pages, el, dev, "k_pages"), _pool(shape, v_pages, el, dev, "v_pages"),
-        _buf(block_table, i32, n * shape.max_pages, dev, "block_table"),
-        _buf(lens, i32, n, dev, "lens"), softmax_scale, _buf(out, el, nq, dev, "out"),
-        _buf(ws, None, 0, dev, "ws"), _nbytes(ws), _stream_on(stream, dev))
-    _check("paged_decode_attn", st)
+        _buf(v_new, el, nk, dev, "v_new"), _buf(cu_add, _I64, n + 1, dev, "cu_add"),
+        _buf(slot_map, _I64, 0, dev, "slot_map"), 0 if slot_map is None else slot_map.numel(),
+        _pool(k_pages, el, inner, pages, apart, dev, "k_pages"),
+        _pool(v_pages, el, inner, pages, apart, dev, "v_pages"),
+        _buf(block_table, _I32, n * shape.max_pages, dev, "block_table"),
+        _buf(lens, _I32, n, dev, "lens"), softmax_scale, _buf(out, el, nq, dev, "out"), wp, wn,
+        _stream_on(stream, dev))
+    if st:
+        raise KvError("paged_decode_attn", st)
 
 
 def kv_check_device_status(ws, stream=None) -> int:

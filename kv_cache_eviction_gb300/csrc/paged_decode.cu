@@ -35,7 +35,7 @@ constexpr int kPThreads = kPWarps * 32;
 constexpr int kMaxCtas = 320;
 constexpr int kRingBytes = 16 * 1024;   // of a warp
 // Tiles per CTA at least: a small call runs on as few CTAs as that allows.
-constexpr int kMinTiles = 8;
+constexpr int kMinTiles = 4;
 // A boundary inside a unit of at most this many tiles moves to the unit's nearer end.
 constexpr int kSnapTiles = 16;
 // Part of a unit in the workspace: max[8], sum[8], then o[G][D].
