@@ -488,7 +488,7 @@ KV_API size_t kv_paged_workspace_size(int op, const kv_paged_shape* shape);
  * num_pages pages, or takes back more pages than it has room for (nothing is then taken, or
  * returned).
  *
- * lens, add   [U] int32        lens_out [U] int32, may be lens
+ * lens, add   [U] int32        lens_out [U] int32, may be lens (not a part of it, nor of add)
  * free_ring   [num_pages] int32 in/out
  * free_state  [2] int64        free_out [2] int64, may be free_state
  * block_table [U][max_pages] int32 in/out

@@ -521,8 +521,15 @@ kv_status kv_page_map(const kv_paged_shape* shape, const int32_t* lens, const in
       !aligned_to(free_state, 8) || !aligned_to(block_table, 4) || !aligned_to(lens_out, 4) ||
       !aligned_to(free_out, 8) || !aligned_to(cu_add, 8) || !aligned_to(slot_map, 8))
     return KV_ERR_INVALID_ARG;
-  if (lens_out == add) return KV_ERR_INVALID_ARG;
   if (s.U() > KV_PAGE_MAP_MAX_TABLES) return KV_ERR_UNSUPPORTED;
+  // lens_out is lens, or apart from lens and add; free_out likewise
+  auto apart = [](const void* x, const void* y, int64_t bytes) {
+    const char *p = static_cast<const char*>(x), *q = static_cast<const char*>(y);
+    return p + bytes <= q || q + bytes <= p;
+  };
+  if (!apart(lens_out, add, s.U() * 4) || (lens_out != lens && !apart(lens_out, lens, s.U() * 4)) ||
+      (free_out != free_state && !apart(free_out, free_state, 16)))
+    return KV_ERR_INVALID_ARG;
   if (ws_bytes < kPageMapWsBytes) return KV_ERR_WORKSPACE;
   return cuda_status(launch_page_map(s, lens, add, free_ring, free_state, slot_capacity,
                                      block_table, lens_out, free_out, cu_add, slot_map,

@@ -1,40 +1,73 @@
 // Rows of K and V stored at their slots of the page pool: pool[slot / page][h][slot % page] =
-// row i's head h.  A copy: bound by reading and writing every row once.
+// row i's head h.  A copy: bound by reading and writing every row once (latency, for a few rows).
 //
-// A thread moves one 16-byte piece of a row of K and the same piece of V.
+// A warp moves groups of rows, 128 16-byte pieces of K and of V at a time: rows of up to 64
+// pieces share a group, each padded to a power of two pieces so that a lane finds its row by a
+// shift; longer rows take several groups.  The eight loads of a lane do not wait for the slots,
+// only its stores do.  WRITEFIGURES
 #include "kv_internal.cuh"
+#include "tc_ptx.cuh"
 
 namespace kv {
 namespace {
 
 constexpr int kWThreads = 256;
+constexpr int kWPieces = 4;   // pieces of K (and of V) of a lane at a time
 
-__global__ void __launch_bounds__(kWThreads)
-paged_write_kernel(const uint4* __restrict__ k, const uint4* __restrict__ v, int64_t src_vec,
-                   const int64_t* __restrict__ slots, int64_t rows,
-                   const int64_t* __restrict__ n_rows, uint4* __restrict__ kp,
-                   uint4* __restrict__ vp, int hp, int dvec, int shift, int64_t page_vec,
-                   int64_t num_pages, WsHeader* hdr) {
-  if (n_rows != nullptr) {
-    const int64_t n = *n_rows;
-    rows = n < rows ? n : rows;
-  }
-  const int per_row = hp * dvec;
-  const int64_t total = rows * per_row;
-  const int64_t step = (int64_t)gridDim.x * kWThreads;
-  for (int64_t i = (int64_t)blockIdx.x * kWThreads + threadIdx.x; i < total; i += step) {
-    const int64_t row = i / per_row;
-    const int x = (int)(i - row * per_row);
-    const int64_t slot = slots[row];
-    if (slot < 0 || slot >= (num_pages << shift)) {
-      if (slot != -1) raise_dev(hdr, DEV_PAGE_ID, (unsigned)row);
-      continue;
+struct WriteArgs {
+  const uint4 *k, *v;
+  const int64_t* slots;
+  const int64_t* n_rows;
+  uint4 *kp, *vp;
+  WsHeader* hdr;
+  int64_t rows, src_vec, page_vec, num_slots;   // *_vec: 16-byte pieces
+  int per_row, pad_shift;   // pieces of a row, and log2 of its padded pieces (7: whole groups)
+  int dvec, div_dvec;       // pieces of a head's row; x / dvec = x * div_dvec >> 20
+  int page_shift;
+};
+
+__global__ void __launch_bounds__(kWThreads) paged_write_kernel(const WriteArgs a) {
+  const int lane = threadIdx.x & 31;
+  ptx::griddep_launch_dependents();
+  ptx::griddep_wait();   // nothing of the call before is read or written until it ends
+  int64_t rows = a.rows;
+  if (a.n_rows != nullptr) rows = min(rows, *a.n_rows);
+  const int in_group = 128 >> a.pad_shift;   // rows
+  const int64_t warp = (int64_t)blockIdx.x * (kWThreads / 32) + (threadIdx.x >> 5);
+  const int64_t step = (int64_t)gridDim.x * (kWThreads / 32) * in_group;
+  const int heads_apart = ((1 << a.page_shift) - 1) * a.dvec;   // extra pieces from head to head
+  for (int64_t row0 = warp * in_group; row0 < rows; row0 += step) {
+    for (int x0 = 0; x0 < a.per_row; x0 += 128) {
+      uint4 kx[kWPieces], vx[kWPieces];
+      int64_t slot[kWPieces];
+#pragma unroll
+      for (int j = 0; j < kWPieces; ++j) {
+        const int i = lane + 32 * j;
+        const int64_t row = row0 + (i >> a.pad_shift);
+        const int x = x0 + (i & ((1 << a.pad_shift) - 1));
+        slot[j] = -1;
+        if (x < a.per_row && row < rows) {
+          slot[j] = a.slots[row];
+          kx[j] = a.k[row * a.src_vec + x];
+          vx[j] = a.v[row * a.src_vec + x];
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < kWPieces; ++j) {
+        const int i = lane + 32 * j;
+        const int x = x0 + (i & ((1 << a.pad_shift) - 1));
+        if (slot[j] >= 0 && slot[j] < a.num_slots) {
+          const int64_t page = slot[j] >> a.page_shift;
+          const int r = (int)(slot[j] & ((1 << a.page_shift) - 1));
+          const int h = x * a.div_dvec >> 20;
+          const int64_t dst = page * a.page_vec + r * a.dvec + x + h * heads_apart;
+          a.kp[dst] = kx[j];
+          a.vp[dst] = vx[j];
+        } else if (slot[j] != -1) {
+          raise_dev(a.hdr, DEV_PAGE_ID, (unsigned)(row0 + (i >> a.pad_shift)));
+        }
+      }
     }
-    const int h = x / dvec, c = x - h * dvec;
-    const int64_t page = slot >> shift, r = slot & ((1 << shift) - 1);
-    const int64_t dst = page * page_vec + (((int64_t)h << shift) + r) * dvec + c;
-    kp[dst] = k[row * src_vec + x];
-    vp[dst] = v[row * src_vec + x];
   }
 }
 }  // namespace
@@ -46,13 +79,25 @@ cudaError_t launch_paged_write(const PagedShape& s, const void* k, const void* v
   const int ve = 16 / s.esize();
   int shift = 0;
   while ((1 << shift) < s.page) ++shift;
-  const int64_t total = rows * s.Hp() * (s.d / ve);
-  int64_t grid = cdiv(total, kWThreads);
+  const int dvec = s.d / ve, per_row = s.Hp() * dvec;
+  int pad = 0;
+  while (pad < 7 && (1 << pad) < per_row) ++pad;
+  // x / dvec by a product: x < 256 * 32, and the product is too large by less than dvec / 2^20
+  // a unit, so the quotient is exact (8192 * 32 < 2^20)
+  const int div = ((1 << 20) + dvec - 1) / dvec;
+  const WriteArgs a{(const uint4*)k, (const uint4*)v, slots, n_rows, (uint4*)kp, (uint4*)vp, hdr,
+                    rows, src_stride / ve, s.page_stride / ve, s.num_pages << shift, per_row, pad,
+                    dvec, div, shift};
+  int64_t grid = cdiv(rows, (int64_t)(128 >> pad) * (kWThreads / 32));
   if (grid > (int64_t)num_sms() * 8) grid = (int64_t)num_sms() * 8;
-  paged_write_kernel<<<(unsigned)grid, kWThreads, 0, st>>>(
-      (const uint4*)k, (const uint4*)v, src_stride / ve, slots, rows, n_rows, (uint4*)kp,
-      (uint4*)vp, s.Hp(), s.d / ve, shift, s.page_stride / ve, s.num_pages, hdr);
-  const cudaError_t e = cudaGetLastError();
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3((unsigned)grid);
+  cfg.blockDim = dim3(kWThreads);
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1] = {pdl_attribute()};
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, paged_write_kernel, a);
   if (e == cudaSuccess) count_launches(1);
   return e;
 }

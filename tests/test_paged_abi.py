@@ -101,6 +101,9 @@ def test_arguments(L):
     assert call_map(L, s, cap=-1) == inv
     assert call_map(L, s, cap=(1 << 31) - 1) == inv
     assert call_map(L, s, add=P) == inv                      # lens_out over add
+    # lens_out or free_out over a part of lens or free_state
+    assert call_map(L, s, lens_out=ctypes.c_void_p(0x1008)) == inv
+    assert call_map(L, s, state_out=ctypes.c_void_p(0x0ff8)) == inv
     assert call_map(L, shape(seqs=kv.KV_PAGE_MAP_MAX_TABLES + 1)) == kv.KV_ERR_UNSUPPORTED
     for arg in ("k", "v", "slots", "kp", "vp", "ws"):
         assert call_write(L, s, **{arg: None}) == inv
