@@ -52,7 +52,6 @@ struct PagedArgs {
   WsHeader* hdr;
   uint32_t* tick;   // [k]: parts done of the unit that crosses CTA k's end
   float* part;      // two parts a CTA
-  float* far;       // a part a for each warp
   int U, Hp, G, d, shift, max_pages;
   int64_t num_pages, page_stride;
   pmma::Scale scale;
@@ -70,7 +69,6 @@ struct Cfg {
   // a copy instruction of a warp: kRows rows of kLanes 16-byte pieces
   static constexpr int kLanes = NSEG <= 2 ? NSEG * 8 : 32;
   static constexpr int kRows = 32 / kLanes;
-  static_assert(2 * 8 * Tl::D * 4 <= 2 * kHalf, "a warp's two parts fit one stage");
 };
 
 template <typename C>
@@ -80,13 +78,11 @@ struct PagedSmem {
   uint32_t strip[kPThreads];                 // tiles before thread t's tables
   int32_t lens[kPThreads];                   // rows per table, where a thread has one table
   uint32_t wsum[kPWarps];
-  // the parts warp w leaves in one of its stages (at byte `at`): of a unit that began before
-  // its tiles (a), of one that goes on after them (b); unit or -1, and whether the unit of
-  // part a goes on as well
-  float ml[kPWarps][2][16];                  // max[8], sum[8] of parts a and b
-  int32_t at[kPWarps];
+  // the parts warp w leaves: of a unit that began before its tiles (a), of one that goes on
+  // after them (b); unit or -1, and whether the unit of part a goes on as well
+  float part[kPWarps][2][8 * C::Tl::D];      // outputs of parts a and b, [query][column]
+  float ml[kPWarps][2][16];                  // max[8], sum[8]
   int32_t a_unit[kPWarps], b_unit[kPWarps], a_open[kPWarps];
-  int32_t far[kPWarps];                      // part a is in the workspace
   int32_t some[kPWarps];                     // warp w has tiles
   uint2 ends[kPWarps][2];                    // first tile and end of the units of warp w's
                                              // first and last tiles
@@ -447,7 +443,7 @@ paged_decode_kernel(const __grid_constant__ PagedArgs a) {
     }
   };
   int32_t unit_a = -1, unit_b = -1;
-  bool open_a = false, far = false;
+  bool open_a = false;
   if (count > 0) {
     find(xs);
     describe(xs);
@@ -553,35 +549,29 @@ paged_decode_kernel(const __grid_constant__ PagedArgs a) {
             if (8 * t < d) store2(dst + 8 * t, att.o[t][0] * inv, att.o[t][1] * inv);
         }
       } else {
-        // A part of the unit.  Its place is the stage that the warp reads last; a part a that
-        // ends before the warp's tiles do waits in the workspace.
+        // a part of the unit
         if (whole) {
           unit_b = unit;
         } else {
           unit_a = unit;
           open_a = !last;
-          far = i < count - 1;
         }
         if (col == 0) {
           sm.ml[warp][whole][g] = att.m;
           sm.ml[warp][whole][8 + g] = att.l;
         }
-        float* dst = far && !whole
-            ? a.far + (int64_t)(c * kPWarps + warp) * 8 * 128
-            : reinterpret_cast<float*>(ring + s * 2 * C::kHalf) + (whole ? 8 * D : 0);
+        float* dst = sm.part[warp][whole];
 #pragma unroll
         for (int t = 0; t < NT; ++t)
           *reinterpret_cast<float2*>(dst + g * D + 8 * t + col) =
               make_float2(att.o[t][0], att.o[t][1]);
       }
     }
-    if (i < count - 1 && ++s == S) s = 0;
+    if (++s == S) s = 0;
   }
 
   // ---- 3. what the warps leave
   if (lane == 0) {
-    sm.at[warp] = s * 2 * C::kHalf;
-    sm.far[warp] = far ? 1 : 0;
     sm.a_unit[warp] = unit_a;
     sm.a_open[warp] = open_a ? 1 : 0;
     sm.b_unit[warp] = unit_b;
@@ -623,13 +613,8 @@ paged_decode_kernel(const __grid_constant__ PagedArgs a) {
         const bool b = i == k + 1, in = b || (mem >> k & 1) || (i == 0 && k == 0);
         m[k] = in ? sm.ml[k][b][g] : -INFINITY;
         l[k] = in ? sm.ml[k][b][8 + g] : 0.f;
-        o[k] = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (in && !b && sm.far[k])
-          o[k] = __ldcg(reinterpret_cast<const float4*>(
-              a.far + (int64_t)(c * kPWarps + k) * 8 * 128 + g * D + col));
-        else if (in)
-          o[k] = *reinterpret_cast<const float4*>(sm.ring[k] + sm.at[k] +
-                                                  ((b ? 8 * D : 0) + g * D + col) * 4);
+        o[k] = in ? *reinterpret_cast<const float4*>(&sm.part[k][b][g * D + col])
+                  : make_float4(0.f, 0.f, 0.f, 0.f);
       }
       float M = -INFINITY, L = 0.f;
       float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -709,15 +694,14 @@ paged_decode_kernel(const __grid_constant__ PagedArgs a) {
         merge_parts<kB>(m, l, o, M, L, acc);
       }
       if (groups > 1) {
-        // (in the stage that held the warp's parts)
-        float* mine = reinterpret_cast<float*>(ring + sm.at[warp]) + lane * 8;
+        // (where the warp's parts were)
+        float* mine = sm.part[warp][0] + lane * 8;
         *reinterpret_cast<float4*>(mine) = acc;
         *reinterpret_cast<float2*>(mine + 4) = make_float2(M, L);
         __syncthreads();
         for (int k = 1; grp == 0 && k < groups; ++k) {
           const int t = tid + k * nsl;
-          const float* p = reinterpret_cast<const float*>(sm.ring[t >> 5] + sm.at[t >> 5]) +
-                           (t & 31) * 8;
+          const float* p = sm.part[t >> 5][0] + (t & 31) * 8;
           const float m[1] = {p[4]}, l[1] = {p[5]};
           const float4 o[1] = {*reinterpret_cast<const float4*>(p)};
           merge_parts<1>(m, l, o, M, L, acc);
@@ -770,8 +754,7 @@ cudaError_t launch_t(const PagedShape& s, const PagedArgs& a, cudaStream_t st) {
 }  // namespace
 
 size_t paged_decode_ws_bytes(const PagedShape&) {
-  return kWsHeader + kTickBytes + (size_t)2 * kMaxCtas * kPartFloats * sizeof(float) +
-         (size_t)kMaxCtas * kPWarps * 8 * 128 * sizeof(float);
+  return kWsHeader + kTickBytes + (size_t)2 * kMaxCtas * kPartFloats * sizeof(float);
 }
 
 cudaError_t launch_paged_decode(const PagedShape& s, const void* q, const void* kn, const void* vn,
@@ -785,8 +768,6 @@ cudaError_t launch_paged_decode(const PagedShape& s, const void* q, const void* 
   const PagedArgs a{q, kn, vn, cu, slots, slot_capacity, kp, vp, table, lens, out,
                     reinterpret_cast<WsHeader*>(ws), reinterpret_cast<uint32_t*>(ws + kWsHeader),
                     reinterpret_cast<float*>(ws + kWsHeader + kTickBytes),
-                    reinterpret_cast<float*>(ws + kWsHeader + kTickBytes) +
-                        (size_t)2 * kMaxCtas * kPartFloats,
                     (int)s.U(), s.Hp(),
                     s.G(), s.d, shift, s.max_pages, s.num_pages, s.page_stride,
                     pmma::Scale{c2 > FLT_MIN ? c2 : FLT_MIN, flip}};
