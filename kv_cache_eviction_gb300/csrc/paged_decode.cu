@@ -75,12 +75,13 @@ template <typename C>
 struct PagedSmem {
   unsigned char ring[kPWarps][kRingBytes];
   unsigned char side[kPWarps][C::kSide];
+  float4 part4[kPWarps][2][2 * C::Tl::D];    // outputs of the warps' parts a and b (see below),
+                                             // [query][column]
   uint32_t strip[kPThreads];                 // tiles before thread t's tables
   int32_t lens[kPThreads];                   // rows per table, where a thread has one table
   uint32_t wsum[kPWarps];
   // the parts warp w leaves: of a unit that began before its tiles (a), of one that goes on
   // after them (b); unit or -1, and whether the unit of part a goes on as well
-  float part[kPWarps][2][8 * C::Tl::D];      // outputs of parts a and b, [query][column]
   float ml[kPWarps][2][16];                  // max[8], sum[8]
   int32_t a_unit[kPWarps], b_unit[kPWarps], a_open[kPWarps];
   int32_t some[kPWarps];                     // warp w has tiles
@@ -461,8 +462,6 @@ paged_decode_kernel(const __grid_constant__ PagedArgs a) {
     cp_async_commit();
   }
   if (count > 32) describe(xs + 32);
-  uint32_t qw[Tl::NQ];
-  int32_t q_unit = -1;   // unit whose q words qw holds
   bool whole = false;    // the warp has the unit from its first tile on
   int s = 0;             // stage of tile i
   uint32_t firsts = 0, lasts = 0, cuts = 0;   // cur's tiles: units' first, last; not all rows
@@ -482,16 +481,11 @@ paged_decode_kernel(const __grid_constant__ PagedArgs a) {
     const bool last = lasts >> src & 1;
     if (i == 0 || (firsts >> src & 1)) {
       const int32_t unit = __shfl_sync(0xffffffffu, cur.unit, src);
-      if (q_unit != unit) Tl::load_q(qp + (int64_t)unit * G * d, G, d, qw);
+      uint32_t qw[Tl::NQ];
+      Tl::load_q(qp + (int64_t)unit * G * d, G, d, qw);
       att.set_q(qw, a.scale);
       att.begin();
       whole = firsts >> src & 1;
-      // the next unit's q, while this one streams
-      q_unit = -1;
-      if (unit + 1 < a.U * a.Hp && i + 1 < count) {
-        q_unit = unit + 1;
-        Tl::load_q(qp + (int64_t)q_unit * G * d, G, d, qw);
-      }
     }
     cp_async_wait<S - 1>();
     __syncwarp();
@@ -560,7 +554,7 @@ paged_decode_kernel(const __grid_constant__ PagedArgs a) {
           sm.ml[warp][whole][g] = att.m;
           sm.ml[warp][whole][8 + g] = att.l;
         }
-        float* dst = sm.part[warp][whole];
+        float* dst = reinterpret_cast<float*>(sm.part4[warp][whole]);
 #pragma unroll
         for (int t = 0; t < NT; ++t)
           *reinterpret_cast<float2*>(dst + g * D + 8 * t + col) =
@@ -613,7 +607,7 @@ paged_decode_kernel(const __grid_constant__ PagedArgs a) {
         const bool b = i == k + 1, in = b || (mem >> k & 1) || (i == 0 && k == 0);
         m[k] = in ? sm.ml[k][b][g] : -INFINITY;
         l[k] = in ? sm.ml[k][b][8 + g] : 0.f;
-        o[k] = in ? *reinterpret_cast<const float4*>(&sm.part[k][b][g * D + col])
+        o[k] = in ? sm.part4[k][b][(g * D + col) / 4]
                   : make_float4(0.f, 0.f, 0.f, 0.f);
       }
       float M = -INFINITY, L = 0.f;
@@ -695,15 +689,14 @@ paged_decode_kernel(const __grid_constant__ PagedArgs a) {
       }
       if (groups > 1) {
         // (where the warp's parts were)
-        float* mine = sm.part[warp][0] + lane * 8;
-        *reinterpret_cast<float4*>(mine) = acc;
-        *reinterpret_cast<float2*>(mine + 4) = make_float2(M, L);
+        sm.part4[warp][0][2 * lane] = acc;
+        sm.part4[warp][0][2 * lane + 1] = make_float4(M, L, 0.f, 0.f);
         __syncthreads();
         for (int k = 1; grp == 0 && k < groups; ++k) {
           const int t = tid + k * nsl;
-          const float* p = sm.part[t >> 5][0] + (t & 31) * 8;
-          const float m[1] = {p[4]}, l[1] = {p[5]};
-          const float4 o[1] = {*reinterpret_cast<const float4*>(p)};
+          const float4* p = sm.part4[t >> 5][0] + 2 * (t & 31);
+          const float m[1] = {p[1].x}, l[1] = {p[1].y};
+          const float4 o[1] = {p[0]};
           merge_parts<1>(m, l, o, M, L, acc);
         }
         __syncthreads();

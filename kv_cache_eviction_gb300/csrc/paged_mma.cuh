@@ -243,24 +243,27 @@ struct Tile<float, NSEG> : State<NSEG * 4> {
   __device__ __forceinline__ void tile(uint32_t ks, uint32_t vs, uint32_t mask, float c2) {
     constexpr int NB = RT / 8;
     const int lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
-    // scores: the high and the low parts of k in sums of their own
+    // scores: the high and the low parts of k, even and odd k-steps in sums of their own
     float z[NB][2], mt = -INFINITY;
     const uint32_t ka = ks + g * 128 + (g << 4) + 4 * c;
 #pragma unroll
     for (int j = 0; j < NB; ++j) {
-      float s[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+      float s[4][4];
+#pragma unroll
+      for (int i = 0; i < 16; ++i) s[i >> 2][i & 3] = 0.f;
 #pragma unroll
       for (int k = 0; k < NT; ++k) {
         const uint32_t at = (k >> 2) * (RT * 128) + j * 1024;
         uint32_t h0, l0, h1, l1;
         tf32_split(lds_f((ka ^ ((2 * k & 7) << 4)) + at), h0, l0);
         tf32_split(lds_f((ka ^ ((2 * k + 1 & 7) << 4)) + at), h1, l1);
-        mma_tf32_1688(s[0], qh[2 * k], ql[2 * k], qh[2 * k + 1], ql[2 * k + 1], h0, h1);
-        mma_tf32_1688(s[1], qh[2 * k], ql[2 * k], qh[2 * k + 1], ql[2 * k + 1], l0, l1);
+        mma_tf32_1688(s[k & 1], qh[2 * k], ql[2 * k], qh[2 * k + 1], ql[2 * k + 1], h0, h1);
+        mma_tf32_1688(s[2 + (k & 1)], qh[2 * k], ql[2 * k], qh[2 * k + 1], ql[2 * k + 1], l0, l1);
       }
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        z[j][e] = (s[0][e] + s[0][2 + e]) + (s[1][e] + s[1][2 + e]);
+        z[j][e] = ((s[0][e] + s[1][e]) + (s[0][2 + e] + s[1][2 + e])) +
+                  ((s[2][e] + s[3][e]) + (s[2][2 + e] + s[3][2 + e]));
         if (mask != (1u << RT) - 1u && !(mask >> (8 * j + 2 * c + e) & 1)) z[j][e] = -INFINITY;
         mt = fmaxf(mt, z[j][e]);
       }
