@@ -23,6 +23,7 @@
 // are -inf and their values zeros.  No CTA waits for another.
 #include <cfloat>
 #include <cmath>
+#include <type_traits>
 
 #include "paged_mma.cuh"
 
@@ -669,9 +670,9 @@ paged_decode_kernel(const __grid_constant__ PagedArgs a) {
       const bool in_part = grp < groups && idx < nsl;
       float M = -INFINITY, L = 0.f;
       float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-      constexpr int kB = 8;   // parts per round of loads
-#pragma unroll 1
-      for (int k0 = grp; in_part && k0 < parts[y]; k0 += kB * groups) {
+      // a round of loads: as many parts as there are, or 16
+      auto take = [&](int k0, auto parts_at_once) {
+        constexpr int kB = decltype(parts_at_once)::value;
         float m[kB], l[kB];
         float4 o[kB];
 #pragma unroll
@@ -686,6 +687,13 @@ paged_decode_kernel(const __grid_constant__ PagedArgs a) {
                     : make_float4(0.f, 0.f, 0.f, 0.f);
         }
         merge_parts<kB>(m, l, o, M, L, acc);
+      };
+      if (in_part && parts[y] <= 8 * groups) {
+        take(grp, std::integral_constant<int, 8>());
+      } else if (in_part) {
+#pragma unroll 1
+        for (int k0 = grp; k0 < parts[y]; k0 += 16 * groups)
+          take(k0, std::integral_constant<int, 16>());
       }
       if (groups > 1) {
         // (where the warp's parts were)

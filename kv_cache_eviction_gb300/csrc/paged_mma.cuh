@@ -33,8 +33,7 @@ namespace pmma {
 __device__ __forceinline__ void mma_bf16_16816(float (&d)[4], uint32_t a0, uint32_t a1,
                                                uint32_t a2, uint32_t a3, uint32_t b0,
                                                uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
       "{%8,%9}, {%0,%1,%2,%3};"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
@@ -42,8 +41,7 @@ __device__ __forceinline__ void mma_bf16_16816(float (&d)[4], uint32_t a0, uint3
 __device__ __forceinline__ void mma_tf32_1688(float (&d)[4], uint32_t a0, uint32_t a1,
                                               uint32_t a2, uint32_t a3, uint32_t b0,
                                               uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+  asm("mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
       "{%8,%9}, {%0,%1,%2,%3};"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
@@ -174,16 +172,25 @@ struct Tile<__nv_bfloat16, NSEG> : State<NSEG * 8> {
 #pragma unroll
       for (int e = 0; e < 4; ++e) s[j][0][e] = s[j][1][e] = 0.f;
     const uint32_t ka = ks + (lane & 7) * 128 + (((lane >> 3) ^ (lane & 7)) << 4);
+    // (all loads first: their latency once, not once a step)
+    uint32_t b[2 * NSEG][2][4];
 #pragma unroll
-    for (int kk = 0; kk < 2 * NSEG; ++kk) {
+    for (int kk = 0; kk < 2 * NSEG; ++kk)
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+        ldsm4(b[kk][j], (ka ^ ((kk & 1) * 64)) + (kk >> 1) * (RT * 128) + j * 1024);
+#pragma unroll
+    for (int kk = 0; kk < 2 * NSEG; ++kk)
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
-        uint32_t b[4];
-        ldsm4(b, (ka ^ ((kk & 1) * 64)) + (kk >> 1) * (RT * 128) + j * 1024);
-        mma_bf16_16816(s[j][0], q[4 * kk], 0u, q[4 * kk + 1], 0u, b[0], b[1]);
-        mma_bf16_16816(s[j][1], q[4 * kk + 2], 0u, q[4 * kk + 3], 0u, b[2], b[3]);
+        mma_bf16_16816(s[j][0], q[4 * kk], 0u, q[4 * kk + 1], 0u, b[kk][j][0], b[kk][j][1]);
+        mma_bf16_16816(s[j][1], q[4 * kk + 2], 0u, q[4 * kk + 3], 0u, b[kk][j][2], b[kk][j][3]);
       }
-    }
+    // V too, while the softmax is worked out
+    const uint32_t va = vs + (lane & 15) * 128 + (((lane >> 4) ^ (lane & 7)) << 4);
+    uint32_t v[NT / 2][4];
+#pragma unroll
+    for (int t = 0; t < NT; t += 2) ldsm4_t(v[t / 2], (va ^ ((t & 6) * 16)) + (t >> 3) * (RT * 128));
     float z[2][2];
 #pragma unroll
     for (int j = 0; j < 2; ++j)
@@ -207,13 +214,10 @@ struct Tile<__nv_bfloat16, NSEG> : State<NSEG * 8> {
       lo[j] = bf16x2_of(p0 - __uint_as_float(hi[j] << 16),
                         p1 - __uint_as_float(hi[j] & 0xFFFF0000u));
     }
-    const uint32_t va = vs + (lane & 15) * 128 + (((lane >> 4) ^ (lane & 7)) << 4);
 #pragma unroll
     for (int t = 0; t < NT; t += 2) {
-      uint32_t b[4];
-      ldsm4_t(b, (va ^ ((t & 6) * 16)) + (t >> 3) * (RT * 128));
-      mma_bf16_16816(this->o[t], hi[0], lo[0], hi[1], lo[1], b[0], b[1]);
-      mma_bf16_16816(this->o[t + 1], hi[0], lo[0], hi[1], lo[1], b[2], b[3]);
+      mma_bf16_16816(this->o[t], hi[0], lo[0], hi[1], lo[1], v[t / 2][0], v[t / 2][1]);
+      mma_bf16_16816(this->o[t + 1], hi[0], lo[0], hi[1], lo[1], v[t / 2][2], v[t / 2][3]);
     }
   }
 };
@@ -251,12 +255,16 @@ struct Tile<float, NSEG> : State<NSEG * 4> {
       float s[4][4];
 #pragma unroll
       for (int i = 0; i < 16; ++i) s[i >> 2][i & 3] = 0.f;
+      // (all loads first: their latency once, not once a step)
+      float x[2 * NT];
+#pragma unroll
+      for (int k = 0; k < 2 * NT; ++k)
+        x[k] = lds_f((ka ^ ((k & 7) << 4)) + (k >> 3) * (RT * 128) + j * 1024);
 #pragma unroll
       for (int k = 0; k < NT; ++k) {
-        const uint32_t at = (k >> 2) * (RT * 128) + j * 1024;
         uint32_t h0, l0, h1, l1;
-        tf32_split(lds_f((ka ^ ((2 * k & 7) << 4)) + at), h0, l0);
-        tf32_split(lds_f((ka ^ ((2 * k + 1 & 7) << 4)) + at), h1, l1);
+        tf32_split(x[2 * k], h0, l0);
+        tf32_split(x[2 * k + 1], h1, l1);
         mma_tf32_1688(s[k & 1], qh[2 * k], ql[2 * k], qh[2 * k + 1], ql[2 * k + 1], h0, h1);
         mma_tf32_1688(s[2 + (k & 1)], qh[2 * k], ql[2 * k], qh[2 * k + 1], ql[2 * k + 1], l0, l1);
       }
@@ -280,12 +288,18 @@ struct Tile<float, NSEG> : State<NSEG * 4> {
       uint32_t h0, l0, h1, l1;
       tf32_split(p0, h0, l0);
       tf32_split(p1, h1, l1);
+      float x[2 * NT];
 #pragma unroll
       for (int t = 0; t < NT; ++t) {
-        const uint32_t x = (2 * t & 7) << 4, at = (t >> 2) * (RT * 128) + j * 1024;
+        const uint32_t at = (t >> 2) * (RT * 128) + j * 1024;
+        x[2 * t] = lds_f((v0 ^ ((2 * t & 7) << 4)) + at);
+        x[2 * t + 1] = lds_f((v1 ^ ((2 * t & 7) << 4)) + at);
+      }
+#pragma unroll
+      for (int t = 0; t < NT; ++t) {
         uint32_t vh0, vl0, vh1, vl1;
-        tf32_split(lds_f((v0 ^ x) + at), vh0, vl0);
-        tf32_split(lds_f((v1 ^ x) + at), vh1, vl1);
+        tf32_split(x[2 * t], vh0, vl0);
+        tf32_split(x[2 * t + 1], vh1, vl1);
         mma_tf32_1688(this->o[t], h0, l0, h1, l1, vh0, vh1);
         mma_tf32_1688(this->o[t], h0, l0, h1, l1, vl0, vl1);
       }
