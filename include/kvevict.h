@@ -440,8 +440,8 @@ KV_API kv_status flat_decode_attn_noalloc(const kv_shape* shape, const void* q,
  *
  * Limits: page a power of two from 8 to 256, d <= 128 (a multiple of 8), hq / hkv <= 8,
  * hkv <= 256, max_pages * page and num_pages below 2^31, a page_stride below 2^40 bytes, and
- * for kv_page_map at most KV_PAGE_MAP_MAX_TABLES tables, for paged_decode_attn
- * seqs * hkv * max_pages * page below 2^34.
+ * for kv_page_map at most KV_PAGE_MAP_MAX_TABLES tables, for paged_decode_attn at most
+ * KV_PAGED_DECODE_MAX_TABLES tables and seqs * hkv * max_pages * page below 2^34.
  * Alignment: rows (k, v, q, out, k_pages, ...) 16 bytes, strides multiples of 16 bytes, tables
  * only their element's, so that slices can be passed.
  */
@@ -456,6 +456,7 @@ typedef struct {
 } kv_paged_shape;
 
 #define KV_PAGE_MAP_MAX_TABLES 16384
+#define KV_PAGED_DECODE_MAX_TABLES (1 << 20)
 
 /* Bytes of device workspace `op` (kv_paged_op) needs for `shape` (0 for an invalid shape).
  * The same rules as kv_workspace_size: zeroed once before its first use, error word in the
@@ -535,8 +536,11 @@ KV_API kv_status kv_paged_write(const kv_paged_shape* shape, const void* k, cons
  * cu_add, slot_map, slot_capacity: as given to and written by kv_page_map
  * block_table, lens (kv_page_map's lens_out), k_pages, v_pages: the cache
  * out          [seqs][hq][d] dtype
- * Sums, the softmax and out before its rounding are float32.  The K and V rows attended to have
- * to be finite; anything may stand behind a table's last row and in pages of no table.
+ * Sums, the softmax and out before its rounding are float32 (the softmax numerators are held to
+ * 16 bits for bf16, fp32 factors to 22).  The K and V rows attended to and their scores have to
+ * be finite, fp32 below 2^127 (a NaN among them makes the outputs it reaches NaN, an infinity may);
+ * anything may stand behind a table's last row and in pages of no table.  Every result is the
+ * same in every run.
  */
 KV_API kv_status paged_decode_attn(const kv_paged_shape* shape, const void* q, const void* k_new,
                                    const void* v_new, const int64_t* cu_add,

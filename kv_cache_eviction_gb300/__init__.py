@@ -26,6 +26,7 @@ __all__ = [
     "flat_decode_attn", "kv_check_device_status", "kv_status_string", "kv_kernel_launches",
     "flat_decode_attn_noalloc",
     "KV_OP_PAGE_MAP", "KV_OP_PAGED_WRITE", "KV_OP_PAGED_DECODE", "KV_PAGE_MAP_MAX_TABLES",
+    "KV_PAGED_DECODE_MAX_TABLES",
     "KvPagedShape", "kv_paged_workspace_size", "kv_page_map", "kv_paged_write",
     "paged_decode_attn",
 ]
@@ -38,6 +39,7 @@ KV_GROUP_MEAN, KV_GROUP_MAX = 0, 1
 KV_OP_SCORE, KV_OP_ALLOCATE, KV_OP_COMPACT, KV_OP_DECODE = 0, 1, 2, 3
 KV_OP_PAGE_MAP, KV_OP_PAGED_WRITE, KV_OP_PAGED_DECODE = 4, 5, 6
 KV_PAGE_MAP_MAX_TABLES = 16384
+KV_PAGED_DECODE_MAX_TABLES = 1 << 20
 KV_TERMS_MEAN_POOLED, KV_TERMS_L2 = 0, 1
 KV_PROJ_CRIT_GQA, KV_PROJ_LAPROX = 0, 1
 

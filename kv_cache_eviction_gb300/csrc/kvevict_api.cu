@@ -587,8 +587,9 @@ kv_status paged_decode_attn(const kv_paged_shape* shape, const void* q, const vo
   if (!aligned_to(cu_add, 8) || !aligned_to(slot_map, 8) || !aligned_to(block_table, 4) ||
       !aligned_to(lens, 4))
     return KV_ERR_INVALID_ARG;
-  // the kernel counts tiles of at least 8 rows in 31 bits
-  if ((int64_t)s.seqs * s.Hkv > (((int64_t)1 << 34) - 1) / ((int64_t)s.max_pages * s.page))
+  // every CTA reads all lengths; the kernel counts tiles of at least 8 rows in 31 bits
+  if (s.U() > KV_PAGED_DECODE_MAX_TABLES ||
+      (int64_t)s.seqs * s.Hkv > (((int64_t)1 << 34) - 1) / ((int64_t)s.max_pages * s.page))
     return KV_ERR_UNSUPPORTED;
   if (ws_bytes < paged_decode_ws_bytes(s)) return KV_ERR_WORKSPACE;
   return cuda_status(launch_paged_decode(s, q, k_new, v_new, cu_add, slot_map, slot_capacity,

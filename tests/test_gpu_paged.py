@@ -466,7 +466,156 @@ def test_decode_captured_and_on_streams():
         assert kv.kv_check_device_status(w) == 0
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_decode_every_head_dim(dtype):
+    """Every head dim from 8 to 128 and every group size, over lengths around a tile's end."""
+    for i, d in enumerate(range(8, 129, 8)):
+        c = Cache(3, 2, 1 + i % 8, d, 1, 8 << (i % 6), [16 + i, 7, 40], dtype, 30 + i)
+        out, ws = c.run()
+        assert kv.kv_check_device_status(ws) == 0
+        c.check(out)
+        c.check_pools()
+
+
+def test_decode_thousands_of_tables():
+    """Far more tables than threads, most of them empty, runs of empty ones, one long."""
+    rng = np.random.default_rng(11)
+    lens = np.where(rng.random(6000) < 0.05, rng.integers(1, 60, 6000), 0)
+    lens[100:4000] = 0
+    lens[[0, 4001, 5999]] = [3, 2500, 17]
+    c = Cache(1500, 4, 2, 64, 4, 16, lens, "bf16", 12, new=rng.random(6000) < 0.5)
+    out, ws = c.run()
+    assert kv.kv_check_device_status(ws) == 0
+    c.check(out)
+    c.check_pools()
+    assert torch.equal(out, c.run(ws=ws)[0])
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_decode_nan_in_a_row_that_counts(dtype):
+    """A NaN in K or V of a row that counts reaches its head's outputs, and no other's."""
+    for name, long in (("kp", 40), ("vp", 40), ("kp", 3000), ("vp", 3000)):
+        c = Cache(3, 2, 4, 64, 1, 16, [30, long, 50], dtype, 13)
+        pool = getattr(c, name)
+        pool[int(c.table_host[1, 1]), 1, 3, 5] = float("nan")
+        out, ws = c.run()
+        hit = torch.isnan(out.float())
+        assert bool(hit[1, 4:, 5 if name == "vp" else slice(None)].all())
+        assert not bool(hit[1, :4].any()) and not bool(hit[[0, 2]].any())
+        if name == "vp":
+            assert int(hit.sum()) == 4
+
+
+def test_binding_refuses_wrong_tensors():
+    """Types, sizes and strides that the calls cannot take are refused before anything runs."""
+    c = Cache(2, 2, 2, 64, 1, 16, [20, 30], "bf16", 14)
+    ws = workspace(kv.KV_OP_PAGED_DECODE, c.shape)
+    out = torch.empty_like(c.qd)
+
+    def decode(**kw):
+        x = dict(q=c.qd, k_new=c.knd, v_new=c.vnd, cu_add=c.cu, slot_map=c.slots, k_pages=c.kp,
+                 v_pages=c.vp, block_table=c.table, lens=c.lens_t, softmax_scale=0.1, out=out,
+                 ws=ws)
+        x.update(kw)
+        kv.paged_decode_attn(c.shape, **x)
+
+    decode()
+    for kw in (dict(q=c.qd.float()), dict(q=c.qd[:1]), dict(lens=c.lens_t.long()),
+               dict(cu_add=c.cu[:2]), dict(block_table=c.table.t().contiguous().t()),
+               dict(k_pages=c.kp[:-1]), dict(k_pages=c.kp.transpose(1, 2)),
+               dict(v_pages=c.vp.float()), dict(out=out.cpu()), dict(slot_map=c.slots.int()),
+               dict(k_new=c.knd.transpose(0, 1))):
+        with pytest.raises(ValueError):
+            decode(**kw)
+    with pytest.raises(kv.KvError):
+        decode(ws=ws[:1024])
+    with pytest.raises(kv.KvError):
+        decode(k_new=None)
+    wsw = workspace(kv.KV_OP_PAGED_WRITE, c.shape)
+    rows = torch.zeros(5, 2, 64, dtype=torch.bfloat16, device="cuda")
+    slots = torch.zeros(5, dtype=torch.int64, device="cuda")
+    for k, v, sl in ((rows[:, :1], rows, slots), (rows.float(), rows, slots), (rows, rows, slots[:4]),
+                     (rows, rows[:4], slots), (rows.transpose(1, 2), rows, slots),
+                     (rows[::2], rows[:3], slots), (rows, rows, slots.int())):
+        with pytest.raises(ValueError):
+            kv.kv_paged_write(c.shape, k, v, sl, None, c.kp, c.vp, wsw)
+    m = fitting(4, 1, 16, 3, "one")
+    wm = workspace(kv.KV_OP_PAGE_MAP, m.shape)
+    i32, i64 = torch.int32, torch.int64
+    good = dict(lens=dev(m.lens, i32), add=dev(m.add, i32), free_ring=dev(m.ring, i32),
+                free_state=dev(m.state, i64), block_table=dev(m.table, i32),
+                lens_out=dev(m.lens, i32), free_out=dev(m.state, i64),
+                cu_add=dev(np.zeros(5), i64), slot_map=dev(m.slots, i64))
+    kv.kv_page_map(m.shape, ws=wm, **good)
+    for kw in (dict(lens=dev(m.lens, i64)), dict(add=dev(m.add[:3], i32)),
+               dict(free_ring=dev(m.ring[:-1], i32)), dict(block_table=dev(m.table[:3], i32)),
+               dict(cu_add=dev(np.zeros(4), i64)), dict(slot_map=dev(m.slots, i32))):
+        with pytest.raises(ValueError):
+            kv.kv_page_map(m.shape, ws=wm, **{**good, **kw})
+
+
 # ------------------------------------------------------------------------------- together
+
+def test_captured_serving_step():
+    """One decode step -- tables and lengths in place, then attention that stores the new rows --
+    captured once and replayed for 40 tokens without a host round trip: outputs of the last step
+    against 64 bits over every row the replays stored."""
+    seqs, hkv, G, d, page, steps = 5, 2, 4, 64, 8, 40
+    c = Cache(seqs, hkv, G, d, 1, page, [1, 30, 8, 15, 100], "f32", 15, new=[0] * seqs)
+    cols = ceil_div(100 + steps, page)
+    num = c.num_pages + seqs * ceil_div(steps, page) + 5
+    s = kv.KvPagedShape.of(seqs, hkv * G, hkv, d, 1, page, cols, "f32", num)
+    i32, i64 = torch.int32, torch.int64
+    table = torch.full((seqs, cols), -1, dtype=i32, device="cuda")
+    table[:, :c.max_pages] = c.table
+    kp = torch.full((num, hkv, page, d), float("nan"), device="cuda")
+    vp = kp.clone()
+    kp[:c.num_pages], vp[:c.num_pages] = c.kp, c.vp
+    used = {int(c.table_host[u, j]) for u in range(seqs) for j in range(ceil_div(c.lens[u], page))}
+    free = [p for p in range(num) if p not in used]
+    ring = dev(free + [-1] * (num - len(free)), i32)
+    state = dev([0, len(free)], i64)
+    lens, one = c.lens_t.clone(), torch.ones(seqs, dtype=i32, device="cuda")
+    cu = torch.zeros(seqs + 1, dtype=i64, device="cuda")
+    slots = torch.full((seqs,), -1, dtype=i64, device="cuda")
+    ws = [workspace(op, s) for op in (kv.KV_OP_PAGE_MAP, kv.KV_OP_PAGED_DECODE)]
+    gen = torch.Generator(device="cuda").manual_seed(2)
+    tokens = [torch.randn(3, steps, seqs, hkv * G, d, generator=gen, device="cuda")]
+    q = torch.empty(seqs, hkv * G, d, device="cuda")
+    kn, vn = (torch.empty(seqs, hkv, d, device="cuda") for _ in range(2))
+    out = torch.empty_like(q)
+
+    def step():
+        kv.kv_page_map(s, lens, one, ring, state, table, lens, state, cu, slots, ws[0])
+        kv.paged_decode_attn(s, q, kn, vn, cu, slots, kp, vp, table, lens, c.scale, out, ws[1])
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    g = torch.cuda.CUDAGraph()
+    saved = lens.clone(), state.clone(), table.clone()
+    q.zero_(), kn.zero_(), vn.zero_()
+    step()                                   # (the one-time set-up of the kernels)
+    torch.cuda.synchronize()
+    for x, y in zip((lens, state, table), saved):
+        x.copy_(y)
+    with torch.cuda.graph(g, stream=side):
+        step()
+    for t in range(steps):
+        q.copy_(tokens[0][0, t])
+        kn.copy_(tokens[0][1, t, :, :hkv])
+        vn.copy_(tokens[0][2, t, :, :hkv])
+        g.replay()
+    torch.cuda.synchronize()
+    for w in ws:
+        assert kv.kv_check_device_status(w) == 0
+    assert lens.tolist() == [n + steps for n in c.lens]
+    for name, i in (("k", 1), ("v", 2)):
+        fresh = tokens[0][i, :, :, :hkv].cpu()            # [steps][seqs][hkv][d]
+        c.rows[name] = [torch.cat([r, fresh[:, u].transpose(0, 1)], 1)
+                        for u, r in enumerate(c.rows[name])]
+    c.q = tokens[0][0, steps - 1].cpu()
+    c.lens = lens.tolist()
+    c.check(out)
 
 def test_eviction_into_pages_and_decode():
     """Scores, budgets and compaction of an evicted prefix, its rows into a paged cache with a

@@ -76,6 +76,14 @@ def test_decode_counts_its_tiles_in_31_bits(L):
     assert call_decode(L, shape(seqs=1 << 11, max_pages=1 << 16)) == kv.KV_ERR_UNSUPPORTED
 
 
+def test_decode_table_limit(L):
+    s = shape(seqs=kv.KV_PAGED_DECODE_MAX_TABLES, max_pages=1, page=8, hkv=1, hq=1)
+    n = kv.kv_paged_workspace_size(kv.KV_OP_PAGED_DECODE, s)
+    assert call_decode(L, s, n=n - 1) == kv.KV_ERR_WORKSPACE
+    s = shape(seqs=kv.KV_PAGED_DECODE_MAX_TABLES + 1, max_pages=1, page=8, hkv=1, hq=1)
+    assert call_decode(L, s) == kv.KV_ERR_UNSUPPORTED
+
+
 def test_workspace_sizes(L):
     for op in OPS:
         n = kv.kv_paged_workspace_size(op, shape())
