@@ -316,7 +316,8 @@ def _init_torch() -> None:
     _ROWS.update({KV_BF16: torch.bfloat16, KV_F32: torch.float32})
     _stream_now = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
         lambda dev: torch.cuda.current_stream(dev).cuda_stream)
-    _device_now = torch.cuda.current_device
+    torch.cuda.init()   # (current_device() would ask for it on every call)
+    _device_now = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 
 
 def _device(t, what: str) -> int:
@@ -349,7 +350,9 @@ def _buf(t, dtype, count: int, dev: int, what: str) -> Optional[int]:
 
 def _work(ws, dev: int):
     """Pointer and bytes of a workspace (of any type)."""
-    return _buf(ws, ws.dtype, 0, dev, "ws"), ws.numel() * ws.element_size()
+    if ws.get_device() != dev or not ws.is_contiguous():
+        raise ValueError("ws must be contiguous on the current CUDA device")
+    return ws.data_ptr(), ws.nbytes
 
 
 def _rows_view(t, dtype, row: int, dev: int, what: str):
