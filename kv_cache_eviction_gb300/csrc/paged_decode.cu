@@ -49,9 +49,10 @@ constexpr int kRingBytes = 16 * 1024;   // of a warp
 // sequence of 500 rows 8.2 us; with two 8.9, with four 11.2.
 constexpr int kMinTiles = 4;
 // A boundary inside a unit of at most this many tiles moves to the unit's nearer end: a part in
-// the workspace and a ticket cost 2 us, 16 tiles less than that.  (8 tiles: 14.5 against 14.1 us
-// on 256 heads of 128 rows; 32: level.)
-constexpr int kSnapTiles = 16;
+// the workspace and a ticket cost 2 us, the tiles less than that.  16 / 24 / 32 tiles: 11.1 /
+// 10.9 / 10.3 us on 256 heads of 128 rows, 11.5 / 11.0 / 12.0 on skewed ones, and one sequence of
+// 500 rows (32 tiles a head) 8.1 / 8.1 / 10.5.
+constexpr int kSnapTiles = 24;
 // Part of a unit in the workspace: max[8], sum[8], then o[G][D].
 constexpr int kPartHead = 16;
 constexpr int kPartFloats = kPartHead + 8 * 128;
@@ -94,6 +95,7 @@ struct PagedSmem {
   uint32_t strip[kPThreads];                 // tiles before thread t's tables
   int32_t lens[kPThreads];                   // rows per table, where a thread has one table
   uint32_t wsum[kPWarps];
+  uint32_t bnd[2];                           // the CTA's first tile and its end
   // the parts warp w leaves: of a unit that began before its tiles (a), of one that goes on
   // after them (b); unit or -1, and whether the unit of part a goes on as well
   float ml[kPWarps][2][16];                  // max[8], sum[8]
@@ -325,7 +327,21 @@ paged_decode_kernel(const __grid_constant__ PagedArgs a) {
   auto cta_of = [&](uint32_t x) {
     return (int)((((uint64_t)x + 1) * Ne + total - 1) / total) - 1;
   };
-  const uint32_t b0 = bound(c), span = bound(c + 1) - b0;
+  // the CTA's ends: with few tables every warp finds both, else two warps find one each
+  uint32_t b0 = 0, b1 = 0;
+#pragma unroll 1
+  for (int e = 0; e < 2; ++e) {
+    if (!few && warp != e) continue;
+    b1 = bound(c + e);
+    if (e == 0) b0 = b1;
+    if (!few && lane == 0) sm.bnd[e] = b1;
+  }
+  if (!few) {
+    __syncthreads();
+    b0 = sm.bnd[0];
+    b1 = sm.bnd[1];
+  }
+  const uint32_t span = b1 - b0;
   if (span == 0) return;   // uniform in the CTA
   // (rounded up: warp 0 has the CTA's first tile)
   const uint32_t xs = b0 + (uint32_t)(((uint64_t)span * warp + kPWarps - 1) / kPWarps);
