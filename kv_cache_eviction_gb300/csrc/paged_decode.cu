@@ -38,11 +38,17 @@ namespace {
 
 // Eight warps per SM, 128 KB of copies in flight: enough for the memory, and the SMs share it
 // evenly.  With 24 KB a warp (192 KB per SM) some SMs finish a fifth before others: 622 us
-// against 603 on the 4.2 GB cache.  Six warps per SM 610.  One CTA of eight warps instead of two
-// of four: 617 (85 against 87 on one sequence of 131000 rows, whose units cross fewer CTAs).
-constexpr int kPWarps = 4;
-constexpr int kCtasPerSm = 2;
-constexpr int kPThreads = kPWarps * 32;
+// against 603 on the 4.2 GB cache.  Six warps per SM 610.
+//
+// They are two CTAs of four warps or one of eight.  Two even out ragged calls better; one makes
+// half as many parts of a unit to be merged through the workspace, which counts where few units
+// are cut many times.  CTAs of 4 / 8 warps, us: one sequence of 8192 rows 15.5 / 13.1, of
+// 32768 31.6 / 29.7, of 131000 86.8 / 84.5, fp32 5 x 3001 rows of 2 heads 16.0 / 15.2; 64 ragged
+// sequences 84.6 / 86.0, 256 heads of 128 rows 10.9 / 11.1, one sequence of 500 rows 8.1 / 8.5.
+constexpr int kSmWarps = 8;
+// CTAs of eight warps: at most this many units, and (as far as the host knows, from the tables'
+// columns) tiles for every CTA of four.
+constexpr int kLongUnits = 38;
 constexpr int kMaxCtas = 320;
 constexpr int kRingBytes = 16 * 1024;   // of a warp
 // Tiles per CTA at least: a small call runs on as few CTAs as that allows.  One tile a warp: one
@@ -86,14 +92,14 @@ struct Cfg {
   static constexpr int kRows = 32 / kLanes;
 };
 
-template <typename C>
+template <typename C, int kPWarps>
 struct PagedSmem {
   unsigned char ring[kPWarps][kRingBytes];
   unsigned char side[kPWarps][C::kSide];
   float4 part4[kPWarps][2][2 * C::Tl::D];    // outputs of the warps' parts a and b (see below),
                                              // [query][column]
-  uint32_t strip[kPThreads];                 // tiles before thread t's tables
-  int32_t lens[kPThreads];                   // rows per table, where a thread has one table
+  uint32_t strip[kPWarps * 32];              // tiles before thread t's tables
+  int32_t lens[kPWarps * 32];                // rows per table, where a thread has one table
   uint32_t wsum[kPWarps];
   uint32_t bnd[2];                           // the CTA's first tile and its end
   // the parts warp w leaves: of a unit that began before its tiles (a), of one that goes on
@@ -220,15 +226,17 @@ __device__ __forceinline__ void merge_parts(const float (&m)[kB], const float (&
   }
 }
 
-template <typename T, int NSEG>
-__global__ void __launch_bounds__(kPThreads, kCtasPerSm)
+// kPWarps: warps of a CTA.
+template <typename T, int NSEG, int kPWarps>
+__global__ void __launch_bounds__(kPWarps * 32, kSmWarps / kPWarps)
 paged_decode_kernel(const __grid_constant__ PagedArgs a) {
+  constexpr int kPThreads = kPWarps * 32;
   using C = Cfg<T, NSEG>;
   using Tl = typename C::Tl;
   constexpr int RT = C::RT, S = C::kStages, NT = Tl::NT, D = Tl::D;
   constexpr int VE = 16 / (int)sizeof(T);   // elements of a piece
   extern __shared__ unsigned char dsm_raw[];
-  PagedSmem<C>& sm = *reinterpret_cast<PagedSmem<C>*>(
+  PagedSmem<C, kPWarps>& sm = *reinterpret_cast<PagedSmem<C, kPWarps>*>(
       (reinterpret_cast<uintptr_t>(dsm_raw) + 1023) & ~(uintptr_t)1023);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int N = (int)gridDim.x, c = (int)blockIdx.x;
@@ -752,34 +760,43 @@ paged_decode_kernel(const __grid_constant__ PagedArgs a) {
 constexpr size_t kTickBytes = 2048;
 static_assert(kMaxCtas * sizeof(uint32_t) <= kTickBytes, "tickets");
 
-template <typename T, int NSEG>
-cudaError_t launch_t(const PagedShape& s, const PagedArgs& a, cudaStream_t st) {
+template <typename T, int NSEG, int kPWarps>
+cudaError_t launch_w(const PagedShape& s, const PagedArgs& a, int64_t tiles, cudaStream_t st) {
   using C = Cfg<T, NSEG>;
-  constexpr size_t smem = sizeof(PagedSmem<C>) + 1024;
-  static_assert(kCtasPerSm * (smem + 1024) <= 228 * 1024, "CTAs per SM");
+  constexpr int per_sm = kSmWarps / kPWarps;
+  constexpr size_t smem = sizeof(PagedSmem<C, kPWarps>) + 1024;
+  static_assert(per_sm * (smem + 1024) <= 228 * 1024 && smem <= 227 * 1024, "CTAs per SM");
   static std::atomic<int> slot[kMaxDevices];
   const int ok = per_device(slot, []() {
-    return cudaFuncSetAttribute(paged_decode_kernel<T, NSEG>,
+    return cudaFuncSetAttribute(paged_decode_kernel<T, NSEG, kPWarps>,
                                 cudaFuncAttributeMaxDynamicSharedMemorySize,
                                 (int)smem) == cudaSuccess ? 1 : 0;
   });
   if (!ok) return cudaErrorInvalidConfiguration;
   // no more CTAs than the tables could ever fill
-  const int64_t tiles = (int64_t)s.seqs * s.Hkv * cdiv((int64_t)s.max_pages * s.page, C::RT);
   int64_t grid = cdiv(tiles, kMinTiles);
-  if (grid > kCtasPerSm * num_sms()) grid = kCtasPerSm * num_sms();
+  if (grid > per_sm * num_sms()) grid = per_sm * num_sms();
   if (grid > kMaxCtas) grid = kMaxCtas;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3((unsigned)grid);
-  cfg.blockDim = dim3(kPThreads);
+  cfg.blockDim = dim3(kPWarps * 32);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
   cudaLaunchAttribute attr[1] = {pdl_attribute()};
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, paged_decode_kernel<T, NSEG>, a);
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, paged_decode_kernel<T, NSEG, kPWarps>, a);
   if (e == cudaSuccess) count_launches(1);
   return e;
+}
+
+template <typename T, int NSEG>
+cudaError_t launch_t(const PagedShape& s, const PagedArgs& a, cudaStream_t st) {
+  const int64_t units = (int64_t)s.seqs * s.Hkv;
+  // tiles that the tables could hold
+  const int64_t tiles = units * cdiv((int64_t)s.max_pages * s.page, Cfg<T, NSEG>::RT);
+  const bool few_long = units <= kLongUnits && tiles >= 2 * (int64_t)num_sms() * kMinTiles;
+  return few_long ? launch_w<T, NSEG, 8>(s, a, tiles, st) : launch_w<T, NSEG, 4>(s, a, tiles, st);
 }
 }  // namespace
 
