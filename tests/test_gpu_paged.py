@@ -238,10 +238,10 @@ def test_write(dtype, rows, hkv, tables, d, page, fused, extra):
     inner = hp * page * d
     s = kv.KvPagedShape.of(1, hkv, hkv, d, tables, page, num, dtype, num,
                            inner + extra if extra else 0)
-    width = 3 * hp * d if fused else hp * d
+    width = 4 * hp * d if fused else hp * d
     src = torch.randn(2, rows, width, generator=gen, device="cuda").to(dt)
     k = src[0, :, hp * d:2 * hp * d] if fused else src[0].view(rows, hp, d)
-    v = src[1, :, 2 * hp * d:] if fused else src[1].view(rows, hp, d)
+    v = src[1, :, 2 * hp * d:3 * hp * d] if fused else src[1].view(rows, hp, d)
     slots = torch.randperm(num * page, generator=gen, device="cuda")[:rows]
     slots[torch.rand(rows, generator=gen, device="cuda") < 0.1] = -1
     for n in (None, 0, rows // 2, rows + 5, -4):
