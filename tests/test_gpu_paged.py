@@ -283,6 +283,40 @@ def test_write_bad_slots():
     assert torch.equal(flat, want)
 
 
+def test_far_slots():
+    """Slots past 2^32 rows' worth of pages in the map, and bytes past 2^32 in the pool."""
+    num, page = 1 << 25, 256
+    s = kv.KvPagedShape.of(2, 1, 1, 64, 1, page, 4, "bf16", num)
+    i32, i64 = torch.int32, torch.int64
+    ring = torch.full((num,), -1, dtype=i32, device="cuda")
+    ring[:3] = dev([num - 1, 1 << 24, num - 2], i32)
+    lens, state = dev([0, 0], i32), dev([0, 3], i64)
+    table = torch.full((2, 4), -1, dtype=i32, device="cuda")
+    cu, slots = torch.zeros(3, dtype=i64, device="cuda"), torch.zeros(300, dtype=i64, device="cuda")
+    ws = workspace(kv.KV_OP_PAGE_MAP, s)
+    kv.kv_page_map(s, lens, dev([257, 2], i32), ring, state, table, lens, state, cu, slots, ws)
+    assert kv.kv_check_device_status(ws) == 0
+    want = [(num - 1) * page + i for i in range(256)] + [(1 << 24) * page] + \
+           [(num - 2) * page, (num - 2) * page + 1]
+    assert slots[:259].tolist() == want and max(want) > 1 << 32
+
+    num, heads, d = 9000, 8, 128
+    s = kv.KvPagedShape.of(1, heads, heads, d, 1, page, num, "bf16", num)
+    kp = torch.zeros(num, heads, page, d, dtype=torch.bfloat16, device="cuda")
+    vp = torch.zeros_like(kp)
+    assert kp.numel() > 1 << 31
+    k, v = (torch.randn(4, heads, d, device="cuda").bfloat16() for _ in range(2))
+    at = [0, num * page - 1, (num - 2) * page + 5, 17 * page]
+    ws = workspace(kv.KV_OP_PAGED_WRITE, s)
+    kv.kv_paged_write(s, k, v, dev(at, i64), None, kp, vp, ws)
+    assert kv.kv_check_device_status(ws) == 0
+    for pool, rows in ((kp, k), (vp, v)):
+        for i, x in enumerate(at):
+            assert torch.equal(pool[x // page, :, x % page], rows[i])
+            pool[x // page, :, x % page] = 0
+        assert not bool(pool.any())
+
+
 # ------------------------------------------------------------------------------- decode
 
 LENS = {"one": [1], "few": [3, 1, 2], "empty": [0, 5, 0, 0, 17, 0], "none": [0, 0],
