@@ -436,7 +436,9 @@ KV_API kv_status flat_decode_attn_noalloc(const kv_shape* shape, const void* q,
  *   lens             [U] int32: rows held
  * A slot names a row of the pool: page number * page + row within the page (int64), -1 for none.
  * Table u belongs to sequence u / tables (and, with head tables, KV head u % tables).  A caller
- * with L layers in one call takes seqs = batch * layers.
+ * with L layers in one call takes seqs = batch * layers.  With seqs = 0 a call does nothing: no
+ * output is written, and the ring's state stays where it is.  Outputs do not overlap inputs,
+ * except where a call says that they may.
  *
  * Limits: page a power of two from 8 to 256, d <= 128 (a multiple of 8), hq / hkv <= 8,
  * hkv <= 256, max_pages * page and num_pages below 2^31, a page_stride below 2^40 bytes, and

@@ -373,6 +373,8 @@ def _rows_view(t, dtype, row: int, dev: int, what: str):
             step *= size[k]
         if n > 1:
             stride = strides[0]
+            if stride < row:   # (0 would mean dense rows)
+                raise ValueError("the rows of %s must not overlap" % what)
     return t.data_ptr(), n, stride
 
 

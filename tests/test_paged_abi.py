@@ -155,6 +155,21 @@ def test_binding_refuses_host_tensors(L):
         kv.paged_decode_attn(s, t[0, 0], None, None, None, None, t, t, i, i, 0.1, t[0, 0], i)
 
 
+def test_binding_refuses_rows_that_overlap():
+    """Rows a stride of 0 apart (expanded ones) are no dense rows, which 0 means to the library."""
+    import torch
+    row = torch.zeros(1, 2, 64)
+    view = lambda t: kv._rows_view(t, torch.float32, 128, -1, "k")[1:]
+    assert view(row) == (1, 128)
+    assert view(row.expand(1, 2, 64)) == (1, 128)
+    assert view(torch.zeros(5, 6, 64)[:, 2:4]) == (5, 6 * 64)
+    assert view(torch.zeros(0, 2, 64)) == (0, 128)
+    for t in (row.expand(5, 2, 64), torch.zeros(400).as_strided((3, 2, 64), (64, 64, 1)),
+              torch.zeros(5, 1, 64).expand(5, 2, 64)):
+        with pytest.raises(ValueError):
+            view(t)
+
+
 def test_reference_map_keeps_every_page():
     """Random steps of the reference: every page is either free or in exactly one table, and
     a table's slots are its rows' places."""
