@@ -50,7 +50,7 @@ constexpr int kSmWarps = 8;
 // columns) tiles for every CTA of four.
 constexpr int kLongUnits = 38;
 constexpr int kMaxCtas = 320;
-constexpr int kRingBytes = 16 * 1024;   // of a warp
+constexpr int kRingBytes = 18 * 1024;   // of a warp, at most
 // Tiles per CTA at least: a small call runs on as few CTAs as that allows.  One tile a warp: one
 // sequence of 500 rows 8.2 us; with two 8.9, with four 11.2.
 constexpr int kMinTiles = 4;
@@ -78,23 +78,24 @@ struct PagedArgs {
   pmma::Scale scale;
 };
 
-template <typename T, int NSEG>
+// H: 64-byte parts of a row.
+template <typename T, int H>
 struct Cfg {
-  using Tl = pmma::Tile<T, NSEG>;
+  using Tl = pmma::Tile<T, H>;
   static constexpr int RT = Tl::RT;
-  static constexpr int kRow = NSEG * 128;                  // bytes of a row in a stage
-  static constexpr int kHalf = RT * kRow;                  // K, then V
-  static constexpr int kStages = kRingBytes / (2 * kHalf);
+  static constexpr int kRow = H * 64;                      // bytes of a row in a stage
+  static constexpr int kStage = RT * 2 * kRow;             // of a tile, K and V
+  static constexpr int kStages = kRingBytes / kStage;
   static_assert(kStages >= 2, "ring");
   static constexpr int kSide = kStages * 2 * kRow;         // of a warp: its stages' new rows
   // a copy instruction of a warp: kRows rows of kLanes 16-byte pieces
-  static constexpr int kLanes = NSEG <= 2 ? NSEG * 8 : 32;
+  static constexpr int kLanes = H <= 2 ? 8 : H <= 4 ? 16 : 32;
   static constexpr int kRows = 32 / kLanes;
 };
 
 template <typename C, int kPWarps>
 struct PagedSmem {
-  unsigned char ring[kPWarps][kRingBytes];
+  unsigned char ring[kPWarps][C::kStages * C::kStage];
   unsigned char side[kPWarps][C::kSide];
   float4 part4[kPWarps][2][2 * C::Tl::D];    // outputs of the warps' parts a and b (see below),
                                              // [query][column]
@@ -227,11 +228,11 @@ __device__ __forceinline__ void merge_parts(const float (&m)[kB], const float (&
 }
 
 // kPWarps: warps of a CTA.
-template <typename T, int NSEG, int kPWarps>
+template <typename T, int H, int kPWarps>
 __global__ void __launch_bounds__(kPWarps * 32, kSmWarps / kPWarps)
 paged_decode_kernel(const __grid_constant__ PagedArgs a) {
   constexpr int kPThreads = kPWarps * 32;
-  using C = Cfg<T, NSEG>;
+  using C = Cfg<T, H>;
   using Tl = typename C::Tl;
   constexpr int RT = C::RT, S = C::kStages, NT = Tl::NT, D = Tl::D;
   constexpr int VE = 16 / (int)sizeof(T);   // elements of a piece
@@ -438,16 +439,17 @@ paged_decode_kernel(const __grid_constant__ PagedArgs a) {
     if (p_c1 > p_c0 && p_c1 > 0 && p_c1 <= a.slot_cap) nxt.slot = a.slots[p_c1 - 1];
   };
   // Lane src's tile of t into stage s: rows `i kRows + lr`, piece `pc` of each is this lane's.
-  // (A piece's address is xor its row's low bits, and kRows divides 8: one address per lane, xor
-  // and plus constants.)
+  // (A piece's address is xor its row's low bits, and kRows divides 8: one address per lane for K
+  // and one for V, xor and plus constants.)
   const int pc = lane % C::kLanes, lr = lane / C::kLanes;
-  const uint32_t to = ring_u + (pc >> 3) * (RT * 128) + lr * 128 + (((pc & 7) ^ lr) << 4);
+  const uint32_t to = ring_u + pmma::k_piece<RT, H>(lr, pc);
+  const uint32_t to_v = ring_u + pmma::v_piece<RT, H>(lr, pc);
   const int64_t from = (int64_t)lr * d + pc * VE;
   auto issue = [&](const Desc& t, int src, int s) {
     constexpr uint32_t kAll = (1u << RT) - 1u;
     const int64_t at = __shfl_sync(0xffffffffu, (long long)t.at, src) + from;
     const uint32_t mask = __shfl_sync(0xffffffffu, t.mask, src);
-    const uint32_t dst = to + s * 2 * C::kHalf;
+    const uint32_t dst = to + s * C::kStage, dst_v = to_v + s * C::kStage;
     const T* ks = (const T*)a.kp + at;
     const T* vs = (const T*)a.vp + at;
     // in pages of 8 rows: from a row of the first 8 to one of the second
@@ -457,19 +459,19 @@ paged_decode_kernel(const __grid_constant__ PagedArgs a) {
       if ((mask & kAll) == kAll && page >= RT) {
 #pragma unroll
         for (int i = 0; i < RT / C::kRows; ++i) {
-          const uint32_t x = (dst ^ (((i * C::kRows) & 7) << 4)) + i * C::kRows * 128;
-          cp_async16(x, ks + i * C::kRows * d);
-          cp_async16(x + C::kHalf, vs + i * C::kRows * d);
+          const uint32_t flip = ((i * C::kRows) & 7) << 4;
+          cp_async16((dst ^ flip) + i * C::kRows * 128, ks + i * C::kRows * d);
+          cp_async16((dst_v ^ flip) + i * C::kRows * 128, vs + i * C::kRows * d);
         }
       } else {
         // rows that do not count are not read: zeros
 #pragma unroll
         for (int i = 0; i < RT / C::kRows; ++i) {
-          const uint32_t x = (dst ^ (((i * C::kRows) & 7) << 4)) + i * C::kRows * 128;
+          const uint32_t flip = ((i * C::kRows) & 7) << 4;
           const int r = i * C::kRows + lr, n = mask >> r & 1 ? 16 : 0;
           const int64_t o = n == 0 ? -at : i * C::kRows * d + (page < RT && r >= 8 ? skip : (int64_t)0);
-          cp_async16(x, ks + o, n);
-          cp_async16(x + C::kHalf, vs + o, n);
+          cp_async16((dst ^ flip) + i * C::kRows * 128, ks + o, n);
+          cp_async16((dst_v ^ flip) + i * C::kRows * 128, vs + o, n);
         }
       }
     }
@@ -489,8 +491,8 @@ paged_decode_kernel(const __grid_constant__ PagedArgs a) {
     settle();
     cur = nxt;
   }
-  if (pieces < NSEG * 8) {   // columns past d: zeros, for good
-    for (int i = lane; i < kRingBytes / 16; i += 32)
+  if (pieces < H * 4) {   // columns past d: zeros, for good
+    for (int i = lane; i < S * C::kStage / 16; i += 32)
       reinterpret_cast<uint4*>(ring)[i] = make_uint4(0u, 0u, 0u, 0u);
     __syncwarp();
   }
@@ -528,13 +530,12 @@ paged_decode_kernel(const __grid_constant__ PagedArgs a) {
     cp_async_wait<S - 1>();
     __syncwarp();
     {
-      const uint32_t ks = ring_u + s * 2 * C::kHalf, vs = ks + C::kHalf;
       uint32_t mask = (1u << RT) - 1u;
       if ((cuts >> src & 1) || (has_new && last)) {
         mask = __shfl_sync(0xffffffffu, cur.mask, src);
         const int r = mask >> 24 & 15;   // the unit's last row, if this is its last tile
         mask &= (1u << RT) - 1u;
-        unsigned char* st = ring + s * 2 * C::kHalf;
+        unsigned char* st = ring + s * C::kStage;
         if (has_new && last) {
           const int64_t slot = __shfl_sync(0xffffffffu, (long long)cur.slot, src);
           const int32_t unit = __shfl_sync(0xffffffffu, cur.unit, src);
@@ -549,8 +550,8 @@ paged_decode_kernel(const __grid_constant__ PagedArgs a) {
               const uint4 kx = *reinterpret_cast<const uint4*>(side + s * 2 * C::kRow + p * 16);
               const uint4 vx =
                   *reinterpret_cast<const uint4*>(side + s * 2 * C::kRow + C::kRow + p * 16);
-              *reinterpret_cast<uint4*>(st + pmma::piece<RT>(r, p)) = kx;
-              *reinterpret_cast<uint4*>(st + C::kHalf + pmma::piece<RT>(r, p)) = vx;
+              *reinterpret_cast<uint4*>(st + pmma::k_piece<RT, H>(r, p)) = kx;
+              *reinterpret_cast<uint4*>(st + pmma::v_piece<RT, H>(r, p)) = vx;
               *reinterpret_cast<uint4*>((T*)a.kp + at + p * (16 / (int)sizeof(T))) = kx;
               *reinterpret_cast<uint4*>((T*)a.vp + at + p * (16 / (int)sizeof(T))) = vx;
             }
@@ -558,7 +559,7 @@ paged_decode_kernel(const __grid_constant__ PagedArgs a) {
         }
         __syncwarp();
       }
-      att.tile(ks, vs, mask, a.scale.c2);
+      att.tile(ring_u + s * C::kStage, mask, a.scale.c2);
       __syncwarp();   // every lane is done with stage s
       const int n = src + S;
       if (i + S < count) {
@@ -760,15 +761,15 @@ paged_decode_kernel(const __grid_constant__ PagedArgs a) {
 constexpr size_t kTickBytes = 2048;
 static_assert(kMaxCtas * sizeof(uint32_t) <= kTickBytes, "tickets");
 
-template <typename T, int NSEG, int kPWarps>
+template <typename T, int H, int kPWarps>
 cudaError_t launch_w(const PagedShape& s, const PagedArgs& a, int64_t tiles, cudaStream_t st) {
-  using C = Cfg<T, NSEG>;
+  using C = Cfg<T, H>;
   constexpr int per_sm = kSmWarps / kPWarps;
   constexpr size_t smem = sizeof(PagedSmem<C, kPWarps>) + 1024;
   static_assert(per_sm * (smem + 1024) <= 228 * 1024 && smem <= 227 * 1024, "CTAs per SM");
   static std::atomic<int> slot[kMaxDevices];
   const int ok = per_device(slot, []() {
-    return cudaFuncSetAttribute(paged_decode_kernel<T, NSEG, kPWarps>,
+    return cudaFuncSetAttribute(paged_decode_kernel<T, H, kPWarps>,
                                 cudaFuncAttributeMaxDynamicSharedMemorySize,
                                 (int)smem) == cudaSuccess ? 1 : 0;
   });
@@ -788,18 +789,18 @@ cudaError_t launch_w(const PagedShape& s, const PagedArgs& a, int64_t tiles, cud
   cudaLaunchAttribute attr[1] = {pdl_attribute()};
   cfg.attrs = attr;
   cfg.numAttrs = grid >= per_sm * num_sms() ? 1 : 0;
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, paged_decode_kernel<T, NSEG, kPWarps>, a);
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, paged_decode_kernel<T, H, kPWarps>, a);
   if (e == cudaSuccess) count_launches(1);
   return e;
 }
 
-template <typename T, int NSEG>
+template <typename T, int H>
 cudaError_t launch_t(const PagedShape& s, const PagedArgs& a, cudaStream_t st) {
   const int64_t units = (int64_t)s.seqs * s.Hkv;
   // tiles that the tables could hold
-  const int64_t tiles = units * cdiv((int64_t)s.max_pages * s.page, Cfg<T, NSEG>::RT);
+  const int64_t tiles = units * cdiv((int64_t)s.max_pages * s.page, Cfg<T, H>::RT);
   const bool few_long = units <= kLongUnits && tiles >= 2 * (int64_t)num_sms() * kMinTiles;
-  return few_long ? launch_w<T, NSEG, 8>(s, a, tiles, st) : launch_w<T, NSEG, 4>(s, a, tiles, st);
+  return few_long ? launch_w<T, H, 8>(s, a, tiles, st) : launch_w<T, H, 4>(s, a, tiles, st);
 }
 }  // namespace
 
@@ -821,14 +822,14 @@ cudaError_t launch_paged_decode(const PagedShape& s, const void* q, const void* 
                     (int)s.U(), s.Hp(),
                     s.G(), s.d, shift, s.max_pages, s.num_pages, s.page_stride,
                     pmma::Scale{c2 > FLT_MIN ? c2 : FLT_MIN, flip}};
-  if (s.dtype == KV_BF16)
-    return s.d <= 64 ? launch_t<__nv_bfloat16, 1>(s, a, st) : launch_t<__nv_bfloat16, 2>(s, a, st);
-  switch ((s.d + 31) / 32) {
-    case 1: return launch_t<float, 1>(s, a, st);
-    case 2: return launch_t<float, 2>(s, a, st);
-    case 3: return launch_t<float, 3>(s, a, st);
-    default: return launch_t<float, 4>(s, a, st);
+  if (s.dtype == KV_BF16) {
+    if (s.d <= 64) return launch_t<__nv_bfloat16, 2>(s, a, st);
+    return s.d <= 96 ? launch_t<__nv_bfloat16, 3>(s, a, st) : launch_t<__nv_bfloat16, 4>(s, a, st);
   }
+  if (s.d <= 32) return launch_t<float, 2>(s, a, st);
+  if (s.d <= 64) return launch_t<float, 4>(s, a, st);
+  if (s.d <= 80) return launch_t<float, 5>(s, a, st);
+  return s.d <= 96 ? launch_t<float, 6>(s, a, st) : launch_t<float, 8>(s, a, st);
 }
 
 }  // namespace kv

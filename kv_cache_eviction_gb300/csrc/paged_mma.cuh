@@ -2,9 +2,10 @@
 // instructions, for up to 8 query rows:  (m, l, o) := running maximum, sum and output of
 //   p_r = exp2(c2 (q . k_r - m)),  l = sum p_r,  o = sum p_r v_r,   c2 > 0.
 //
-// A tile is RT rows, K then V, each as NSEG segments of [RT][128 bytes] with the 16-byte
-// pieces of row r permuted by r & 7, so that every access below touches 8
-// different pieces of the 32 banks.
+// A tile is RT rows of K and V of H half segments (64 bytes) each, in segments of [RT][128 bytes]
+// with the 16-byte pieces of row r permuted by r & 7, so that every access below touches 8
+// different pieces of the 32 banks: K's whole segments, V's, and for odd H one that holds the
+// rest of K's row, then of V's.
 //
 // m16n8k16 (bf16) and m16n8k8 (tf32) have 16 rows where a KV head has at most 8 queries.  The
 // other 8 rows carry what is lost by holding the left operand in few bits: rows 0..7 hold the
@@ -63,26 +64,29 @@ __device__ __forceinline__ float lds_f(uint32_t addr) {
   asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
   return v;
 }
-// The nearest tf32 (11 significant bits) to x, as fp32 bits.
-__device__ __forceinline__ uint32_t tf32_of(float x) {
-  uint32_t r;
-  asm("cvt.rna.tf32.f32 %0, %1;" : "=r"(r) : "f"(x));
-  return r;
-}
-// x = hi + lo to 22 bits (x - hi is exact).
+// x = hi + lo to 22 bits, both tf32 (11 significant bits, the low 13 of the word zero): hi is x
+// to the nearest (halves away from zero), x - hi is exact and at most 2^-11 of x's power of two,
+// so what lo's truncation drops is below 2^-22 of x.  (Adding half a step to the word rounds as
+// cvt.rna.tf32 does, in fewer instructions: 31 % of the kernel at d = 128; a NaN stays one in lo.)
 __device__ __forceinline__ void tf32_split(float x, uint32_t& hi, uint32_t& lo) {
-  hi = tf32_of(x);
-  lo = tf32_of(x - __uint_as_float(hi));
+  hi = (__float_as_uint(x) + 0x1000u) & 0xFFFFE000u;
+  lo = __float_as_uint(x - __uint_as_float(hi)) & 0xFFFFE000u;
 }
 __device__ __forceinline__ uint32_t bf16x2_of(float x, float y) {   // x in the low half
   const __nv_bfloat162 b = __floats2bfloat162_rn(x, y);
   return *reinterpret_cast<const uint32_t*>(&b);
 }
 
-// Byte offset of 16-byte piece c of row r within a tile of RT rows.
-template <int RT>
-__device__ __forceinline__ uint32_t piece(int r, int c) {
-  return (uint32_t)((c >> 3) * (RT * 128) + r * 128 + (((c ^ r) & 7) << 4));
+// Byte offset of 16-byte piece c of K's (V's) row r within a tile of RT rows.
+template <int RT, int H>
+__device__ __forceinline__ uint32_t k_piece(int r, int c) {
+  const int seg = c >> 3;
+  return (uint32_t)((seg < H / 2 ? seg : H / 2 * 2) * (RT * 128) + r * 128 + (((c ^ r) & 7) << 4));
+}
+template <int RT, int H>
+__device__ __forceinline__ uint32_t v_piece(int r, int c) {
+  const int seg = c >> 3;
+  return seg < H / 2 ? k_piece<RT, H>(r, c) + H / 2 * (RT * 128) : k_piece<RT, H>(r, c) ^ 64u;
 }
 
 struct Scale {
@@ -90,7 +94,7 @@ struct Scale {
   uint32_t flip;   // sign bits of q to flip (bf16: of both halves)
 };
 
-template <typename T, int NSEG>
+template <typename T, int H>
 struct Tile;
 
 // What both types share: lane (4 g + c)'s running state for query g, and its part of o:
@@ -136,12 +140,12 @@ struct State {
   }
 };
 
-template <int NSEG>
-struct Tile<__nv_bfloat16, NSEG> : State<NSEG * 8> {
+template <int H>
+struct Tile<__nv_bfloat16, H> : State<H * 4> {
   static constexpr int RT = 16;
-  static constexpr int NT = NSEG * 8;
-  static constexpr int D = NSEG * 64;     // columns held (d rounded up; the rest is zero)
-  static constexpr int NQ = NSEG * 8;     // 32-bit words of q per lane
+  static constexpr int NT = H * 4;
+  static constexpr int D = H * 32;     // columns held (d rounded up; the rest is zero)
+  static constexpr int NQ = H * 4;     // 32-bit words of q per lane
   uint32_t q[NQ];
 
   // Words of q for query g = lane / 4 (zero past d and for g >= G).
@@ -159,11 +163,11 @@ struct Tile<__nv_bfloat16, NSEG> : State<NSEG * 8> {
     for (int i = 0; i < NQ; ++i) q[i] = w[i] ^ sc.flip;
   }
 
-  // One tile at shared addresses ks, vs (1024-byte aligned); bit r of `mask`: row r counts
+  // One tile at shared address st (128-byte aligned); bit r of `mask`: row r counts
   // (others hold zeros: 0 * NaN is NaN).
   // A piece's address is its row's with piece bits under xor (r & 7) * 16, so the pieces of a
   // lane's row are one address xor a constant.
-  __device__ __forceinline__ void tile(uint32_t ks, uint32_t vs, uint32_t mask, float c2) {
+  __device__ __forceinline__ void tile(uint32_t st, uint32_t mask, float c2) {
     const int lane = threadIdx.x & 31, c = lane & 3;
     // scores: two sums per 8 rows (even and odd k-steps), short chains
     float s[2][2][4];
@@ -171,26 +175,31 @@ struct Tile<__nv_bfloat16, NSEG> : State<NSEG * 8> {
     for (int j = 0; j < 2; ++j)
 #pragma unroll
       for (int e = 0; e < 4; ++e) s[j][0][e] = s[j][1][e] = 0.f;
-    const uint32_t ka = ks + (lane & 7) * 128 + (((lane >> 3) ^ (lane & 7)) << 4);
+    const uint32_t ka = st + (lane & 7) * 128 + (((lane >> 3) ^ (lane & 7)) << 4);
     // (all loads first: their latency once, not once a step)
-    uint32_t b[2 * NSEG][2][4];
+    uint32_t b[H][2][4];
 #pragma unroll
-    for (int kk = 0; kk < 2 * NSEG; ++kk)
+    for (int kk = 0; kk < H; ++kk)
 #pragma unroll
       for (int j = 0; j < 2; ++j)
-        ldsm4(b[kk][j], (ka ^ ((kk & 1) * 64)) + (kk >> 1) * (RT * 128) + j * 1024);
+        ldsm4(b[kk][j], (ka ^ ((kk & 1) * 64)) + (kk < H / 2 * 2 ? kk >> 1 : kk) * (RT * 128) +
+                            j * 1024);
 #pragma unroll
-    for (int kk = 0; kk < 2 * NSEG; ++kk)
+    for (int kk = 0; kk < H; ++kk)
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
         mma_bf16_16816(s[j][0], q[4 * kk], 0u, q[4 * kk + 1], 0u, b[kk][j][0], b[kk][j][1]);
         mma_bf16_16816(s[j][1], q[4 * kk + 2], 0u, q[4 * kk + 3], 0u, b[kk][j][2], b[kk][j][3]);
       }
     // V too, while the softmax is worked out
-    const uint32_t va = vs + (lane & 15) * 128 + (((lane >> 4) ^ (lane & 7)) << 4);
+    const uint32_t va = st + (lane & 15) * 128 + (((lane >> 4) ^ (lane & 7)) << 4);
     uint32_t v[NT / 2][4];
 #pragma unroll
-    for (int t = 0; t < NT; t += 2) ldsm4_t(v[t / 2], (va ^ ((t & 6) * 16)) + (t >> 3) * (RT * 128));
+    for (int t = 0; t < NT; t += 2) {
+      const bool rest = (t >> 3) >= H / 2;   // behind K's
+      ldsm4_t(v[t / 2], (va ^ ((rest ? t & 2 | 4 : t & 6) * 16)) +
+                            (rest ? H / 2 * 2 : H / 2 + (t >> 3)) * (RT * 128));
+    }
     float z[2][2];
 #pragma unroll
     for (int j = 0; j < 2; ++j)
@@ -222,12 +231,12 @@ struct Tile<__nv_bfloat16, NSEG> : State<NSEG * 8> {
   }
 };
 
-template <int NSEG>
-struct Tile<float, NSEG> : State<NSEG * 4> {
-  static constexpr int RT = NSEG > 2 ? 8 : 16;
-  static constexpr int NT = NSEG * 4;
-  static constexpr int D = NSEG * 32;
-  static constexpr int NQ = NSEG * 8;
+template <int H>
+struct Tile<float, H> : State<H * 2> {
+  static constexpr int RT = H > 4 ? 8 : 16;
+  static constexpr int NT = H * 2;
+  static constexpr int D = H * 16;
+  static constexpr int NQ = H * 4;
   uint32_t qh[NQ], ql[NQ];
 
   static __device__ __forceinline__ void load_q(const float* src, int G, int d,
@@ -244,12 +253,12 @@ struct Tile<float, NSEG> : State<NSEG * 4> {
     for (int i = 0; i < NQ; ++i) tf32_split(__uint_as_float(w[i] ^ sc.flip), qh[i], ql[i]);
   }
 
-  __device__ __forceinline__ void tile(uint32_t ks, uint32_t vs, uint32_t mask, float c2) {
+  __device__ __forceinline__ void tile(uint32_t st, uint32_t mask, float c2) {
     constexpr int NB = RT / 8;
     const int lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
     // scores: the high and the low parts of k, even and odd k-steps in sums of their own
     float z[NB][2], mt = -INFINITY;
-    const uint32_t ka = ks + g * 128 + (g << 4) + 4 * c;
+    const uint32_t ka = st + g * 128 + (g << 4) + 4 * c;
 #pragma unroll
     for (int j = 0; j < NB; ++j) {
       float s[4][4];
@@ -259,7 +268,8 @@ struct Tile<float, NSEG> : State<NSEG * 4> {
       float x[2 * NT];
 #pragma unroll
       for (int k = 0; k < 2 * NT; ++k)
-        x[k] = lds_f((ka ^ ((k & 7) << 4)) + (k >> 3) * (RT * 128) + j * 1024);
+        x[k] = lds_f((ka ^ ((k & 7) << 4)) + (k < H / 2 * 8 ? k >> 3 : H / 2 * 2) * (RT * 128) +
+                     j * 1024);
 #pragma unroll
       for (int k = 0; k < NT; ++k) {
         uint32_t h0, l0, h1, l1;
@@ -279,7 +289,7 @@ struct Tile<float, NSEG> : State<NSEG * 4> {
     this->raise(mt, c2);
     const float base = this->base(c2);
     // rows 2 c and 2 c + 1 of each 8, pieces under xor their row
-    const uint32_t v0 = vs + 2 * c * 128 + (((g >> 2) ^ (2 * c)) << 4) + 4 * (g & 3);
+    const uint32_t v0 = st + 2 * c * 128 + (((g >> 2) ^ (2 * c)) << 4) + 4 * (g & 3);
     const uint32_t v1 = v0 + 128 - (((g >> 2) ^ (2 * c)) << 4) + (((g >> 2) ^ (2 * c + 1)) << 4);
 #pragma unroll
     for (int j = 0; j < NB; ++j) {
@@ -291,9 +301,11 @@ struct Tile<float, NSEG> : State<NSEG * 4> {
       float x[2 * NT];
 #pragma unroll
       for (int t = 0; t < NT; ++t) {
-        const uint32_t at = (t >> 2) * (RT * 128) + j * 1024;
-        x[2 * t] = lds_f((v0 ^ ((2 * t & 7) << 4)) + at);
-        x[2 * t + 1] = lds_f((v1 ^ ((2 * t & 7) << 4)) + at);
+        const bool rest = (t >> 2) >= H / 2;   // behind K's
+        const uint32_t at = (rest ? H / 2 * 2 : H / 2 + (t >> 2)) * (RT * 128) + j * 1024;
+        const uint32_t flip = (rest ? 2 * t & 3 | 4 : 2 * t & 7) << 4;
+        x[2 * t] = lds_f((v0 ^ flip) + at);
+        x[2 * t + 1] = lds_f((v1 ^ flip) + at);
       }
 #pragma unroll
       for (int t = 0; t < NT; ++t) {
