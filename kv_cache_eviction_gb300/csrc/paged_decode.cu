@@ -36,8 +36,8 @@
 namespace kv {
 namespace {
 
-// Eight warps per SM, 128 KB of copies in flight: enough for the memory, and the SMs share it
-// evenly.  With 24 KB a warp (192 KB per SM) some SMs finish a fifth before others: 622 us
+// Eight warps per SM, 92 to 144 KB of copies in flight: enough for the memory, and the SMs share
+// it evenly.  With 24 KB a warp (192 KB per SM) some SMs finish a fifth before others: 622 us
 // against 603 on the 4.2 GB cache.  Six warps per SM 610.
 //
 // They are two CTAs of four warps or one of eight.  Two even out ragged calls better; one makes
@@ -50,7 +50,7 @@ constexpr int kSmWarps = 8;
 // columns) tiles for every CTA of four.
 constexpr int kLongUnits = 38;
 constexpr int kMaxCtas = 320;
-constexpr int kRingBytes = 18 * 1024;   // of a warp, at most
+constexpr int kRingBytes = 20 * 1024;   // of a warp, at most (and four tiles)
 // Tiles per CTA at least: a small call runs on as few CTAs as that allows.  One tile a warp: one
 // sequence of 500 rows 8.2 us; with two 8.9, with four 11.2.
 constexpr int kMinTiles = 4;
@@ -78,14 +78,15 @@ struct PagedArgs {
   pmma::Scale scale;
 };
 
-// H: 64-byte parts of a row.
+// H: 64-byte parts of a row.  Stages as wide as d needs: fp32 d = 72 in 5 instead of 6 parts took
+// 8 % less time, bf16 d = 96 in 3 instead of 4 2 %.
 template <typename T, int H>
 struct Cfg {
   using Tl = pmma::Tile<T, H>;
   static constexpr int RT = Tl::RT;
   static constexpr int kRow = H * 64;                      // bytes of a row in a stage
   static constexpr int kStage = RT * 2 * kRow;             // of a tile, K and V
-  static constexpr int kStages = kRingBytes / kStage;
+  static constexpr int kStages = kRingBytes / kStage < 4 ? kRingBytes / kStage : 4;
   static_assert(kStages >= 2, "ring");
   static constexpr int kSide = kStages * 2 * kRow;         // of a warp: its stages' new rows
   // a copy instruction of a warp: kRows rows of kLanes 16-byte pieces
@@ -456,22 +457,26 @@ paged_decode_kernel(const __grid_constant__ PagedArgs a) {
     int64_t skip = 0;
     if (page < RT) skip = __shfl_sync(0xffffffffu, (long long)(t.at2 - t.at), src) - 8 * (int64_t)d;
     if (pc < pieces) {
-      if ((mask & kAll) == kAll && page >= RT) {
+      // (without odd half segments V's stage is K's with an offset)
+      auto copy = [&](int i, const T* k, const T* v, int bytes) {
+        const uint32_t flip = ((i * C::kRows) & 7) << 4, row = i * C::kRows * 128;
+        const uint32_t x = (dst ^ flip) + row;
+        cp_async16(x, k, bytes);
+        cp_async16(H % 2 == 0 ? x + C::kStage / 2 : (dst_v ^ flip) + row, v, bytes);
+      };
+      if ((mask & kAll) == kAll) {
 #pragma unroll
         for (int i = 0; i < RT / C::kRows; ++i) {
-          const uint32_t flip = ((i * C::kRows) & 7) << 4;
-          cp_async16((dst ^ flip) + i * C::kRows * 128, ks + i * C::kRows * d);
-          cp_async16((dst_v ^ flip) + i * C::kRows * 128, vs + i * C::kRows * d);
+          const int64_t o = i * C::kRows * d + (i * C::kRows >= 8 ? skip : (int64_t)0);
+          copy(i, ks + o, vs + o, 16);
         }
       } else {
         // rows that do not count are not read: zeros
 #pragma unroll
         for (int i = 0; i < RT / C::kRows; ++i) {
-          const uint32_t flip = ((i * C::kRows) & 7) << 4;
           const int r = i * C::kRows + lr, n = mask >> r & 1 ? 16 : 0;
-          const int64_t o = n == 0 ? -at : i * C::kRows * d + (page < RT && r >= 8 ? skip : (int64_t)0);
-          cp_async16((dst ^ flip) + i * C::kRows * 128, ks + o, n);
-          cp_async16((dst_v ^ flip) + i * C::kRows * 128, vs + o, n);
+          const int64_t o = n == 0 ? -at : i * C::kRows * d + (r >= 8 ? skip : (int64_t)0);
+          copy(i, ks + o, vs + o, n);
         }
       }
     }

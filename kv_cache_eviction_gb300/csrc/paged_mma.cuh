@@ -233,7 +233,9 @@ struct Tile<__nv_bfloat16, H> : State<H * 4> {
 
 template <int H>
 struct Tile<float, H> : State<H * 2> {
-  static constexpr int RT = H > 4 ? 8 : 16;
+  // 16 rows where two stages of them fit a warp's ring: fewer instructions a row (64 ragged
+  // sequences, d = 72: 112 us against 122 with 8)
+  static constexpr int RT = H > 5 ? 8 : 16;
   static constexpr int NT = H * 2;
   static constexpr int D = H * 16;
   static constexpr int NQ = H * 4;
