@@ -5,8 +5,9 @@
 // bound by that stream, or by latency when the cache is small.  So the rows are split evenly,
 // whatever the lengths.  On GB300 (32 query heads over 8, bf16, d = 128): 128 ragged sequences of
 // 8000 rows, 4.2 GB, 600 us (6.95 TB/s, 1.02 of the measured copy rate); 64 of 2000 rows 85 us
-// (6.0 TB/s); one of 131000 rows 86 us (6.2 TB/s); 256 heads of 128 rows 11.4 us; one sequence of
-// 500 rows 8.0 us.
+// (6.0 TB/s); one of 131000 rows 85 us (6.3 TB/s); 256 heads of 128 rows 10.9 us; one sequence of
+// 500 rows 8.1 us.  fp32, 64 of 4000 rows: d = 128 315 us (6.6 TB/s), 96 245 us (6.35), 72 209 us
+// (5.6), 64 161 us (6.45).
 //
 //   1. Every CTA reads the tables' lengths.  In tiles of RT rows, the units (table, head) laid
 //      one after the other are one range [0, total): CTA c takes [total c / Ne, total (c + 1) /
