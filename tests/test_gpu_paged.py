@@ -445,6 +445,21 @@ def test_decode_bad_pages_slots_and_lengths():
     c.check(out)
 
 
+@pytest.mark.parametrize("page", [8, 16])
+@pytest.mark.parametrize("dtype,d", [("bf16", 64), ("bf16", 72), ("bf16", 96), ("f32", 32),
+                                     ("f32", 72), ("f32", 80), ("f32", 96), ("f32", 128)])
+def test_decode_bad_pages_of_every_width(dtype, d, page):
+    """Pages outside the pool, either half of a tile's rows, in rows of every width of a stage."""
+    c = Cache(3, 2, 5, d, 1, page, [101, 40, 64], dtype, 17, new=[1, 0, 1])
+    bad = [(0, 0), (0, 3), (1, 1), (2, 0), (2, 1), (2, 2)]
+    for u, col in bad:
+        c.table[u, col] = c.num_pages + u if col & 1 else -1 - u
+    out, ws = c.run()
+    assert kv.kv_check_device_status(ws) == ERR_ID
+    c.check(out, skip=bad)
+    c.check_pools()
+
+
 def test_decode_refused_table_keeps_its_rows():
     """A table that asked for a row and got no page (slot -1): nothing is stored, it attends over
     the rows it holds."""
