@@ -206,6 +206,8 @@ __device__ __forceinline__ void cp_async_wait() {   // all groups but the last N
 }
 
 // Merge of up to kB parts (max, sum, 4 outputs each; max -inf: none) into (M, L, acc).
+// (A part whose every score is a NaN has max -inf too, and a sum and outputs of NaN: with factors
+// of 0, not left out, they stay.)
 template <int kB>
 __device__ __forceinline__ void merge_parts(const float (&m)[kB], const float (&l)[kB],
                                             const float4 (&o)[kB], float& M, float& L,
@@ -213,14 +215,14 @@ __device__ __forceinline__ void merge_parts(const float (&m)[kB], const float (&
   float mn = M;
 #pragma unroll
   for (int b = 0; b < kB; ++b) mn = fmaxf(mn, m[b]);
-  if (mn == -INFINITY) return;
-  const float f = ptx::ex2(M - mn);   // 0 while M is -inf
+  const float base = mn == -INFINITY ? 0.f : mn;
+  const float f = ptx::ex2(M - base);   // 0 while M is -inf
   M = mn;
   L *= f;
   acc = make_float4(acc.x * f, acc.y * f, acc.z * f, acc.w * f);
 #pragma unroll
   for (int b = 0; b < kB; ++b) {
-    const float w = ptx::ex2(m[b] - mn);
+    const float w = ptx::ex2(m[b] - base);
     L = fmaf(l[b], w, L);
     acc.x = fmaf(o[b].x, w, acc.x);
     acc.y = fmaf(o[b].y, w, acc.y);
