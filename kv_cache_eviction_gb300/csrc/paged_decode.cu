@@ -205,24 +205,24 @@ __device__ __forceinline__ void cp_async_wait() {   // all groups but the last N
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
-// Merge of up to kB parts (max, sum, 4 outputs each; max -inf: none) into (M, L, acc).
+// Merge of up to kB parts (max of q . k, sum, 4 outputs each; max -inf: none) into (M, L, acc).
 // (A part whose every score is a NaN has max -inf too, and a sum and outputs of NaN: with factors
 // of 0, not left out, they stay.)
 template <int kB>
 __device__ __forceinline__ void merge_parts(const float (&m)[kB], const float (&l)[kB],
-                                            const float4 (&o)[kB], float& M, float& L,
+                                            const float4 (&o)[kB], float c2, float& M, float& L,
                                             float4& acc) {
   float mn = M;
 #pragma unroll
   for (int b = 0; b < kB; ++b) mn = fmaxf(mn, m[b]);
   const float base = mn == -INFINITY ? 0.f : mn;
-  const float f = ptx::ex2(M - base);   // 0 while M is -inf
+  const float f = ptx::ex2((M - base) * c2);   // 0 while M is -inf
   M = mn;
   L *= f;
   acc = make_float4(acc.x * f, acc.y * f, acc.z * f, acc.w * f);
 #pragma unroll
   for (int b = 0; b < kB; ++b) {
-    const float w = ptx::ex2(m[b] - base);
+    const float w = ptx::ex2((m[b] - base) * c2);
     L = fmaf(l[b], w, L);
     acc.x = fmaf(o[b].x, w, acc.x);
     acc.y = fmaf(o[b].y, w, acc.y);
@@ -579,7 +579,7 @@ paged_decode_kernel(const __grid_constant__ PagedArgs a) {
     // ---- the end of a unit, or of the warp's tiles
     if (last || i == count - 1) {
       const int32_t unit = __shfl_sync(0xffffffffu, cur.unit, src);
-      att.finish(a.scale.c2);
+      att.finish();
       const int g = lane >> 2, col = 2 * (lane & 3);
       if (whole && last) {
         if (g < G) {
@@ -659,7 +659,7 @@ paged_decode_kernel(const __grid_constant__ PagedArgs a) {
       }
       float M = -INFINITY, L = 0.f;
       float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-      merge_parts<kPWarps>(m, l, o, M, L, acc);
+      merge_parts<kPWarps>(m, l, o, a.scale.c2, M, L, acc);
       if (cross >> i & 1) {
         float* Q = a.part + (int64_t)(2 * c + (i == 0 ? 0 : 1)) * kPartFloats;
         if (col == 0) {
@@ -732,7 +732,7 @@ paged_decode_kernel(const __grid_constant__ PagedArgs a) {
           o[b] = in ? __ldcg(reinterpret_cast<const float4*>(P + kPartHead + g * D + col))
                     : make_float4(0.f, 0.f, 0.f, 0.f);
         }
-        merge_parts<kB>(m, l, o, M, L, acc);
+        merge_parts<kB>(m, l, o, a.scale.c2, M, L, acc);
       };
       if (in_part && parts[y] <= 8 * groups) {
         take(grp, std::integral_constant<int, 8>());
@@ -751,7 +751,7 @@ paged_decode_kernel(const __grid_constant__ PagedArgs a) {
           const float4* p = sm.part4[t >> 5][0] + 2 * (t & 31);
           const float m[1] = {p[1].x}, l[1] = {p[1].y};
           const float4 o[1] = {p[0]};
-          merge_parts<1>(m, l, o, M, L, acc);
+          merge_parts<1>(m, l, o, a.scale.c2, M, L, acc);
         }
         __syncthreads();
       }

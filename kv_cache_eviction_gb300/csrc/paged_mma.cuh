@@ -20,9 +20,11 @@
 // columns c and c + 4, the rows of each 8 are taken in the order 0, 2, 4, 6, 1, 3, 5, 7), so p
 // never leaves its lane.
 //
-// The scale is no factor of its own: p = exp2(fma(s, c2, -m c2)).  A negative scale is taken
-// into q's sign, and a zero one is the smallest positive number, so that masked scores (-inf)
-// give zeros (Scale).
+// The scale is no factor of its own: p = exp2((s - m) c2), maxima are of q . k.  (As
+// exp2(fma(s, c2, -m c2)), an addition less a score, the rounding of m c2 moves every exponent,
+// beyond float's range for |m c2| past 2^31: finite scores gave zeros and NaN.)  A negative scale is
+// taken into q's sign, and a zero one is the smallest positive number, so that masked scores
+// (-inf) give zeros (Scale).
 #pragma once
 
 #include "kv_internal.cuh"
@@ -126,10 +128,9 @@ struct State {
         for (int e = 0; e < 4; ++e) o[t][e] *= a;
     }
   }
-  __device__ __forceinline__ float base(float c2) const { return m == -INFINITY ? 0.f : -m * c2; }
-  // After the last tile: m in units of log2, l whole in every lane of the query, o in [0..1].
-  __device__ __forceinline__ void finish(float c2) {
-    m *= c2;
+  __device__ __forceinline__ float base() const { return m == -INFINITY ? 0.f : m; }
+  // After the last tile: l whole in every lane of the query, o in [0..1].
+  __device__ __forceinline__ void finish() {
     l += __shfl_xor_sync(0xffffffffu, l, 1);
     l += __shfl_xor_sync(0xffffffffu, l, 2);
 #pragma unroll
@@ -213,11 +214,11 @@ struct Tile<__nv_bfloat16, H> : State<H * 4> {
           if (!(mask >> (8 * j + 2 * c + e) & 1)) z[j][e] = -INFINITY;
     }
     this->raise(fmaxf(fmaxf(z[0][0], z[0][1]), fmaxf(z[1][0], z[1][1])), c2);
-    const float base = this->base(c2);
+    const float base = this->base();
     uint32_t hi[2], lo[2];
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
-      const float p0 = ptx::ex2(fmaf(z[j][0], c2, base)), p1 = ptx::ex2(fmaf(z[j][1], c2, base));
+      const float p0 = ptx::ex2((z[j][0] - base) * c2), p1 = ptx::ex2((z[j][1] - base) * c2);
       this->l += p0 + p1;
       hi[j] = bf16x2_of(p0, p1);
       lo[j] = bf16x2_of(p0 - __uint_as_float(hi[j] << 16),
@@ -289,13 +290,13 @@ struct Tile<float, H> : State<H * 2> {
       }
     }
     this->raise(mt, c2);
-    const float base = this->base(c2);
+    const float base = this->base();
     // rows 2 c and 2 c + 1 of each 8, pieces under xor their row
     const uint32_t v0 = st + 2 * c * 128 + (((g >> 2) ^ (2 * c)) << 4) + 4 * (g & 3);
     const uint32_t v1 = v0 + 128 - (((g >> 2) ^ (2 * c)) << 4) + (((g >> 2) ^ (2 * c + 1)) << 4);
 #pragma unroll
     for (int j = 0; j < NB; ++j) {
-      const float p0 = ptx::ex2(fmaf(z[j][0], c2, base)), p1 = ptx::ex2(fmaf(z[j][1], c2, base));
+      const float p0 = ptx::ex2((z[j][0] - base) * c2), p1 = ptx::ex2((z[j][1] - base) * c2);
       this->l += p0 + p1;
       uint32_t h0, l0, h1, l1;
       tf32_split(p0, h0, l0);

@@ -1,4 +1,5 @@
 """paged_decode_attn and kv_page_map on the GPU at the edges of what their arguments may hold."""
+import numpy as np
 import pytest
 import torch
 
@@ -64,3 +65,73 @@ def test_decode_nan_rows(dtype, d, G, lens, u, first, count):
     for b in range(len(lens)):
         if b != u:
             assert torch.equal(out[b], want[b])
+
+
+# ------------------------------------------------------------------------------- scores
+
+U23 = 2.0 ** -23
+
+
+def place(c, name):
+    """c.rows[name] into the device pool, whole rows (none is left to k_new / v_new)."""
+    pool = c.kp if name == "k" else c.vp
+    for u, n in enumerate(c.lens):
+        x = c.rows[name][u].cuda()
+        pages = c.table_host[u, :-(-n // c.page)].cuda()
+        r = torch.arange(n, device="cuda")
+        pool[pages[r // c.page], :, r % c.page] = x.transpose(0, 1)
+
+
+def check_exact_scores(c, out):
+    """Against 64 bits where every score is a float32 number whatever the order of its sum, so
+    that only what follows the scores can be off: the exponent (z - max) * scale, rounded twice, with
+    a factor rounded once, 2^-22 of itself; exp2 and the rescaling by it, 2^-22 at a time, at most 64
+    of those; the weights' bits (2^-16 of bf16's, 2^-21 of fp32's factors); sums of as many
+    terms as the head has tiles; the output's rounding."""
+    t_p = 2.0 ** -16 if c.dtype == "bf16" else 2.0 ** -20
+    half = torch.finfo(c.dt).eps / 2
+    got = out.double().cpu().numpy()
+    q = c.q.double().numpy()
+    for u, n in enumerate(c.lens):
+        for h in range(c.hkv):
+            k, v = (c.rows[x][u][h].double().numpy() for x in "kv")
+            for g in range(c.G):
+                z = k @ q[u, h * c.G + g]
+                assert np.array_equal(z, z.astype(np.float32))
+                x = (z - z.max()) * c.scale
+                p = np.exp(x)
+                p /= p.sum()
+                want, mag = p @ v, p @ np.abs(v)
+                e = np.abs(x) * 2.0 ** -22 + 64 * 2.0 ** -22
+                tol = ((p * e) @ np.abs(v) + (p @ e) * mag +
+                       ((2 * n / 8 + 64) * U23 + t_p) * mag + half * np.abs(want))
+                off = np.abs(got[u, h * c.G + g] - want)
+                assert bool((off <= tol).all()), (u, h, g, float((off / tol).max()))
+
+
+@pytest.mark.parametrize("lens", [[16], [64, 16], [500, 40], [3000, 16, 700], [9000]])
+@pytest.mark.parametrize("dtype,d,G", [("bf16", 128, 4), ("bf16", 72, 2), ("f32", 128, 2),
+                                       ("f32", 64, 3)])
+@pytest.mark.parametrize("power,up", [(24, 1), (24, -1), (40, 1)])
+def test_decode_far_scores(dtype, d, G, lens, power, up):
+    """Scores around 2^24 (where one rounding of score * scale moves an exponent by a half) and
+    2^40 (by thousands), rising or falling over the rows: the softmax goes by their differences."""
+    c = Cache(len(lens), 2, G, d, 1, 16, lens, dtype, 43, new=[0] * len(lens))
+    step = 2.0 ** (power - 23)                    # one step of float32 at 2^power
+    c.q.zero_()
+    c.q[:, :, 0] = 2.0 ** (power // 2)
+    c.q[:, :, 9] = step
+    for u, n in enumerate(lens):
+        k = c.rows["k"][u]
+        k.zero_()
+        k[:, :, 0] = 2.0 ** (power - power // 2)
+        r = torch.arange(n).float()
+        # 0..127 over the rows, so that the maximum moves from tile to tile; every value many times
+        k[:, :, 9] = ((r if up > 0 else n - 1 - r) * 128 / n).floor().to(c.dt)
+    place(c, "k")
+    place(c, "v")
+    c.qd.copy_(c.q)
+    c.scale = 0.125
+    out, ws = c.run(with_new=False)
+    assert kv.kv_check_device_status(ws) == 0
+    check_exact_scores(c, out)
