@@ -248,8 +248,8 @@ __global__ void __launch_bounds__(kMThreads) page_map_kernel(const MapArgs a) {
     if (!last) return;
   }
   for (int u = tid; u < a.U; u += nthreads) {
-    if (alone && cuS[u + 1] != cuS[u] && cuS[u + 1] - cuS[u] <= kOwnRows) continue;   // done
     const Ask k = ask_of(a.lens[u], a.add[u], a.max_pages, a.shift);
+    if (alone && k.gain > 0 && k.gain <= kOwnRows) continue;   // done
     const bool ok = served(u, k);
     a.lens_out[u] = ok ? k.now : k.len;
     if (ok && k.need > 0) taken = max(taken, needS[u] + k.need);

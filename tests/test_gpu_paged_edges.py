@@ -4,7 +4,7 @@ import pytest
 import torch
 
 import kv_cache_eviction_gb300 as kv
-from tests.paged import Cache
+from tests.paged import Cache, workspace
 
 pytestmark = pytest.mark.gpu
 
@@ -135,3 +135,29 @@ def test_decode_far_scores(dtype, d, G, lens, power, up):
     out, ws = c.run(with_new=False)
     assert kv.kv_check_device_status(ws) == 0
     check_exact_scores(c, out)
+
+
+# ------------------------------------------------------------------------------- page map
+
+@pytest.mark.parametrize("first,second", [(2**31 - 3, 100), (2**31 - 2, 100), (2**31 - 5, 1000),
+                                          (2**31 - 5, 3)])
+def test_map_sums_of_gains_past_32_bits(first, second):
+    """A garbage gain just under 2^31 and a table behind it: both are refused, and every length is
+    written."""
+    i32, i64 = torch.int32, torch.int64
+    s = kv.KvPagedShape.of(4, 1, 1, 64, 1, 8, 4, "bf16", 30)
+    lens = torch.tensor([10, 7, 5, 9], dtype=i32, device="cuda")
+    add = torch.tensor([first, second, 0, -9], dtype=i32, device="cuda")
+    ring = torch.arange(30, dtype=i32, device="cuda")
+    state = torch.tensor([6, 30], device="cuda")
+    table = torch.arange(16, dtype=i32, device="cuda").view(4, 4) % 6
+    out, state_out = torch.full((4,), -3, dtype=i32, device="cuda"), torch.zeros(2, dtype=i64,
+                                                                                 device="cuda")
+    cu, slots = torch.zeros(5, dtype=i64, device="cuda"), torch.full((6,), -7, device="cuda")
+    ws = workspace(kv.KV_OP_PAGE_MAP, s)
+    kv.kv_page_map(s, lens, add, ring, state, table, out, state_out, cu, slots, ws)
+    assert kv.kv_check_device_status(ws) in (7, 9)
+    assert out.tolist() == [10, 7, 5, 0]
+    assert state_out.tolist() == [6, 32]
+    assert cu.tolist() == [0, first, first + second, first + second, first + second]
+    assert slots.tolist() == [-1] * 6
