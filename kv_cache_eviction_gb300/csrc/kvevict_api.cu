@@ -545,7 +545,7 @@ kv_status kv_paged_write(const kv_paged_shape* shape, const void* k, const void*
   if (st != KV_OK) return st;
   if (ws == nullptr || !aligned16(ws)) return KV_ERR_INVALID_ARG;
   if (rows < 0 || rows > INT32_MAX || src_stride < 0) return KV_ERR_INVALID_ARG;
-  if (rows == 0) return KV_OK;
+  if (s.seqs == 0 || rows == 0) return KV_OK;
   if (k == nullptr || v == nullptr || slot_map == nullptr || k_pages == nullptr ||
       v_pages == nullptr)
     return KV_ERR_INVALID_ARG;

@@ -198,3 +198,11 @@ def test_reference_map_keeps_every_page():
         assert (slots[min(cu[-1], 150):] == -7).all()
         lens = new
     assert seen == {ERR_PAGES, ERR_TABLE, ERR_SLOTS}
+
+
+def test_write_of_no_sequences(L):
+    """With seqs = 0 the row write does nothing either, whatever the number of rows."""
+    assert call_write(L, shape(seqs=0)) == kv.KV_OK
+    assert call_write(L, shape(seqs=0), None, None, 0, None, 10, None, None, None) == kv.KV_OK
+    assert call_write(L, shape(seqs=0), rows=-1) == kv.KV_ERR_INVALID_ARG
+    assert call_write(L, shape(seqs=0), ws=None) == kv.KV_ERR_INVALID_ARG
