@@ -49,6 +49,23 @@ __device__ __forceinline__ void mma_tf32_1688(float (&d)[4], uint32_t a0, uint32
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
+// The same with sums that start from zero.
+__device__ __forceinline__ void mma_bf16_16816_new(float (&d)[4], uint32_t a0, uint32_t a1,
+                                                   uint32_t a2, uint32_t a3, uint32_t b0,
+                                                   uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+      "{%8,%9}, {%10,%10,%10,%10};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
+}
+__device__ __forceinline__ void mma_tf32_1688_new(float (&d)[4], uint32_t a0, uint32_t a1,
+                                                  uint32_t a2, uint32_t a3, uint32_t b0,
+                                                  uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+      "{%8,%9}, {%10,%10,%10,%10};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
+}
 __device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
@@ -101,17 +118,55 @@ struct Tile;
 
 // What both types share: lane (4 g + c)'s running state for query g, and its part of o:
 // columns 8 t + 2 c and + 1 for every t < NT.
-template <int NT>
+//
+// The matrix instruction cuts its sums off instead of rounding them, always towards zero: with o as
+// its accumulator over all tiles of a warp, outputs of positive values shrank by 2^-25 to 2^-23 a
+// tile (fp32: 1e-5 to 4.5e-5 after 446 tiles, where plain float sums are 1e-7 off).  So it adds up
+// kHold tiles at most, and their sums are added to o rounded to the nearest (4e-7).  bf16 takes a
+// tile: 607 us on 4.2 GB, 606 with o as accumulator.  fp32, bound by instructions, takes four up to
+// d = 96 and one above, where registers are short.  64 sequences of 4000 rows, o as accumulator /
+// four / one, us: d = 64 162 / 163 / 162, 72 210 / 209 / 227, 96 245 / 254 / 259, 128 315 / 324 / 317.
+template <int NT, int kHold>
 struct State {
-  float m, l;        // l: this lane's share of the sum
-  float o[NT][4];    // [0..1] high rows, [2..3] low rows
+  float m, l, lc;    // l: this lane's share of the sum; lc: what its rounding has added
+  float o[NT][2];
+  // sums of the last `held` tiles: [0..1] high rows, [2..3] low rows
+  float acc[kHold > 1 ? NT : 1][4];
+  int held;
   __device__ __forceinline__ void begin() {
     m = -INFINITY;
-    l = 0.f;
+    l = lc = 0.f;
+    held = 0;
 #pragma unroll
-    for (int t = 0; t < NT; ++t)
+    for (int t = 0; t < NT; ++t) {
+      o[t][0] = o[t][1] = 0.f;
+      if (kHold > 1) acc[t][0] = acc[t][1] = acc[t][2] = acc[t][3] = 0.f;
+    }
+  }
+  // l gains x, a tile's weights (one value a tile and a lane, so a compensated sum is cheap; equal
+  // weights round to the same side tile after tile, 4e-6 after 446 tiles).
+  __device__ __forceinline__ void add_l(float x) {
+    x -= lc;
+    const float s = l + x;
+    lc = (s - l) - x;
+    l = s;
+  }
+  // Sums of columns 8 t.. (high rows, low rows) to o.
+  __device__ __forceinline__ void add(int t, const float (&d)[4]) {
+    const float2 s = ptx::fadd2(make_float2(o[t][0], o[t][1]),
+                                ptx::fadd2(make_float2(d[0], d[1]), make_float2(d[2], d[3])));
+    o[t][0] = s.x;
+    o[t][1] = s.y;
+  }
+  // After a tile in acc.
+  __device__ __forceinline__ void tile_done() {
+    if (++held < kHold) return;
+    held = 0;
 #pragma unroll
-      for (int e = 0; e < 4; ++e) o[t][e] = 0.f;
+    for (int t = 0; t < NT; ++t) {
+      add(t, acc[t]);
+      acc[t][0] = acc[t][1] = acc[t][2] = acc[t][3] = 0.f;
+    }
   }
   // New maximum of this lane's query from the tile's scores; o and l follow.
   __device__ __forceinline__ void raise(float mt, float c2) {
@@ -122,27 +177,33 @@ struct State {
       const float a = mn > m ? ptx::ex2((m - mn) * c2) : 1.f;   // 0 while m is -inf
       m = mn;
       l *= a;
+      lc *= a;
 #pragma unroll
       for (int t = 0; t < NT; ++t)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) o[t][e] *= a;
+        for (int e = 0; e < 2; ++e) {
+          o[t][e] *= a;
+          if (kHold > 1) {
+            acc[t][e] *= a;
+            acc[t][2 + e] *= a;
+          }
+        }
     }
   }
   __device__ __forceinline__ float base() const { return m == -INFINITY ? 0.f : m; }
-  // After the last tile: l whole in every lane of the query, o in [0..1].
+  // After the last tile: l whole in every lane of the query.
   __device__ __forceinline__ void finish() {
     l += __shfl_xor_sync(0xffffffffu, l, 1);
     l += __shfl_xor_sync(0xffffffffu, l, 2);
+    if (kHold > 1) {
 #pragma unroll
-    for (int t = 0; t < NT; ++t) {
-      o[t][0] += o[t][2];
-      o[t][1] += o[t][3];
+      for (int t = 0; t < NT; ++t) add(t, acc[t]);
     }
   }
 };
 
 template <int H>
-struct Tile<__nv_bfloat16, H> : State<H * 4> {
+struct Tile<__nv_bfloat16, H> : State<H * 4, 1> {
   static constexpr int RT = 16;
   static constexpr int NT = H * 4;
   static constexpr int D = H * 32;     // columns held (d rounded up; the rest is zero)
@@ -216,24 +277,30 @@ struct Tile<__nv_bfloat16, H> : State<H * 4> {
     this->raise(fmaxf(fmaxf(z[0][0], z[0][1]), fmaxf(z[1][0], z[1][1])), c2);
     const float base = this->base();
     uint32_t hi[2], lo[2];
+    float ps[2];
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
       const float p0 = ptx::ex2((z[j][0] - base) * c2), p1 = ptx::ex2((z[j][1] - base) * c2);
-      this->l += p0 + p1;
+      ps[j] = p0 + p1;
       hi[j] = bf16x2_of(p0, p1);
       lo[j] = bf16x2_of(p0 - __uint_as_float(hi[j] << 16),
                         p1 - __uint_as_float(hi[j] & 0xFFFF0000u));
     }
+    this->add_l(ps[0] + ps[1]);
 #pragma unroll
     for (int t = 0; t < NT; t += 2) {
-      mma_bf16_16816(this->o[t], hi[0], lo[0], hi[1], lo[1], v[t / 2][0], v[t / 2][1]);
-      mma_bf16_16816(this->o[t + 1], hi[0], lo[0], hi[1], lo[1], v[t / 2][2], v[t / 2][3]);
+      float d[2][4];
+      mma_bf16_16816_new(d[0], hi[0], lo[0], hi[1], lo[1], v[t / 2][0], v[t / 2][1]);
+      mma_bf16_16816_new(d[1], hi[0], lo[0], hi[1], lo[1], v[t / 2][2], v[t / 2][3]);
+      this->add(t, d[0]);
+      this->add(t + 1, d[1]);
     }
   }
 };
 
 template <int H>
-struct Tile<float, H> : State<H * 2> {
+struct Tile<float, H> : State<H * 2, (H > 6 ? 1 : 4)> {
+  static constexpr int kHold = H > 6 ? 1 : 4;
   // 16 rows where two stages of them fit a warp's ring: fewer instructions a row (64 ragged
   // sequences, d = 72: 112 us against 122 with 8)
   static constexpr int RT = H > 5 ? 8 : 16;
@@ -294,31 +361,43 @@ struct Tile<float, H> : State<H * 2> {
     // rows 2 c and 2 c + 1 of each 8, pieces under xor their row
     const uint32_t v0 = st + 2 * c * 128 + (((g >> 2) ^ (2 * c)) << 4) + 4 * (g & 3);
     const uint32_t v1 = v0 + 128 - (((g >> 2) ^ (2 * c)) << 4) + (((g >> 2) ^ (2 * c + 1)) << 4);
+    uint32_t h0[NB], l0[NB], h1[NB], l1[NB];
+    float ps = 0.f;
 #pragma unroll
     for (int j = 0; j < NB; ++j) {
       const float p0 = ptx::ex2((z[j][0] - base) * c2), p1 = ptx::ex2((z[j][1] - base) * c2);
-      this->l += p0 + p1;
-      uint32_t h0, l0, h1, l1;
-      tf32_split(p0, h0, l0);
-      tf32_split(p1, h1, l1);
-      float x[2 * NT];
+      ps += p0 + p1;
+      tf32_split(p0, h0[j], l0[j]);
+      tf32_split(p1, h1[j], l1[j]);
+    }
+    this->add_l(ps);
+    float x[NB][2 * NT];
 #pragma unroll
-      for (int t = 0; t < NT; ++t) {
+    for (int t = 0; t < NT; ++t)
+#pragma unroll
+      for (int j = 0; j < NB; ++j) {
         const bool rest = (t >> 2) >= H / 2;   // behind K's
         const uint32_t at = (rest ? H / 2 * 2 : H / 2 + (t >> 2)) * (RT * 128) + j * 1024;
         const uint32_t flip = (rest ? 2 * t & 3 | 4 : 2 * t & 7) << 4;
-        x[2 * t] = lds_f((v0 ^ flip) + at);
-        x[2 * t + 1] = lds_f((v1 ^ flip) + at);
+        x[j][2 * t] = lds_f((v0 ^ flip) + at);
+        x[j][2 * t + 1] = lds_f((v1 ^ flip) + at);
       }
 #pragma unroll
-      for (int t = 0; t < NT; ++t) {
+    for (int t = 0; t < NT; ++t) {
+      float fresh[4];
+      float(&d)[4] = kHold > 1 ? this->acc[kHold > 1 ? t : 0] : fresh;
+#pragma unroll
+      for (int j = 0; j < NB; ++j) {
         uint32_t vh0, vl0, vh1, vl1;
-        tf32_split(x[2 * t], vh0, vl0);
-        tf32_split(x[2 * t + 1], vh1, vl1);
-        mma_tf32_1688(this->o[t], h0, l0, h1, l1, vh0, vh1);
-        mma_tf32_1688(this->o[t], h0, l0, h1, l1, vl0, vl1);
+        tf32_split(x[j][2 * t], vh0, vl0);
+        tf32_split(x[j][2 * t + 1], vh1, vl1);
+        if (kHold == 1 && j == 0) mma_tf32_1688_new(d, h0[j], l0[j], h1[j], l1[j], vh0, vh1);
+        else mma_tf32_1688(d, h0[j], l0[j], h1[j], l1[j], vh0, vh1);
+        mma_tf32_1688(d, h0[j], l0[j], h1[j], l1[j], vl0, vl1);
       }
+      if (kHold == 1) this->add(t, d);
     }
+    if (kHold > 1) this->tile_done();
   }
 };
 

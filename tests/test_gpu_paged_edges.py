@@ -161,3 +161,111 @@ def test_map_sums_of_gains_past_32_bits(first, second):
     assert state_out.tolist() == [6, 32]
     assert cu.tolist() == [0, first, first + second, first + second, first + second]
     assert slots.tolist() == [-1] * 6
+
+
+# ------------------------------------------------------------------------------- long sums
+
+class Many:
+    """A paged cache built and checked on the device, for calls with many tiles.  Scores are exact:
+    q and K are whole numbers, or (whole=False) every score is 0 but each 128th row's, which is
+    0.7 more.  V is positive."""
+
+    def __init__(self, seqs, hkv, G, d, page, lens, dtype, seed, whole=True):
+        gen = torch.Generator(device="cuda").manual_seed(seed)
+        self.hkv, self.G, self.d, self.page, self.lens = hkv, G, d, page, lens
+        self.dt = torch.bfloat16 if dtype == "bf16" else torch.float32
+        self.dtype, self.scale = dtype, 2.0 ** -6
+        used = [-(-n // page) for n in lens]
+        num, cols = sum(used) + 2, max(used)
+        order = torch.randperm(num, generator=gen, device="cuda")
+        self.table = torch.zeros(seqs, cols, dtype=torch.int32, device="cuda")
+        at = 0
+        for u, n in enumerate(used):
+            self.table[u, :n] = order[at:at + n]
+            at += n
+        self.shape = kv.KvPagedShape.of(seqs, hkv * G, hkv, d, 1, page, cols, dtype, num)
+
+        def ints(most, *size):
+            return torch.randint(-most, most + 1, size, generator=gen, device="cuda",
+                                 dtype=torch.int8).to(self.dt)
+
+        if whole:
+            self.q, self.kp = ints(3, seqs, hkv * G, d), ints(2, num, hkv, page, d)
+        else:
+            self.q = torch.zeros(seqs, hkv * G, d, dtype=self.dt, device="cuda")
+            self.kp = torch.zeros(num, hkv, page, d, dtype=self.dt, device="cuda")
+            self.q[..., 3], self.scale = 1, 0.7
+            for u, n in enumerate(used):
+                self.kp[self.table[u, :n:128 // page].long(), :, 0, 3] = 1
+        self.vp = self.v_all = torch.rand(num, hkv, page, d, generator=gen, device="cuda").add_(0.5).to(self.dt)
+        self.lens_t = torch.tensor(lens, dtype=torch.int32, device="cuda")
+
+    def rows(self, pool, u, h):
+        n = self.lens[u]
+        pages = self.table[u, :-(-n // self.page)].long()
+        return pool[pages, h].flatten(0, 1)[:n]
+
+    def mark_blocks(self, i, m):
+        """V of block b (8 rows) of a head is left in column b % d, and only where b / d % m = i."""
+        v = self.v_all
+        for u, n in enumerate(self.lens):
+            pages = self.table[u, :-(-n // self.page)].long()
+            b = torch.arange(len(pages) * self.page, device="cuda").view(-1, 1, self.page, 1) // 8
+            col = torch.arange(self.d, device="cuda")
+            for x in range(0, len(pages), 4096):
+                y = b[x:x + 4096]
+                self.vp[pages[x:x + 4096]] = v[pages[x:x + 4096]] * (
+                    (y % self.d == col) & (y // self.d % m == i))
+
+    def run(self):
+        out = torch.full((len(self.lens), self.hkv * self.G, self.d), float("nan"), dtype=self.dt,
+                         device="cuda")
+        ws = workspace(kv.KV_OP_PAGED_DECODE, self.shape)
+        kv.paged_decode_attn(self.shape, self.q, None, None, None, None, self.kp, self.vp,
+                             self.table, self.lens_t, self.scale, out, ws)
+        assert kv.kv_check_device_status(ws) == 0
+        return out.double()
+
+    def expected(self):
+        """64 bits, and the largest distance of a score to its maximum, times scale."""
+        out = torch.zeros(len(self.lens), self.hkv * self.G, self.d, dtype=torch.float64,
+                          device="cuda")
+        far = 0.0
+        for u in range(len(self.lens)):
+            for h in range(self.hkv):
+                g = slice(h * self.G, (h + 1) * self.G)
+                z = self.q[u, g].double() @ self.rows(self.kp, u, h).double().T * self.scale
+                z -= z.amax(1, keepdim=True)
+                far = max(far, float(-z.amin()))
+                p = z.exp()
+                out[u, g] = (p / p.sum(1, keepdim=True)) @ self.rows(self.vp, u, h).double()
+        return out, far
+
+    def tiles_of_a_warp(self):
+        """At most: an even share of the tiles, and what a boundary moves by."""
+        rt = 8 if self.dtype == "f32" and self.d > 80 else 16
+        tiles = sum(-(-n // rt) for n in self.lens) * self.hkv
+        warps = 8 * torch.cuda.get_device_properties(0).multi_processor_count
+        return tiles // warps + 25
+
+
+@pytest.mark.parametrize("seqs,hkv,G,d,lens", [
+    (1, 1, 2, 8, [6000001]), (3, 4, 4, 64, [90001, 250000, 17]), (1, 8, 4, 128, [131072]),
+    (40, 2, 1, 72, [20000 + 37 * i for i in range(40)]), (2, 8, 8, 96, [40000, 9]),
+    (64, 8, 4, 64, [8000] * 64), (16, 8, 2, 128, [24000] * 16)])
+def test_decode_fp32_sums_over_many_tiles(seqs, hkv, G, d, lens):
+    """Two weights, 1 and exp(-0.7), and positive values: all that can be off is what is kept of
+    weights and values and their sums.  (An error that all rows of one weight share moves the output
+    by its part times the difference of the two kinds' means.)  V and the weights count to 22 bits
+    of the half that has all rows, 2^-22 each at most.  What the matrix instruction adds by itself is
+    4 tiles, 32 sums at most, each cut off by up to 2^-23; that 64, and as much as half of it again for
+    the merges, in units of 2^-24.  All else is rounded to the nearest: of D errors of at most
+    2^-24 with no sign of their own, in the output and in the sum of the weights, 8 sqrt(D) is more
+    than ten standard deviations (2^-24 / sqrt(3) each).  Sums that are cut off over all D tiles
+    lean to one side, by 2^-24 and more a tile."""
+    c = Many(seqs, hkv, G, d, 64, lens, "f32", 51, whole=False)
+    want, _ = c.expected()
+    D = c.tiles_of_a_warp()
+    tol = (2 * 2.0 ** -22 + (16 * D ** 0.5 + 96) * 2.0 ** -24) * want
+    off = (c.run() - want).abs()
+    assert bool((off <= tol).all()), (D, float((off / want).max() * 2 ** 24))
