@@ -537,6 +537,7 @@ KV_API kv_status kv_paged_write(const kv_paged_shape* shape, const void* k, cons
  * k_new, v_new [seqs][hkv][d] dtype, or both NULL (cu_add and slot_map are then not read)
  * cu_add, slot_map, slot_capacity: as given to and written by kv_page_map
  * block_table, lens (kv_page_map's lens_out), k_pages, v_pages: the cache
+ * softmax_scale  below 2^127 in size (KV_ERR_INVALID_ARG)
  * out          [seqs][hq][d] dtype
  * Sums, the softmax and out before its rounding are float32 (the softmax numerators are held to
  * 16 bits for bf16, fp32 factors to 22).  The K and V rows attended to and their scores have to

@@ -573,7 +573,7 @@ kv_status paged_decode_attn(const kv_paged_shape* shape, const void* q, const vo
   if (st != KV_OK) return st;
   if (ws == nullptr || !aligned16(ws)) return KV_ERR_INVALID_ARG;
   if ((k_new == nullptr) != (v_new == nullptr)) return KV_ERR_INVALID_ARG;
-  if (!std::isfinite(softmax_scale)) return KV_ERR_INVALID_ARG;
+  if (!(std::fabs(softmax_scale) < 0x1p127f)) return KV_ERR_INVALID_ARG;   // times log2 e is finite
   if (slot_capacity < 0 || slot_capacity > INT32_MAX) return KV_ERR_INVALID_ARG;
   if (s.seqs == 0) return KV_OK;
   if (q == nullptr || k_pages == nullptr || v_pages == nullptr || block_table == nullptr ||

@@ -206,3 +206,13 @@ def test_write_of_no_sequences(L):
     assert call_write(L, shape(seqs=0), None, None, 0, None, 10, None, None, None) == kv.KV_OK
     assert call_write(L, shape(seqs=0), rows=-1) == kv.KV_ERR_INVALID_ARG
     assert call_write(L, shape(seqs=0), ws=None) == kv.KV_ERR_INVALID_ARG
+
+
+def test_scales_past_the_range_of_their_product_with_log2_e(L):
+    """scale * log2(e) is a float32 number too: 2^127 and more is refused, either sign."""
+    s = shape()
+    n = kv.kv_paged_workspace_size(kv.KV_OP_PAGED_DECODE, s)
+    for scale in (2.0 ** 127, -2.0 ** 127, 3e38, -3.4e38, float("nan"), -float("inf")):
+        assert call_decode(L, s, scale=scale) == kv.KV_ERR_INVALID_ARG
+    for scale in (1.7e38, -1.7e38, 1e-45, 0.0):
+        assert call_decode(L, s, scale=scale, n=n - 1) == kv.KV_ERR_WORKSPACE
