@@ -269,3 +269,44 @@ def test_decode_fp32_sums_over_many_tiles(seqs, hkv, G, d, lens):
     tol = (2 * 2.0 ** -22 + (16 * D ** 0.5 + 96) * 2.0 ** -24) * want
     off = (c.run() - want).abs()
     assert bool((off <= tol).all()), (D, float((off / want).max() * 2 ** 24))
+
+
+@pytest.mark.parametrize("dtype,seqs,hkv,G,d,lens", [
+    ("bf16", 1, 8, 1, 128, [65001]), ("bf16", 1, 4, 4, 128, [20011]),
+    ("bf16", 4, 8, 3, 64, [30000, 9000, 100, 26001]), ("bf16", 1, 1, 8, 64, [100000]),
+    ("bf16", 51, 8, 2, 128, [3] * 49 + [20000, 45000]), ("bf16", 1, 2, 4, 8, [20001]),
+    ("f32", 1, 8, 1, 40, [65001]), ("f32", 52, 4, 1, 40, [1] * 50 + [20000, 45000]),
+    ("f32", 1, 8, 2, 128, [65001]), ("f32", 7, 2, 5, 72, [20011, 8, 7, 16, 40000, 33, 1000]),
+    ("bf16", 200, 8, 4, 128, [900 + 13 * i for i in range(200)])])
+def test_decode_no_tile_of_a_long_head_is_lost(dtype, seqs, hkv, G, d, lens):
+    """Warps with more than 32 tiles, units that cross many CTAs: every 8 rows count in one column
+    of V alone (a call for every m-th part of them), so a tile that is left out, taken twice or from
+    a wrong page moves that column by about 8 d m / n of itself, and by a fifth of that where its
+    weights are small: more than four times the bound.  That is the weights' errors (2^-22 for
+    exp2, the exponent's rounding, and each of at most 64 rescalings), their bits, sums of D tiles,
+    the output's rounding; scores are exact and all values positive.  One such loss is put into the
+    expected values of the longest head, on the CPU, and has to be past the bound."""
+    c = Many(seqs, hkv, G, d, 32, lens, dtype, 52)
+    c.vp = c.v_all.clone()
+    t_p = 2.0 ** -16 if dtype == "bf16" else 2.0 ** -20
+    m = -(-max(lens) // (80 * d))
+    for i in range(m):
+        c.mark_blocks(i, m)
+        want, far = c.expected()
+        rel = (2 * (64 + far) * 2.0 ** -22 + t_p + (2 * c.tiles_of_a_warp() + 64) * U23 +
+               torch.finfo(c.dt).eps / 2)
+        assert 4 * rel < 0.2 * 8 * d * m / max(lens)      # (what the test rests on)
+        off = (c.run() - want).abs()
+        assert bool((off <= rel * want.abs() + 1e-37).all()), (i, float((off / want).nan_to_num().max()))
+        if i == 0:
+            u = lens.index(max(lens))
+            k, v = (c.rows(pool, u, 0).double().cpu() for pool in (c.kp, c.vp))
+            p = (c.q[u, :G].double().cpu() @ k.T * c.scale).exp()
+            p /= p.sum(1, keepdim=True)
+            assert torch.allclose(p @ v, want[u, :G].cpu(), rtol=1e-9)
+            for first in (0, 32, 48):            # blocks of part 0: its first d
+                lost = p.clone()
+                lost[:, first:first + 8] = 0
+                lost /= lost.sum(1, keepdim=True)
+                moved = (lost @ v - p @ v).abs() > rel * (p @ v)
+                assert bool(moved.any(1).all())
