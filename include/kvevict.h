@@ -462,7 +462,10 @@ typedef struct {
 
 /* Bytes of device workspace `op` (kv_paged_op) needs for `shape` (0 for an invalid shape).
  * The same rules as kv_workspace_size: zeroed once before its first use, error word in the
- * first 256 bytes, calls that share one are ordered on one stream. */
+ * first 256 bytes, calls that share one are ordered on one stream.  kv_page_map,
+ * kv_paged_write and paged_decode_attn of any shapes may share one: each leaves its counters at
+ * zero.  The calls of the flat cache leave other bytes there, so one that they have used is zeroed
+ * again first. */
 KV_API size_t kv_paged_workspace_size(int op, const kv_paged_shape* shape);
 
 /*

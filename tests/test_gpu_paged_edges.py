@@ -310,3 +310,52 @@ def test_decode_no_tile_of_a_long_head_is_lost(dtype, seqs, hkv, G, d, lens):
                 lost /= lost.sum(1, keepdim=True)
                 moved = (lost @ v - p @ v).abs() > rel * (p @ v)
                 assert bool(moved.any(1).all())
+
+
+# ------------------------------------------------------------------------------- capacity
+
+@pytest.mark.parametrize("dtype,d", [("bf16", 128), ("bf16", 72), ("f32", 64), ("f32", 128)])
+@pytest.mark.parametrize("lens", [[500], [1, 0, 17], [3001, 40], [5] * 40 + [700]])
+def test_decode_short_rows_in_long_tables(dtype, d, lens):
+    """Block tables sized for 131072 rows a sequence, as a server sizes them, and few rows held: the
+    host goes by the capacity, the kernel by the lengths."""
+    c = Cache(len(lens), 2, 4, d, 1, 16, lens, dtype, 44)
+    far = torch.full((len(lens), 131072 // 16), -1, dtype=torch.int32, device="cuda")
+    far[:, :c.max_pages] = c.table
+    c.table = far
+    c.shape = kv.KvPagedShape.of(len(lens), 8, 2, d, 1, 16, far.shape[1], dtype, c.num_pages)
+    out, ws = c.run()
+    assert kv.kv_check_device_status(ws) == 0
+    c.check(out)
+    c.check_pools()
+
+
+def test_calls_of_several_shapes_share_a_workspace():
+    """One workspace for maps, writes and decodes of several shapes, one after the other on a stream:
+    the results of workspaces of their own."""
+    caches = [Cache(len(n), 2, G, d, t, 16, n * t, dtype, 45 + d, new=[0] * len(n) * t)
+              for n, G, d, t, dtype in (([3000, 5, 700], 4, 128, 1, "bf16"), ([9000], 2, 72, 1, "f32"),
+                                        ([40] * 60, 1, 64, 2, "bf16"), ([20000, 16], 8, 96, 1, "bf16"))]
+    want = [c.run()[0] for c in caches]
+    ws = torch.zeros(1 << 22, dtype=torch.uint8, device="cuda")
+    i32 = torch.int32
+    s = kv.KvPagedShape.of(40, 1, 1, 64, 1, 8, 2000, "bf16", 40000)
+    lens, add = torch.zeros(40, dtype=i32, device="cuda"), torch.full((40,), 900, dtype=i32,
+                                                                      device="cuda")
+    ring = torch.arange(40000, dtype=i32, device="cuda")
+    state = torch.tensor([0, 40000], device="cuda")
+    table = torch.full((40, 2000), -1, dtype=i32, device="cuda")
+    cu, slots = torch.zeros(41, dtype=torch.int64, device="cuda"), torch.zeros(
+        36000, dtype=torch.int64, device="cuda")
+    rows = torch.randn(36000, 1, 64, device="cuda").bfloat16()
+    kp, vp = (torch.zeros(40000, 1, 8, 64, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    for step in range(6):
+        kv.kv_page_map(s, lens, add, ring, state, table, lens, state, cu, slots, ws)
+        kv.kv_paged_write(s, rows, rows, slots, cu[40:], kp, vp, ws)
+        for c, w in zip(caches, want):
+            assert torch.equal(c.run(ws=ws)[0], w)
+        assert lens.tolist() == [900 * (step + 1)] * 40
+        assert bool((kp[slots // 8, 0, slots % 8] == rows[:, 0]).all())
+    assert kv.kv_check_device_status(ws) == 0
+    # (a page that is never given back: 900 rows six times are 675 pages a table)
+    assert state.tolist() == [40 * 675, 40000]
