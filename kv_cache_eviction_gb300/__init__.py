@@ -322,7 +322,7 @@ def _init_torch() -> None:
 
 def _device(t, what: str) -> int:
     """The current device (a host tensor raises before CUDA is asked)."""
-    if not isinstance(t, int) and not t.is_cuda:
+    if t is not None and not isinstance(t, int) and not t.is_cuda:
         raise ValueError("%s must be on a CUDA device" % what)
     if _device_now is None:
         _init_torch()
@@ -349,7 +349,9 @@ def _buf(t, dtype, count: int, dev: int, what: str) -> Optional[int]:
 
 
 def _work(ws, dev: int):
-    """Pointer and bytes of a workspace (of any type)."""
+    """Pointer and bytes of a workspace (of any type; None stays NULL)."""
+    if ws is None:
+        return None, 0
     if ws.get_device() != dev or not ws.is_contiguous():
         raise ValueError("ws must be contiguous on the current CUDA device")
     return ws.data_ptr(), ws.nbytes
@@ -358,7 +360,7 @@ def _work(ws, dev: int):
 def _rows_view(t, dtype, row: int, dev: int, what: str):
     """Pointer, count and stride (elements) of rows of `row` elements, [n][...]; a row is
     contiguous, rows may lie apart (parts of a fused projection)."""
-    if t.get_device() != dev or t.dtype is not dtype:
+    if t is None or t.get_device() != dev or t.dtype is not dtype:
         raise ValueError("%s must be %s on the current CUDA device" % (what, dtype))
     size = t.shape
     n = size[0]
@@ -409,14 +411,14 @@ def _stream_on(stream, dev: int) -> Optional[int]:
 def kv_page_map(shape: KvPagedShape, lens, add, free_ring, free_state, block_table, lens_out,
                 free_out, cu_add, slot_map, ws, stream=None) -> None:
     """Block tables, slots and lengths for the rows each table gains or loses.  ``lens_out`` may
-    be ``lens`` and ``free_out`` may be ``free_state``."""
+    be ``lens`` and ``free_out`` may be ``free_state``; ``slot_map`` None: no table gains rows."""
     dev = _device(lens, "lens")
     i32, i64, n = _I32, _I64, shape.seqs * shape.tables
     wp, wn = _work(ws, dev)
     st = lib().kv_page_map(
         ctypes.byref(shape), _buf(lens, i32, n, dev, "lens"), _buf(add, i32, n, dev, "add"),
         _buf(free_ring, i32, shape.num_pages, dev, "free_ring"),
-        _buf(free_state, i64, 2, dev, "free_state"), slot_map.numel(),
+        _buf(free_state, i64, 2, dev, "free_state"), 0 if slot_map is None else slot_map.numel(),
         _buf(block_table, i32, n * shape.max_pages, dev, "block_table"),
         _buf(lens_out, i32, n, dev, "lens_out"), _buf(free_out, i64, 2, dev, "free_out"),
         _buf(cu_add, i64, n + 1, dev, "cu_add"), _buf(slot_map, i64, 0, dev, "slot_map"), wp, wn,

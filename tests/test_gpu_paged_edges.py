@@ -359,3 +359,46 @@ def test_calls_of_several_shapes_share_a_workspace():
     assert kv.kv_check_device_status(ws) == 0
     # (a page that is never given back: 900 rows six times are 675 pages a table)
     assert state.tolist() == [40 * 675, 40000]
+
+
+# ------------------------------------------------------------------------------- binding
+
+@pytest.mark.parametrize("slots", [None, "empty"])
+def test_map_that_only_gives_pages_back_has_no_slot_map(slots):
+    """slot_map NULL with a capacity of 0, as the header allows it: None, or an empty tensor."""
+    i32, i64 = torch.int32, torch.int64
+    s = kv.KvPagedShape.of(3, 1, 1, 64, 1, 8, 4, "bf16", 12)
+    lens = torch.tensor([30, 8, 17], dtype=i32, device="cuda")
+    add = torch.tensor([-30, 0, -9], dtype=i32, device="cuda")
+    ring = torch.arange(12, dtype=i32, device="cuda")
+    state = torch.tensor([8, 12], device="cuda")
+    table = torch.tensor([[0, 1, 2, 3], [4, -1, -1, -1], [5, 6, 7, -1]], dtype=i32, device="cuda")
+    cu = torch.zeros(4, dtype=i64, device="cuda")
+    ws = workspace(kv.KV_OP_PAGE_MAP, s)
+    kv.kv_page_map(s, lens, add, ring, state, table, lens, state, cu,
+                   None if slots is None else torch.zeros(0, dtype=i64, device="cuda"), ws)
+    assert kv.kv_check_device_status(ws) == 0
+    assert lens.tolist() == [0, 8, 8] and state.tolist() == [8, 18] and cu.tolist() == [0] * 4
+    assert [ring[i % 12].item() for i in range(8, 18)] == [8, 9, 10, 11, 0, 1, 2, 3, 6, 7]
+
+
+def test_binding_refuses_missing_tensors():
+    """None where a call needs a tensor is an error of the library or a ValueError, as elsewhere."""
+    c = Cache(2, 2, 2, 64, 1, 16, [20, 30], "bf16", 14)
+    ws = workspace(kv.KV_OP_PAGED_DECODE, c.shape)
+    out = torch.empty_like(c.qd)
+    args = [c.qd, c.knd, c.vnd, c.cu, c.slots, c.kp, c.vp, c.table, c.lens_t, 0.1, out, ws]
+    for i in (0, 1, 2, 3, 5, 6, 7, 8, 10, 11):     # (slot_map may be None: no slots)
+        with pytest.raises((kv.KvError, ValueError)):
+            kv.paged_decode_attn(c.shape, *[None if j == i else x for j, x in enumerate(args)])
+    rows = torch.zeros(2, 2, 64, dtype=torch.bfloat16, device="cuda")
+    args = [rows, rows, c.slots, None, c.kp, c.vp, ws]
+    for i in (0, 1, 2, 4, 5, 6):
+        with pytest.raises((kv.KvError, ValueError)):
+            kv.kv_paged_write(c.shape, *[None if j == i else x for j, x in enumerate(args)])
+    ring = torch.zeros(c.num_pages, dtype=torch.int32, device="cuda")
+    state = torch.zeros(2, dtype=torch.int64, device="cuda")
+    args = [c.lens_t, c.lens_t.clone(), ring, state, c.table, c.lens_t, state, c.cu, c.slots, ws]
+    for i in (0, 1, 2, 3, 4, 5, 6, 7, 9):
+        with pytest.raises((kv.KvError, ValueError)):
+            kv.kv_page_map(c.shape, *[None if j == i else x for j, x in enumerate(args)])
