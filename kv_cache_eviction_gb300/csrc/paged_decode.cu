@@ -3,11 +3,11 @@
 //
 // The step reads every K and V row once and little else (4 d G flops for 2 d elements): it is
 // bound by that stream, or by latency when the cache is small.  So the rows are split evenly,
-// whatever the lengths.  On GB300 (32 query heads over 8, bf16, d = 128): 128 ragged sequences of
-// 8000 rows, 4.2 GB, 600 us (6.95 TB/s, 1.02 of the measured copy rate); 64 of 2000 rows 85 us
-// (6.0 TB/s); one of 131000 rows 85 us (6.3 TB/s); 256 heads of 128 rows 10.9 us; one sequence of
-// 500 rows 8.1 us.  fp32, 64 of 4000 rows: d = 128 315 us (6.6 TB/s), 96 245 us (6.35), 72 209 us
-// (5.6), 64 161 us (6.45).
+// whatever the lengths.  On GB300 (32 query heads over 8, bf16, d = 128; devices differ by 1 %):
+// 128 ragged sequences of 8000 rows, 4.2 GB, 606 us (6.87 TB/s, 1.01 of the measured copy rate); 64 of
+// 2000 rows 85 us (6.0 TB/s); one of 131000 rows 85 us (6.3 TB/s); 256 heads of 128 rows 11.0 us;
+// one sequence of 500 rows 8.3 us.  fp32, 64 of 4000 rows: d = 128 317 us (6.6 TB/s), 96 254 us
+// (6.1), 72 209 us (5.6), 64 163 us (6.4).
 //
 //   1. Every CTA reads the tables' lengths.  In tiles of RT rows, the units (table, head) laid
 //      one after the other are one range [0, total): CTA c takes [total c / Ne, total (c + 1) /
@@ -37,18 +37,26 @@
 namespace kv {
 namespace {
 
-// Eight warps per SM, 92 to 144 KB of copies in flight: enough for the memory, and the SMs share
-// it evenly.  With 24 KB a warp (192 KB per SM) some SMs finish a fifth before others: 622 us
-// against 603 on the 4.2 GB cache.  Six warps per SM 610.
+// Eight warps per SM and rings of 128 KB (144 where a row has three or six half segments, 160 where
+// it has five), full of copies in flight: enough for the memory, and the SMs share it evenly.  With
+// 24 KB a warp (192 KB per SM) some SMs finish a fifth before others: 622 us against 603 on the
+// 4.2 GB cache.  Six warps per SM 610.
 //
 // They are two CTAs of four warps or one of eight.  Two even out ragged calls better; one makes
 // half as many parts of a unit to be merged through the workspace, which counts where few units
-// are cut many times.  CTAs of 4 / 8 warps, us: one sequence of 8192 rows 15.5 / 13.1, of
-// 32768 31.6 / 29.7, of 131000 86.8 / 84.5, fp32 5 x 3001 rows of 2 heads 16.0 / 15.2; 64 ragged
-// sequences 84.6 / 86.0, 256 heads of 128 rows 10.9 / 11.1, one sequence of 500 rows 8.1 / 8.5.
+// are cut many times.  CTAs of 4 / 8 warps, us, ragged lengths:
+//   units                8           16          32          40          64          128
+//   500 rows         8.2 / 8.8   9.8 / 10.5  10.7 / 11.0  11.1 / 11.3  11.6 / 11.7  13.2 / 13.6
+//   2000            13.3 / 9.4  13.0 / 12.1  16.9 / 15.3  18.2 / 17.8  21.0 / 21.0  27.6 / 28.1
+//   8000            15.5 / 13.9 23.2 / 21.5  31.2 / 30.5  35.1 / 35.1  48.4 / 48.8  75.5 / 76.2
+// fp32, d = 72, 3000 rows: 10 units 15.6 / 14.7, 16 17.0 / 16.6, 38 24.8 / 25.4, 64 32.3 / 33.8.
 constexpr int kSmWarps = 8;
-// CTAs of eight warps: at most this many units, and (as far as the host knows, from the tables'
-// columns) tiles for every CTA of four.
+// CTAs of eight warps: at most this many units, a quarter of the SMs (from there on the two are level,
+// or four warps are ahead), and tiles for every CTA of four, as far as the host knows them from the
+// tables' columns.  With fewer tiles neither is ahead throughout: of 8 to 32 units of equal lengths,
+// four warps by 2 to 14 % at 500 to 700 rows, eight by 10 to 40 % at 300 rows and for 8 units of 1400 or
+// 2000; of ragged ones, eight by 3 to 10 % from 700 rows.  Where the tables have columns for 131072
+// rows and few are held: 8 units of 500 rows 8.4 / 8.5, of 2000 12.6 / 9.5, 40 units of 500 11.3 / 11.4.
 constexpr int kLongUnits = 38;
 constexpr int kMaxCtas = 320;
 constexpr int kRingBytes = 20 * 1024;   // of a warp, at most (and four tiles)
@@ -56,9 +64,10 @@ constexpr int kRingBytes = 20 * 1024;   // of a warp, at most (and four tiles)
 // sequence of 500 rows 8.2 us; with two 8.9, with four 11.2.
 constexpr int kMinTiles = 4;
 // A boundary inside a unit of at most this many tiles moves to the unit's nearer end: a part in
-// the workspace and a ticket cost 2 us, the tiles less than that.  16 / 24 / 32 tiles: 11.1 /
-// 10.9 / 10.3 us on 256 heads of 128 rows, 11.5 / 11.0 / 12.0 on skewed ones, and one sequence of
-// 500 rows (32 tiles a head) 8.1 / 8.1 / 10.5.
+// the workspace and a ticket cost 2 us, the tiles less than that.  16 / 24 / 32 / 48 tiles: 256 heads
+// of 128 rows 11.2 / 10.9 / 10.6 / 10.6 us; units of 500 rows (32 tiles), 8 of them 8.2 / 8.2 / 11.2 /
+// 11.2, 16 9.8 / 9.8 / 11.4 / 11.4, 64 11.6 / 11.7 / 11.7 / 13.2, 128 13.2 / 13.2 / 13.1 / 15.2;
+// units of 2000 rows level.
 constexpr int kSnapTiles = 24;
 // Part of a unit in the workspace: max[8], sum[8], then o[G][D].
 constexpr int kPartHead = 16;

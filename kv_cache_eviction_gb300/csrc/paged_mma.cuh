@@ -302,7 +302,7 @@ template <int H>
 struct Tile<float, H> : State<H * 2, (H > 6 ? 1 : 4)> {
   static constexpr int kHold = H > 6 ? 1 : 4;
   // 16 rows where two stages of them fit a warp's ring: fewer instructions a row (64 ragged
-  // sequences, d = 72: 112 us against 122 with 8)
+  // sequences, d = 72: 111 us against 127 with 8)
   static constexpr int RT = H > 5 ? 8 : 16;
   static constexpr int NT = H * 2;
   static constexpr int D = H * 16;

@@ -6,7 +6,7 @@
 // shift; longer rows take several groups.  The eight loads of a lane do not wait for the slots,
 // only its stores do.  On GB300: 131072 rows of 8 heads of 128 bf16 (1.07 GB read and written)
 // 161 us, 6.67 TB/s or 0.98 of the measured copy rate (172 us with one piece a thread and its
-// divisions); 100003 rows of one head of 64 fp32 16.7 us, 6.2 TB/s; 64 rows 2.1 us.
+// divisions); 100003 rows of one head of 64 fp32 16.7 us, 6.2 TB/s; 64 rows 2.3 us.
 #include "kv_internal.cuh"
 #include "tc_ptx.cuh"
 
