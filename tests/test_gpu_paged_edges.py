@@ -277,7 +277,10 @@ def test_decode_fp32_sums_over_many_tiles(seqs, hkv, G, d, lens):
     ("bf16", 51, 8, 2, 128, [3] * 49 + [20000, 45000]), ("bf16", 1, 2, 4, 8, [20001]),
     ("f32", 1, 8, 1, 40, [65001]), ("f32", 52, 4, 1, 40, [1] * 50 + [20000, 45000]),
     ("f32", 1, 8, 2, 128, [65001]), ("f32", 7, 2, 5, 72, [20011, 8, 7, 16, 40000, 33, 1000]),
-    ("bf16", 200, 8, 4, 128, [900 + 13 * i for i in range(200)])])
+    ("bf16", 200, 8, 4, 128, [900 + 13 * i for i in range(200)]),
+    # (33 to 38 tables: more than a warp holds, and CTAs of eight warps)
+    ("bf16", 36, 1, 4, 128, [9000 - 250 * i for i in range(36)]),
+    ("f32", 34, 1, 3, 72, [4, 8000] * 17), ("f32", 37, 1, 8, 128, [100 * i for i in range(1, 38)])])
 def test_decode_no_tile_of_a_long_head_is_lost(dtype, seqs, hkv, G, d, lens):
     """Warps with more than 32 tiles, units that cross many CTAs: every 8 rows count in one column
     of V alone (a call for every m-th part of them), so a tile that is left out, taken twice or from
