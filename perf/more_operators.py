@@ -43,34 +43,34 @@ def listed():
         _rotary("rotary 131072 rows", rows=131072, hq=32, hkv=8, d=128, rot=128, layout="half",
                 dtype="bf16", scaling="linear", fused=True, prompt=True),
         # Interleaved pairs, part of the head, fp32, an odd number of rows.
-        _rotary("rotary 20011 rows, part, fp32", rows=20011, hq=6, hkv=2, d=80, rot=24,
+        _rotary("rotary 20011 rows fp32 part", rows=20011, hq=6, hkv=2, d=80, rot=24,
                 layout="interleaved", dtype="f32", scaling="yarn", fused=False, prompt=True),
         # One new row for each sequence of a decode batch, into blocks that hold rows already.
-        _write("write 64 rows, one each", rows=64, seqs=64, heads=8, d=128, page=16,
+        _write("write 64 rows one each", rows=64, seqs=64, heads=8, d=128, page=16,
                format="e4m3", dtype="bf16", fused=True, lens_seed=31),
         # A whole 128K prompt of one layer, from the fused projection's rows.
         _write("write 131072 rows", rows=131072, seqs=1, heads=8, d=128, page=16, format="e4m3",
                dtype="bf16", fused=True, lens_seed=32),
         # Compacted rows of head tables (one head per page), fp32, in int8.
-        _write("write 100003 head rows, int8, fp32", rows=100003, seqs=256, heads=1, d=64,
+        _write("write 100003 rows int8 fp32", rows=100003, seqs=256, heads=1, d=64,
                page=32, format="int8", dtype="f32", fused=False, lens_seed=33),
         # The rows of a short shared prefix, for the attention of a prompt's next piece.
         _read("read 513 rows", rows=513, seqs=3, heads=8, d=128, page=16, format="e4m3",
               dtype="bf16", lens_seed=34),
         # The held part of a 128K prompt.
-        _read("read 131072 rows, int8", rows=131072, seqs=1, heads=8, d=128, page=64,
+        _read("read 131072 rows int8", rows=131072, seqs=1, heads=8, d=128, page=64,
               format="int8", dtype="bf16", lens_seed=35),
         # The first tokens after a short prompt, one sequence: latency.
         _decode("decode 1 x 500", seqs=1, hq=32, hkv=8, d=128, tables=1, page=16, mean=500,
                 sigma=0.0, format="e4m3", dtype="bf16", lens_seed=41),
         # 32 layers of one evicted sequence, every head with its own length and table.
-        _decode("decode 256 head tables, mean 128, int8", seqs=32, hq=32, hkv=8, d=128, tables=8,
+        _decode("decode 256 head tables int8", seqs=32, hq=32, hkv=8, d=128, tables=8,
                 page=16, mean=128, sigma=0.4, format="int8", dtype="bf16", lens_seed=42),
         # One sequence with a 128K context, fp32 queries and outputs.
-        _decode("decode 1 x 131000, int8, fp32", seqs=1, hq=32, hkv=8, d=128, tables=1, page=64,
+        _decode("decode 1 x 131000 int8 fp32", seqs=1, hq=32, hkv=8, d=128, tables=1, page=64,
                 mean=131000, sigma=0.0, format="int8", dtype="f32", lens_seed=43),
         # A full cache of a large batch: the streaming rate.
-        _decode("decode 128 ragged, mean 8000", seqs=128, hq=32, hkv=8, d=128, tables=1, page=32,
+        _decode("decode 128 ragged 8000", seqs=128, hq=32, hkv=8, d=128, tables=1, page=32,
                 mean=8000, sigma=0.3, format="e4m3", dtype="bf16", lens_seed=44),
     ]
 
