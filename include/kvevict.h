@@ -72,6 +72,12 @@ typedef enum { KV_GROUP_MEAN = 0, KV_GROUP_MAX = 1 } kv_group_reduce;
 typedef enum { KV_OP_SCORE = 0, KV_OP_ALLOCATE = 1, KV_OP_COMPACT = 2, KV_OP_DECODE = 3 } kv_op;
 /* ops of the paged cache, for kv_paged_workspace_size */
 typedef enum { KV_OP_PAGE_MAP = 4, KV_OP_PAGED_WRITE = 5, KV_OP_PAGED_DECODE = 6 } kv_paged_op;
+/* ops of the paged cache in 8 bits, for the same function */
+typedef enum {
+  KV_OP_QUANT_WRITE = 16, KV_OP_QUANT_READ = 17, KV_OP_QUANT_DECODE = 18
+} kv_quant_op;
+typedef enum { KV_E4M3 = 0, KV_INT8 = 1 } kv_quant_format;
+typedef enum { KV_ROTARY_HALF = 0, KV_ROTARY_INTERLEAVED = 1 } kv_rotary_layout;
 typedef enum { KV_TERMS_MEAN_POOLED = 0, KV_TERMS_L2 = 1 } kv_terms_kind;
 typedef enum { KV_PROJ_CRIT_GQA = 0, KV_PROJ_LAPROX = 1 } kv_proj_kind;
 
@@ -555,6 +561,103 @@ KV_API kv_status paged_decode_attn(const kv_paged_shape* shape, const void* q, c
                                    void* v_pages, const int32_t* block_table, const int32_t* lens,
                                    float softmax_scale, void* out, void* ws, size_t ws_bytes,
                                    void* stream);
+
+/*
+ * The paged cache in 8 bits
+ * -------------------------
+ * The paged cache with its rows held as codes (kv_quant_format: e4m3, or int8 from -127 to 127) and
+ * a scale for each block of KV_QUANT_BLOCK = 16 rows of one head, K and V apart: half the memory,
+ * and half the time of a decode step over a long cache, for a rounding of every value.  kv_page_map
+ * serves it as it is.  (The method's pages have no counterpart: they keep rows in 16 bits.)
+ *
+ *   k_pages, v_pages [num_pages][Hp][page][d] bytes, pages page_stride bytes apart
+ *   k_scale, v_scale [num_pages][Hp][page / 16] float32
+ *   value = code * scale, and shape.dtype is the type of q, k, v and out
+ *
+ * Scales are powers of two from 2^-96 on: the smallest that holds the block's largest finite value,
+ * |x| <= 448 (e4m3) or 127 (int8) times it, so that code * scale is exact in bf16 and fp32.  A value
+ * is off by at most 2^-4 of itself in e4m3 (2^-10 of the scale where that is more), and by half a
+ * scale in int8 (below 2^-6 of the block's largest value).  Rows have to be below 2^127 in size;
+ * infinities become the largest code, a NaN stays one in e4m3 and becomes 0 in int8.
+ *
+ * Rows that are added to a block which holds some take its scale, or raise it: the codes of the
+ * rows held are then rounded to the new scale (in e4m3 that changes only values below 2^-6 of it).
+ * The rows that a call writes to a block are rounded once, at the scale that holds them all.  The rows
+ * held are those below the first that the call writes, so a block that is filled anew from its first
+ * row on forgets what it had.  A block that gets rows belongs to one table.
+ *
+ * Limits: those of the paged cache, and page >= 16, d a multiple of 16 (KV_ERR_UNSUPPORTED).
+ * page_stride is a multiple of 16.  Workspaces: kv_paged_workspace_size with the ops of kv_quant_op;
+ * one may be shared with the calls of the paged cache under the same rules.
+ */
+#define KV_QUANT_BLOCK 16
+
+/*
+ * kv_quant_write -- kv_paged_write into the cache in 8 bits.
+ * For i < rows, with slot = slot_map[i] and the scales as above: code = round(x / scale), halves to
+ * even.  Rows with slot -1 are skipped; any other slot outside the pool sets the device error word
+ * (10) and is skipped.  The rows of one block are neighbours in slot_map, in ascending order and with
+ * no gap (kv_page_map's are); a block's rows appear once per call.
+ *
+ * k, v, src_stride, rows, n_rows as in kv_paged_write
+ */
+KV_API kv_status kv_quant_write(const kv_paged_shape* shape, int format, const void* k,
+                                const void* v, int64_t src_stride, const int64_t* slot_map,
+                                int64_t rows, const int64_t* n_rows, void* k_pages, void* v_pages,
+                                float* k_scale, float* v_scale, void* ws, size_t ws_bytes,
+                                void* stream);
+
+/*
+ * kv_quant_read -- rows of the cache in 8 bits as values, for what takes rows in 16 or 32 bits (the
+ * scores of a re-eviction, the attention of a prompt's next piece).
+ * For i < rows:  k / v [i][h][:] = code * scale of slot_map[i]; rows with slot -1, and rows whose
+ * slot lies outside the pool (10), are left as they were.  A slot may appear any number of times.
+ *
+ * k, v      rows of [Hp][d] dtype out, dst_stride elements apart (0 means dense)
+ * rows, n_rows as in kv_paged_write
+ */
+KV_API kv_status kv_quant_read(const kv_paged_shape* shape, int format, const void* k_pages,
+                               const void* v_pages, const float* k_scale, const float* v_scale,
+                               const int64_t* slot_map, int64_t rows, const int64_t* n_rows,
+                               void* k, void* v, int64_t dst_stride, void* ws, size_t ws_bytes,
+                               void* stream);
+
+/*
+ * Rotary positions: pairs of columns of queries and keys turned by their position, before the keys
+ * are scored or cached.  (The method's pages take rotated rows as given.)
+ */
+typedef struct {
+  int32_t hq, hkv, d;   /* heads of q and of k (either may be 0), head dim                     */
+  int32_t rot;          /* columns that turn, from the first on; the others stay                */
+  int32_t layout;       /* kv_rotary_layout: pairs (i, i + rot / 2), or (2 i, 2 i + 1)          */
+  int32_t dtype;        /* kv_dtype of the rows                                                 */
+  float magnitude;      /* factor on the turned columns (1; other values come with some stretched
+                           frequencies)                                                         */
+} kv_rotary_shape;
+
+/*
+ * kv_rotary -- for every row r with positions[r] >= 0, every head of q and k and every pair i,
+ * with t = positions[r] * inv_freq[i] (whole turns drop off exactly) and m the magnitude:
+ *   (a, b) -> m (a cos t - b sin t, a sin t + b cos t).
+ * Columns from rot on are copied.  Rows with a position below 0 (an idle sequence, kv_compact's
+ * reserve rows in kept_idx) are left as they were in q_out and k_out.
+ * back != 0: t -> -t.  That is the gradient of the call (and, for magnitude 1, its inverse): with
+ * kept_idx[r] - new position it moves the keys of a compacted cache to new positions.
+ *
+ * q, k      rows of [hq][d], [hkv][d] dtype, q_stride / k_stride elements apart (0 means dense), so
+ *           that they may be parts of a fused projection's rows; NULL for 0 heads
+ * q_out, k_out the same with strides of their own.  q_out may be q with the same stride, and k_out k;
+ *           other overlaps of an input's rows with its output are refused (KV_ERR_INVALID_ARG)
+ * positions [rows] int32, inv_freq [rot / 2] float64 (below 2^52)
+ * rows, n_rows as in kv_paged_write
+ * Limits: d a multiple of 8 up to 256, rot a multiple of 8, hq and hkv up to 4096.  No workspace.
+ * Alignment: rows 16 bytes, strides multiples of 16 bytes, positions 4, inv_freq and n_rows 8.
+ */
+KV_API kv_status kv_rotary(const kv_rotary_shape* shape, int back, const void* q, int64_t q_stride,
+                           const void* k, int64_t k_stride, const int32_t* positions,
+                           const double* inv_freq, int64_t rows, const int64_t* n_rows,
+                           void* q_out, int64_t q_out_stride, void* k_out, int64_t k_out_stride,
+                           void* stream);
 
 /* Synchronises `stream`, reads the device error word of `ws` and clears it.
  * Returns KV_OK or KV_ERR_DEVICE_CHECK (KV_ERR_CUDA if the copy fails).

@@ -13,6 +13,8 @@ import ctypes
 import os
 from typing import Optional
 
+from .rotary import kv_rotary_inv_freq
+
 __all__ = [
     "KV_OK", "KV_ERR_INVALID_ARG", "KV_ERR_UNSUPPORTED", "KV_ERR_WORKSPACE", "KV_ERR_CAPACITY",
     "KV_ERR_CUDA", "KV_ERR_DEVICE_CHECK", "KV_BF16", "KV_F32", "KV_SCORE_ADA", "KV_SCORE_LAVA",
@@ -29,6 +31,9 @@ __all__ = [
     "KV_PAGED_DECODE_MAX_TABLES",
     "KvPagedShape", "kv_paged_workspace_size", "kv_page_map", "kv_paged_write",
     "paged_decode_attn",
+    "KV_OP_QUANT_WRITE", "KV_OP_QUANT_READ", "KV_OP_QUANT_DECODE", "KV_E4M3", "KV_INT8",
+    "KV_QUANT_BLOCK", "kv_quant_write", "kv_quant_read",
+    "KV_ROTARY_HALF", "KV_ROTARY_INTERLEAVED", "KvRotaryShape", "kv_rotary", "kv_rotary_inv_freq",
 ]
 
 KV_OK, KV_ERR_INVALID_ARG, KV_ERR_UNSUPPORTED, KV_ERR_WORKSPACE = 0, 1, 2, 3
@@ -38,6 +43,10 @@ KV_SCORE_ADA, KV_SCORE_LAVA, KV_SCORE_CRITICAL = 0, 1, 2
 KV_GROUP_MEAN, KV_GROUP_MAX = 0, 1
 KV_OP_SCORE, KV_OP_ALLOCATE, KV_OP_COMPACT, KV_OP_DECODE = 0, 1, 2, 3
 KV_OP_PAGE_MAP, KV_OP_PAGED_WRITE, KV_OP_PAGED_DECODE = 4, 5, 6
+KV_OP_QUANT_WRITE, KV_OP_QUANT_READ, KV_OP_QUANT_DECODE = 16, 17, 18
+KV_E4M3, KV_INT8 = 0, 1
+KV_QUANT_BLOCK = 16
+KV_ROTARY_HALF, KV_ROTARY_INTERLEAVED = 0, 1
 KV_PAGE_MAP_MAX_TABLES = 16384
 KV_PAGED_DECODE_MAX_TABLES = 1 << 20
 KV_TERMS_MEAN_POOLED, KV_TERMS_L2 = 0, 1
@@ -78,6 +87,18 @@ class KvPagedShape(ctypes.Structure):
         if isinstance(dtype, str):
             dtype = KV_BF16 if dtype == "bf16" else KV_F32
         return cls(seqs, hq, hkv, d, tables, page, max_pages, dtype, num_pages, page_stride)
+
+
+class KvRotaryShape(ctypes.Structure):
+    """Heads and pairs of ``kv_rotary``; ``magnitude`` goes with ``kv_rotary_inv_freq``."""
+    _fields_ = [(f, ctypes.c_int32) for f in ("hq", "hkv", "d", "rot", "layout", "dtype")] + \
+               [("magnitude", ctypes.c_float)]
+
+    @classmethod
+    def of(cls, hq, hkv, d, rot, layout, dtype, magnitude=1.0) -> "KvRotaryShape":
+        if isinstance(dtype, str):
+            dtype = KV_BF16 if dtype == "bf16" else KV_F32
+        return cls(hq, hkv, d, rot, layout, dtype, magnitude)
 
 
 class KvError(RuntimeError):
@@ -127,6 +148,12 @@ _SIGS = {
                                       _vp, _vp, _vp, _vp, _sz, _vp]),
     "paged_decode_attn": (ctypes.c_int, [ctypes.POINTER(KvPagedShape), _vp, _vp, _vp, _vp, _vp,
                                          _i64, _vp, _vp, _vp, _vp, _f32, _vp, _vp, _sz, _vp]),
+    "kv_quant_write": (ctypes.c_int, [ctypes.POINTER(KvPagedShape), ctypes.c_int, _vp, _vp, _i64,
+                                      _vp, _i64, _vp, _vp, _vp, _vp, _vp, _vp, _sz, _vp]),
+    "kv_quant_read": (ctypes.c_int, [ctypes.POINTER(KvPagedShape), ctypes.c_int, _vp, _vp, _vp,
+                                     _vp, _vp, _i64, _vp, _vp, _vp, _i64, _vp, _sz, _vp]),
+    "kv_rotary": (ctypes.c_int, [ctypes.POINTER(KvRotaryShape), ctypes.c_int, _vp, _i64, _vp, _i64,
+                                 _vp, _vp, _i64, _vp, _vp, _i64, _vp, _i64, _vp]),
 }
 
 
@@ -305,15 +332,17 @@ def kv_paged_workspace_size(op: int, shape: KvPagedShape) -> int:
 
 
 # torch's dtypes and lookups for the paged calls, set when the first of them runs
-_I32 = _I64 = _device_now = _stream_now = None
+_I32 = _I64 = _F32 = _F64 = _device_now = _stream_now = None
 _ROWS = {}
+_CODES = {}   # types that the codes of a format may come as
 
 
 def _init_torch() -> None:
-    global _I32, _I64, _device_now, _stream_now
+    global _I32, _I64, _F32, _F64, _device_now, _stream_now
     import torch
-    _I32, _I64 = torch.int32, torch.int64
+    _I32, _I64, _F32, _F64 = torch.int32, torch.int64, torch.float32, torch.float64
     _ROWS.update({KV_BF16: torch.bfloat16, KV_F32: torch.float32})
+    _CODES.update({KV_E4M3: (torch.float8_e4m3fn, torch.uint8), KV_INT8: (torch.int8,)})
     _stream_now = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
         lambda dev: torch.cuda.current_stream(dev).cuda_stream)
     torch.cuda.init()   # (current_device() would ask for it on every call)
@@ -469,6 +498,95 @@ def paged_decode_attn(shape: KvPagedShape, q, k_new, v_new, cu_add, slot_map, k_
         _stream_on(stream, dev))
     if st:
         raise KvError("paged_decode_attn", st)
+
+
+def _code_pool(t, format: int, inner: int, pages: int, page_stride: int, dev: int, what: str):
+    """Pointer of a page pool of codes (one byte each)."""
+    types = _CODES.get(format)
+    if types is None:
+        raise ValueError("format must be KV_E4M3 or KV_INT8")
+    el = getattr(t, "dtype", None)
+    return _pool(t, el if el in types else types[0], inner, pages, page_stride, dev, what)
+
+
+def kv_quant_write(shape: KvPagedShape, format: int, k, v, slot_map, n_rows, k_pages, v_pages,
+                   k_scale, v_scale, ws, stream=None) -> None:
+    """``kv_paged_write`` into a cache in 8 bits: ``k_pages`` / ``v_pages`` hold codes (float8 e4m3
+    or uint8 for KV_E4M3, int8 for KV_INT8), ``k_scale`` / ``v_scale`` [num_pages][heads per
+    page][page / 16] float32 the scales of their blocks of 16 rows."""
+    dev = _device(k, "k")
+    heads, pages = shape.hkv // shape.tables, shape.num_pages
+    el, row, inner = _ROWS.get(shape.dtype), heads * shape.d, heads * shape.d * shape.page
+    apart, blocks = shape.page_stride or inner, pages * heads * (shape.page // 16)
+    kp, n, ks = _rows_view(k, el, row, dev, "k")
+    vp, nv, vs = _rows_view(v, el, row, dev, "v")
+    if ks != vs or n != nv:
+        raise ValueError("k and v must have the same rows and row stride")
+    wp, wn = _work(ws, dev)
+    st = lib().kv_quant_write(
+        ctypes.byref(shape), format, kp, vp, ks, _buf(slot_map, _I64, n, dev, "slot_map"), n,
+        _buf(n_rows, _I64, 1, dev, "n_rows"),
+        _code_pool(k_pages, format, inner, pages, apart, dev, "k_pages"),
+        _code_pool(v_pages, format, inner, pages, apart, dev, "v_pages"),
+        _buf(k_scale, _F32, blocks, dev, "k_scale"), _buf(v_scale, _F32, blocks, dev, "v_scale"),
+        wp, wn, _stream_on(stream, dev))
+    if st:
+        raise KvError("kv_quant_write", st)
+
+
+def kv_quant_read(shape: KvPagedShape, format: int, k_pages, v_pages, k_scale, v_scale, slot_map,
+                  n_rows, k, v, ws, stream=None) -> None:
+    """Rows of a cache in 8 bits as values, into rows ``k`` and ``v`` ([n][heads per page][d], rows
+    may lie apart).  ``n_rows`` (a device int64, or None): rows from there on are left out."""
+    dev = _device(k, "k")
+    heads, pages = shape.hkv // shape.tables, shape.num_pages
+    el, row, inner = _ROWS.get(shape.dtype), heads * shape.d, heads * shape.d * shape.page
+    apart, blocks = shape.page_stride or inner, pages * heads * (shape.page // 16)
+    kp, n, ks = _rows_view(k, el, row, dev, "k")
+    vp, nv, vs = _rows_view(v, el, row, dev, "v")
+    if ks != vs or n != nv:
+        raise ValueError("k and v must have the same rows and row stride")
+    wp, wn = _work(ws, dev)
+    st = lib().kv_quant_read(
+        ctypes.byref(shape), format,
+        _code_pool(k_pages, format, inner, pages, apart, dev, "k_pages"),
+        _code_pool(v_pages, format, inner, pages, apart, dev, "v_pages"),
+        _buf(k_scale, _F32, blocks, dev, "k_scale"), _buf(v_scale, _F32, blocks, dev, "v_scale"),
+        _buf(slot_map, _I64, n, dev, "slot_map"), n, _buf(n_rows, _I64, 1, dev, "n_rows"), kp, vp,
+        ks, wp, wn, _stream_on(stream, dev))
+    if st:
+        raise KvError("kv_quant_read", st)
+
+
+def kv_rotary(shape: KvRotaryShape, q, k, positions, inv_freq, q_out, k_out, n_rows=None,
+              back: bool = False, stream=None) -> None:
+    """Rotary positions of ``q`` ([n][hq][d]) and ``k`` ([n][hkv][d], None for 0 heads), rows may
+    lie apart; in place where an output is its input.  ``positions`` int32 (rows below 0 are left
+    alone), ``inv_freq`` [rot / 2] float64 on the device (``kv_rotary_inv_freq``).  ``back``:
+    turned back, which is the gradient.  ``n_rows`` (a device int64, or None): rows from there on
+    are left out."""
+    dev = _device(positions, "positions")
+    el, n, sides = _ROWS.get(shape.dtype), None, []
+    for heads, pair in ((shape.hq, ((q, "q"), (q_out, "q_out"))),
+                        (shape.hkv, ((k, "k"), (k_out, "k_out")))):
+        for t, what in pair:
+            if heads == 0:
+                sides += (None, 0)
+                continue
+            p, rows, stride = _rows_view(t, el, heads * shape.d, dev, what)
+            if n is not None and rows != n:
+                raise ValueError("%s has %d rows, others %d" % (what, rows, n))
+            n = rows
+            sides += (p, stride)
+    n = n or 0
+    qp, qs, qop, qos, kp, ks, kop, kos = sides
+    st = lib().kv_rotary(
+        ctypes.byref(shape), 1 if back else 0, qp, qs, kp, ks,
+        _buf(positions, _I32, n, dev, "positions"),
+        _buf(inv_freq, _F64, shape.rot // 2, dev, "inv_freq"), n,
+        _buf(n_rows, _I64, 1, dev, "n_rows"), qop, qos, kop, kos, _stream_on(stream, dev))
+    if st:
+        raise KvError("kv_rotary", st)
 
 
 def kv_check_device_status(ws, stream=None) -> int:

@@ -208,6 +208,27 @@ cudaError_t launch_paged_decode(const PagedShape& s, const void* q, const void* 
                                 void* kp, void* vp, const int32_t* table, const int32_t* lens,
                                 float scale, void* out, char* ws, cudaStream_t st);
 
+// ----------------------------- cache in 8 bits ------------------------------
+cudaError_t launch_quant_write(const PagedShape& s, int format, const void* k, const void* v,
+                               int64_t src_stride, const int64_t* slots, int64_t rows,
+                               const int64_t* n_rows, void* kp, void* vp, float* ks, float* vs,
+                               WsHeader* hdr, cudaStream_t st);
+cudaError_t launch_quant_read(const PagedShape& s, int format, const void* kp, const void* vp,
+                              const float* ks, const float* vs, const int64_t* slots, int64_t rows,
+                              const int64_t* n_rows, void* k, void* v, int64_t dst_stride,
+                              WsHeader* hdr, cudaStream_t st);
+
+// ----------------------------- rotary positions -----------------------------
+struct RotaryShape {
+  int hq, hkv, d, rot, layout, dtype;
+  float magnitude;
+  int esize() const { return dtype == KV_BF16 ? 2 : 4; }
+};
+cudaError_t launch_rotary(const RotaryShape& s, bool back, const void* q, int64_t q_stride,
+                          const void* k, int64_t k_stride, const int32_t* pos, const double* freq,
+                          int64_t rows, const int64_t* n_rows, void* q_out, int64_t qo_stride,
+                          void* k_out, int64_t ko_stride, cudaStream_t st);
+
 int num_sms();
 // Largest dynamic + static shared memory one CTA may opt in to.
 size_t max_smem_optin();

@@ -96,6 +96,21 @@ static bool aligned_to(const void* p, uintptr_t a) {
   return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0;
 }
 
+// The same for the cache in 8 bits, whose pages are bytes.
+static kv_status quant_shape_check(const kv_paged_shape* sh, PagedShape* out) {
+  if (sh == nullptr) return KV_ERR_INVALID_ARG;
+  kv_paged_shape dense = *sh;
+  dense.page_stride = 0;
+  const kv_status st = paged_shape_check(&dense, out);
+  if (st != KV_OK) return st;
+  if (out->page < KV_QUANT_BLOCK || out->d % 16 != 0) return KV_ERR_UNSUPPORTED;
+  if (sh->page_stride == 0) return KV_OK;
+  if (sh->page_stride < out->page_stride || sh->page_stride % 16 != 0) return KV_ERR_INVALID_ARG;
+  if (sh->page_stride >= (int64_t)1 << 40) return KV_ERR_UNSUPPORTED;
+  out->page_stride = sh->page_stride;
+  return KV_OK;
+}
+
 static kv_status cuda_status(cudaError_t e) { return e == cudaSuccess ? KV_OK : KV_ERR_CUDA; }
 
 // The shape of a model-wide selection (kv_allocate layer_entropy_mode 2): the L layers of a
@@ -494,6 +509,10 @@ kv_status flat_decode_attn(const kv_shape* shape, const void* q, const void* k_n
 
 size_t kv_paged_workspace_size(int op, const kv_paged_shape* shape) {
   PagedShape s;
+  if (op >= KV_OP_QUANT_WRITE && op <= KV_OP_QUANT_DECODE) {
+    if (quant_shape_check(shape, &s) != KV_OK) return 0;
+    return op == KV_OP_QUANT_DECODE ? paged_decode_ws_bytes(s) : kWsHeader;
+  }
   if (paged_shape_check(shape, &s) != KV_OK) return 0;
   switch (op) {
     case KV_OP_PAGE_MAP: return kPageMapWsBytes;
@@ -596,6 +615,119 @@ kv_status paged_decode_attn(const kv_paged_shape* shape, const void* q, const vo
                                          k_pages, v_pages, block_table, lens, softmax_scale, out,
                                          static_cast<char*>(ws),
                                          static_cast<cudaStream_t>(stream)));
+}
+
+// What kv_quant_write and kv_quant_read check alike.  `rows_stride` becomes that of dense rows
+// where it is 0; *work is false where there is nothing to do.
+static kv_status quant_rows_check(const kv_paged_shape* shape, int format, const void* k,
+                                  const void* v, int64_t* rows_stride, const int64_t* slot_map,
+                                  int64_t rows, const int64_t* n_rows, const void* k_pages,
+                                  const void* v_pages, const float* k_scale, const float* v_scale,
+                                  const void* ws, size_t ws_bytes, PagedShape* s, bool* work) {
+  *work = false;
+  const kv_status st = quant_shape_check(shape, s);
+  if (st != KV_OK) return st;
+  if (format != KV_E4M3 && format != KV_INT8) return KV_ERR_INVALID_ARG;
+  if (ws == nullptr || !aligned16(ws)) return KV_ERR_INVALID_ARG;
+  if (rows < 0 || rows > INT32_MAX || *rows_stride < 0) return KV_ERR_INVALID_ARG;
+  if (s->seqs == 0 || rows == 0) return KV_OK;
+  if (k == nullptr || v == nullptr || slot_map == nullptr || k_pages == nullptr ||
+      v_pages == nullptr || k_scale == nullptr || v_scale == nullptr)
+    return KV_ERR_INVALID_ARG;
+  if (!aligned16(k) || !aligned16(v) || !aligned16(k_pages) || !aligned16(v_pages) ||
+      !aligned_to(k_scale, 4) || !aligned_to(v_scale, 4) || !aligned_to(slot_map, 8) ||
+      !aligned_to(n_rows, 8))
+    return KV_ERR_INVALID_ARG;
+  const int64_t dense = (int64_t)s->Hp() * s->d;
+  if (*rows_stride == 0) *rows_stride = dense;
+  if (*rows_stride < dense || *rows_stride % (16 / s->esize()) != 0 ||
+      *rows_stride > ((int64_t)1 << 31))
+    return KV_ERR_INVALID_ARG;
+  if (ws_bytes < kWsHeader) return KV_ERR_WORKSPACE;
+  *work = true;
+  return KV_OK;
+}
+
+kv_status kv_quant_write(const kv_paged_shape* shape, int format, const void* k, const void* v,
+                         int64_t src_stride, const int64_t* slot_map, int64_t rows,
+                         const int64_t* n_rows, void* k_pages, void* v_pages, float* k_scale,
+                         float* v_scale, void* ws, size_t ws_bytes, void* stream) {
+  PagedShape s;
+  bool work;
+  const kv_status st = quant_rows_check(shape, format, k, v, &src_stride, slot_map, rows, n_rows,
+                                        k_pages, v_pages, k_scale, v_scale, ws, ws_bytes, &s,
+                                        &work);
+  if (st != KV_OK || !work) return st;
+  return cuda_status(launch_quant_write(s, format, k, v, src_stride, slot_map, rows, n_rows,
+                                        k_pages, v_pages, k_scale, v_scale,
+                                        static_cast<WsHeader*>(ws),
+                                        static_cast<cudaStream_t>(stream)));
+}
+
+kv_status kv_quant_read(const kv_paged_shape* shape, int format, const void* k_pages,
+                        const void* v_pages, const float* k_scale, const float* v_scale,
+                        const int64_t* slot_map, int64_t rows, const int64_t* n_rows, void* k,
+                        void* v, int64_t dst_stride, void* ws, size_t ws_bytes, void* stream) {
+  PagedShape s;
+  bool work;
+  const kv_status st = quant_rows_check(shape, format, k, v, &dst_stride, slot_map, rows, n_rows,
+                                        k_pages, v_pages, k_scale, v_scale, ws, ws_bytes, &s,
+                                        &work);
+  if (st != KV_OK || !work) return st;
+  return cuda_status(launch_quant_read(s, format, k_pages, v_pages, k_scale, v_scale, slot_map,
+                                       rows, n_rows, k, v, dst_stride, static_cast<WsHeader*>(ws),
+                                       static_cast<cudaStream_t>(stream)));
+}
+
+kv_status kv_rotary(const kv_rotary_shape* shape, int back, const void* q, int64_t q_stride,
+                    const void* k, int64_t k_stride, const int32_t* positions,
+                    const double* inv_freq, int64_t rows, const int64_t* n_rows, void* q_out,
+                    int64_t q_out_stride, void* k_out, int64_t k_out_stride, void* stream) {
+  if (shape == nullptr) return KV_ERR_INVALID_ARG;
+  const RotaryShape s{shape->hq, shape->hkv, shape->d, shape->rot, shape->layout, shape->dtype,
+                      shape->magnitude};
+  if (s.hq < 0 || s.hkv < 0 || s.hq + (int64_t)s.hkv == 0 || s.d <= 0 || s.rot <= 0 || s.rot > s.d)
+    return KV_ERR_INVALID_ARG;
+  if (s.d % 8 != 0 || s.rot % 2 != 0) return KV_ERR_INVALID_ARG;
+  if (s.layout != KV_ROTARY_HALF && s.layout != KV_ROTARY_INTERLEAVED) return KV_ERR_INVALID_ARG;
+  if (s.dtype != KV_BF16 && s.dtype != KV_F32) return KV_ERR_INVALID_ARG;
+  if (!std::isfinite(s.magnitude)) return KV_ERR_INVALID_ARG;
+  if (s.d > 256 || s.rot % 8 != 0 || s.hq > 4096 || s.hkv > 4096) return KV_ERR_UNSUPPORTED;
+  if (rows < 0 || rows > INT32_MAX) return KV_ERR_INVALID_ARG;
+  struct Side {
+    int heads;
+    const void* in;
+    const void* out;
+    int64_t *in_stride, *out_stride;
+  } sides[2] = {{s.hq, q, q_out, &q_stride, &q_out_stride},
+                {s.hkv, k, k_out, &k_stride, &k_out_stride}};
+  for (const Side& x : sides) {
+    const int64_t dense = (int64_t)x.heads * s.d;
+    for (int64_t* stride : {x.in_stride, x.out_stride}) {
+      if (*stride == 0) *stride = dense;
+      if (*stride < dense || *stride % (16 / s.esize()) != 0 || *stride > ((int64_t)1 << 31))
+        return KV_ERR_INVALID_ARG;
+    }
+  }
+  if (rows == 0) return KV_OK;
+  if (positions == nullptr || inv_freq == nullptr) return KV_ERR_INVALID_ARG;
+  if (!aligned_to(positions, 4) || !aligned_to(inv_freq, 8) || !aligned_to(n_rows, 8))
+    return KV_ERR_INVALID_ARG;
+  for (const Side& x : sides) {
+    if (x.heads == 0) continue;
+    if (x.in == nullptr || x.out == nullptr || !aligned16(x.in) || !aligned16(x.out))
+      return KV_ERR_INVALID_ARG;
+    // in place, or apart from the rows that are read
+    const char *p = static_cast<const char*>(x.in), *o = static_cast<const char*>(x.out);
+    const int64_t row = (int64_t)x.heads * s.d;
+    const int64_t in_bytes = ((rows - 1) * *x.in_stride + row) * s.esize();
+    const int64_t out_bytes = ((rows - 1) * *x.out_stride + row) * s.esize();
+    if (p == o ? *x.in_stride != *x.out_stride && rows > 1 : p < o + out_bytes && o < p + in_bytes)
+      return KV_ERR_INVALID_ARG;
+  }
+  return cuda_status(launch_rotary(s, back != 0, q, q_stride, k, k_stride, positions, inv_freq,
+                                   rows, n_rows, q_out, q_out_stride, k_out, k_out_stride,
+                                   static_cast<cudaStream_t>(stream)));
 }
 
 kv_status kv_check_device_status(void* ws, void* stream, uint32_t* info) {

@@ -1,0 +1,158 @@
+// Numbers of the 8-bit cache: codes, and the scale of a block of 16 rows of one head.
+//
+// A value is code * scale, with scale a power of two 2^t:  t is the smallest, from kLeast on, with
+//   largest finite |x| of the block <= kMost 2^t,        kMost = 448 (e4m3) or 127 (int8).
+// A power of two costs at most one bit of the code's range.  What it buys: x / 2^t and code * 2^t
+// are exact, so a value is rounded once, by its code alone, and a block that moves to a larger
+// scale rounds again only what falls below the code's last place (in e4m3 what is subnormal there).
+// kLeast keeps scales and their reciprocals normal floats with room for the attention's factors:
+// values below 2^-9 2^kLeast (1.2e-31 in e4m3) become zero.
+//
+// Infinities become the code's largest number and do not count for the scale; a NaN is a NaN in
+// e4m3 and zero in int8.
+#pragma once
+
+#include <cuda_fp16.h>
+
+#include "kv_internal.cuh"
+
+namespace kv {
+namespace quant {
+
+constexpr int kBlock = 16;     // rows
+constexpr int kLeast = -96;
+
+struct E4M3 {
+  // 448 = 0.875 * 2^9: a mantissa past 0.875 (1.75 as 1.m) needs a step more
+  static constexpr int kTopExp = 9;
+  static constexpr uint32_t kTopMant = 0x600000u;
+  // two codes, x in the low byte
+  static __device__ __forceinline__ uint32_t pack2(float x, float y) {
+    uint16_t r;
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(y), "f"(x));
+    return r;
+  }
+  static __device__ __forceinline__ uint32_t pack4(float x, float y, float z, float w) {
+    return pack2(x, y) | pack2(z, w) << 16;
+  }
+  // the numbers of a word's codes 0, 1 and 2, 3
+  static __device__ __forceinline__ void halves(uint32_t w, uint32_t& lo, uint32_t& hi) {
+    asm("{\n\t.reg .b16 l, h;\n\t"
+        "mov.b32 {l, h}, %2;\n\t"
+        "cvt.rn.f16x2.e4m3x2 %0, l;\n\t"
+        "cvt.rn.f16x2.e4m3x2 %1, h;\n\t}"
+        : "=r"(lo), "=r"(hi)
+        : "r"(w));
+  }
+};
+
+struct Int8 {
+  // 127 = 0.9921875 * 2^7
+  static constexpr int kTopExp = 7;
+  static constexpr uint32_t kTopMant = 0x7E0000u;
+  static __device__ __forceinline__ uint32_t pack4(float x, float y, float z, float w) {
+    const int a = max(__float2int_rn(x), -127), b = max(__float2int_rn(y), -127);
+    const int c = max(__float2int_rn(z), -127), d = max(__float2int_rn(w), -127);
+    uint32_t hi, r;
+    asm("cvt.pack.sat.s8.s32.b32 %0, %1, %2, %3;" : "=r"(hi) : "r"(d), "r"(c), "r"(0));
+    asm("cvt.pack.sat.s8.s32.b32 %0, %1, %2, %3;" : "=r"(r) : "r"(b), "r"(a), "r"(hi));
+    return r;
+  }
+  // code + 128 in the last places of 1024: less 1152 it is the code, exactly
+  static __device__ __forceinline__ uint32_t less(uint32_t x) {
+    uint32_t r;
+    asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(x), "r"(0x64806480u));
+    return r;
+  }
+  static __device__ __forceinline__ void halves(uint32_t w, uint32_t& lo, uint32_t& hi) {
+    w ^= 0x80808080u;
+    lo = less(__byte_perm(w, 0x64646464u, 0x4140));
+    hi = less(__byte_perm(w, 0x64646464u, 0x4342));
+  }
+};
+
+__device__ __forceinline__ float2 floats_of(uint32_t h2) {
+  return __half22float2(*reinterpret_cast<const __half2*>(&h2));
+}
+
+// Bits of the larger of m and |x|, non-finite ones left out (m: bits of a finite magnitude).
+__device__ __forceinline__ uint32_t finite_max(uint32_t m, float x) {
+  const uint32_t u = __float_as_uint(x) & 0x7FFFFFFFu;
+  return u < 0x7F800000u && u > m ? u : m;
+}
+
+// The scale of a block whose largest finite magnitude has the bits `top`.
+template <typename F>
+__device__ __forceinline__ float scale_for(uint32_t top) {
+  int t = (int)(top >> 23) - 126 - F::kTopExp + ((top & 0x7FFFFFu) > F::kTopMant ? 1 : 0);
+  t = t < kLeast ? kLeast : t;
+  return __uint_as_float((uint32_t)(t + 127) << 23);
+}
+
+// 16 codes of a piece at another scale: rounded times `by`.
+template <typename F>
+__device__ __forceinline__ uint4 again(uint4 c, float by) {
+  uint32_t* w = reinterpret_cast<uint32_t*>(&c);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    uint32_t lo, hi;
+    F::halves(w[i], lo, hi);
+    const float2 a = floats_of(lo), b = floats_of(hi);
+    w[i] = F::pack4(a.x * by, a.y * by, b.x * by, b.y * by);
+  }
+  return c;
+}
+
+// 16 elements of a row, as loaded.
+template <typename T>
+struct Piece;
+template <>
+struct Piece<float> {
+  static constexpr int kLoads = 4;   // of 16 bytes
+  uint4 w[kLoads];
+  __device__ __forceinline__ float at(int i) const {
+    return __uint_as_float(reinterpret_cast<const uint32_t*>(w)[i]);
+  }
+  __device__ __forceinline__ uint32_t top(uint32_t m) const {
+#pragma unroll
+    for (int i = 0; i < 16; ++i) m = finite_max(m, at(i));
+    return m;
+  }
+};
+template <>
+struct Piece<__nv_bfloat16> {
+  static constexpr int kLoads = 2;
+  uint4 w[kLoads];
+  __device__ __forceinline__ float at(int i) const {
+    const uint32_t x = reinterpret_cast<const uint32_t*>(w)[i >> 1];
+    return __uint_as_float(i & 1 ? x & 0xFFFF0000u : x << 16);
+  }
+  __device__ __forceinline__ uint32_t top(uint32_t m) const {
+    // both halves at a time; one by one where a half is not finite
+    uint32_t p = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      p = __vmaxu2(p, reinterpret_cast<const uint32_t*>(w)[i] & 0x7FFF7FFFu);
+    const uint32_t lo = p << 16, hi = p & 0xFFFF0000u, x = lo > hi ? lo : hi;
+    if (x < 0x7F800000u) return x > m ? x : m;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const uint32_t y = reinterpret_cast<const uint32_t*>(w)[i];
+      m = finite_max(finite_max(m, __uint_as_float(y << 16)), __uint_as_float(y & 0xFFFF0000u));
+    }
+    return m;
+  }
+};
+template <typename F, typename T>
+__device__ __forceinline__ uint4 encode(const Piece<T>& x, float inv) {
+  uint4 c;
+  uint32_t* w = reinterpret_cast<uint32_t*>(&c);
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    w[i] = F::pack4(x.at(4 * i) * inv, x.at(4 * i + 1) * inv, x.at(4 * i + 2) * inv,
+                    x.at(4 * i + 3) * inv);
+  return c;
+}
+
+}  // namespace quant
+}  // namespace kv

@@ -1,0 +1,144 @@
+// Rows of the 8-bit cache as the values they stand for: code * scale, which bf16 and fp32 hold
+// exactly.  Bound by reading the codes and writing the rows once.
+#include "quant_codes.cuh"
+#include "tc_ptx.cuh"
+
+namespace kv {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kPieces = 4;   // pieces of 16 codes of K (and of V) of a lane at a time
+
+struct QReadArgs {
+  const unsigned char *kp, *vp;
+  const float *ks, *vs;
+  const int64_t* slots;
+  const int64_t* n_rows;
+  uint4 *k, *v;
+  WsHeader* hdr;
+  int64_t rows, dst_vec, page_stride, num_slots;   // dst_vec: 16-byte pieces from row to row
+  int per_row, pad_shift;    // pieces of a row, and log2 of its padded pieces (7: whole groups)
+  int Hp, d, shift;
+};
+
+template <typename T, typename F>
+__device__ __forceinline__ void put(uint4* dst, uint4 c, float s) {
+  const uint32_t* w = reinterpret_cast<const uint32_t*>(&c);
+#pragma unroll
+  for (int i = 0; i < 4; i += (sizeof(T) == 2 ? 2 : 1)) {
+    uint4 o;
+    uint32_t* x = reinterpret_cast<uint32_t*>(&o);
+    uint32_t lo, hi;
+    F::halves(w[i], lo, hi);
+    float2 a = quant::floats_of(lo), b = quant::floats_of(hi);
+    if (sizeof(T) == 4) {
+      o = make_uint4(__float_as_uint(a.x * s), __float_as_uint(a.y * s), __float_as_uint(b.x * s),
+                     __float_as_uint(b.y * s));
+      dst[i] = o;
+    } else {
+      auto two = [&](float p, float q) {
+        const __nv_bfloat162 y = __floats2bfloat162_rn(p * s, q * s);
+        return *reinterpret_cast<const uint32_t*>(&y);
+      };
+      x[0] = two(a.x, a.y);
+      x[1] = two(b.x, b.y);
+      F::halves(w[i + 1 < 4 ? i + 1 : i], lo, hi);
+      a = quant::floats_of(lo);
+      b = quant::floats_of(hi);
+      x[2] = two(a.x, a.y);
+      x[3] = two(b.x, b.y);
+      dst[i / 2] = o;
+    }
+  }
+}
+
+template <typename T, typename F>
+__global__ void __launch_bounds__(kThreads) quant_read_kernel(const __grid_constant__ QReadArgs a) {
+  constexpr int kOut = (int)sizeof(T);   // 16-byte pieces out of a piece of 16 codes
+  const int lane = threadIdx.x & 31, page = 1 << a.shift, dv = a.d / 16;
+  ptx::griddep_launch_dependents();
+  ptx::griddep_wait();   // nothing of the call before is read or written until it ends
+  int64_t rows = a.rows;
+  if (a.n_rows != nullptr) rows = min(rows, *a.n_rows);
+  const int in_group = 128 >> a.pad_shift;   // rows
+  const int64_t warp = (int64_t)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
+  const int64_t step = (int64_t)gridDim.x * (kThreads / 32) * in_group;
+  for (int64_t row0 = warp * in_group; row0 < rows; row0 += step) {
+    for (int x0 = 0; x0 < a.per_row; x0 += 128) {
+      uint4 kc[kPieces], vc[kPieces];
+      float ks[kPieces], vs[kPieces];
+      bool in[kPieces];
+#pragma unroll
+      for (int j = 0; j < kPieces; ++j) {
+        const int i = lane + 32 * j;
+        const int64_t row = row0 + (i >> a.pad_shift);
+        const int x = x0 + (i & ((1 << a.pad_shift) - 1));
+        in[j] = false;
+        if (x < a.per_row && row < rows) {
+          const int64_t slot = a.slots[row];
+          in[j] = slot >= 0 && slot < a.num_slots;
+          if (in[j]) {
+            const int64_t pg = slot >> a.shift;
+            const int r = (int)(slot & (page - 1)), h = x / dv;
+            const int64_t at = pg * a.page_stride + ((int64_t)h * page + r) * a.d + (x - h * dv) * 16;
+            const int64_t sc = (pg * a.Hp + h) * (page / quant::kBlock) + r / quant::kBlock;
+            kc[j] = *reinterpret_cast<const uint4*>(a.kp + at);
+            vc[j] = *reinterpret_cast<const uint4*>(a.vp + at);
+            ks[j] = a.ks[sc];
+            vs[j] = a.vs[sc];
+          } else if (slot != -1) {
+            raise_dev(a.hdr, DEV_PAGE_ID, (unsigned)row);
+          }
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < kPieces; ++j) {
+        if (!in[j]) continue;
+        const int i = lane + 32 * j;
+        const int64_t row = row0 + (i >> a.pad_shift);
+        const int x = x0 + (i & ((1 << a.pad_shift) - 1));
+        put<T, F>(a.k + row * a.dst_vec + x * kOut, kc[j], ks[j]);
+        put<T, F>(a.v + row * a.dst_vec + x * kOut, vc[j], vs[j]);
+      }
+    }
+  }
+}
+
+template <typename T, typename F>
+cudaError_t launch(const QReadArgs& a, cudaStream_t st) {
+  int64_t grid = cdiv(a.rows, (int64_t)(128 >> a.pad_shift) * (kThreads / 32));
+  const int64_t most = (int64_t)num_sms() * 8;
+  if (grid > most) grid = most;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3((unsigned)grid);
+  cfg.blockDim = dim3(kThreads);
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1] = {pdl_attribute()};
+  cfg.attrs = attr;
+  cfg.numAttrs = grid == most ? 1 : 0;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, quant_read_kernel<T, F>, a);
+  if (e == cudaSuccess) count_launches(1);
+  return e;
+}
+}  // namespace
+
+cudaError_t launch_quant_read(const PagedShape& s, int format, const void* kp, const void* vp,
+                              const float* ks, const float* vs, const int64_t* slots, int64_t rows,
+                              const int64_t* n_rows, void* k, void* v, int64_t dst_stride,
+                              WsHeader* hdr, cudaStream_t st) {
+  int shift = 0;
+  while ((1 << shift) < s.page) ++shift;
+  const int per_row = s.Hp() * (s.d / 16);
+  int pad = 0;
+  while (pad < 7 && (1 << pad) < per_row) ++pad;
+  const QReadArgs a{(const unsigned char*)kp, (const unsigned char*)vp, ks, vs, slots, n_rows,
+                    (uint4*)k, (uint4*)v, hdr, rows, dst_stride * s.esize() / 16, s.page_stride,
+                    s.num_pages << shift, per_row, pad, s.Hp(), s.d, shift};
+  if (s.dtype == KV_BF16)
+    return format == KV_E4M3 ? launch<__nv_bfloat16, quant::E4M3>(a, st)
+                             : launch<__nv_bfloat16, quant::Int8>(a, st);
+  return format == KV_E4M3 ? launch<float, quant::E4M3>(a, st)
+                           : launch<float, quant::Int8>(a, st);
+}
+
+}  // namespace kv
