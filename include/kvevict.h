@@ -623,6 +623,27 @@ KV_API kv_status kv_quant_read(const kv_paged_shape* shape, int format, const vo
                                void* stream);
 
 /*
+ * quant_decode_attn -- paged_decode_attn over the cache in 8 bits: the new token's row of each table
+ * that gained one is stored as kv_quant_write stores it (its block's earlier rows follow a raised
+ * scale), and attention is over the values that the cache then holds.
+ *
+ * Arguments, layouts, checks and limits as in paged_decode_attn, with format, k_scale and v_scale as
+ * above.  A table's slot has to be the place that its block table gives row lens - 1 (kv_page_map's
+ * is): at any other one in the pool the row is not stored, and the error word is set (10).
+ * Sums, the softmax and out before its rounding are float32 (fp32 q is held to 22 bits, the softmax
+ * numerators to 22 bits or 2^-50 of the largest; bf16 q and the values are exact).  q, the values attended to and their scores
+ * have to be finite (a NaN among them makes the outputs it reaches NaN, an infinity may).  Every
+ * result is the same in every run.
+ */
+KV_API kv_status quant_decode_attn(const kv_paged_shape* shape, int format, const void* q,
+                                   const void* k_new, const void* v_new, const int64_t* cu_add,
+                                   const int64_t* slot_map, int64_t slot_capacity, void* k_pages,
+                                   void* v_pages, float* k_scale, float* v_scale,
+                                   const int32_t* block_table, const int32_t* lens,
+                                   float softmax_scale, void* out, void* ws, size_t ws_bytes,
+                                   void* stream);
+
+/*
  * Rotary positions: pairs of columns of queries and keys turned by their position, before the keys
  * are scored or cached.  (The method's pages take rotated rows as given.)
  */

@@ -32,7 +32,7 @@ __all__ = [
     "KvPagedShape", "kv_paged_workspace_size", "kv_page_map", "kv_paged_write",
     "paged_decode_attn",
     "KV_OP_QUANT_WRITE", "KV_OP_QUANT_READ", "KV_OP_QUANT_DECODE", "KV_E4M3", "KV_INT8",
-    "KV_QUANT_BLOCK", "kv_quant_write", "kv_quant_read",
+    "KV_QUANT_BLOCK", "kv_quant_write", "kv_quant_read", "quant_decode_attn",
     "KV_ROTARY_HALF", "KV_ROTARY_INTERLEAVED", "KvRotaryShape", "kv_rotary", "kv_rotary_inv_freq",
 ]
 
@@ -152,6 +152,9 @@ _SIGS = {
                                       _vp, _i64, _vp, _vp, _vp, _vp, _vp, _vp, _sz, _vp]),
     "kv_quant_read": (ctypes.c_int, [ctypes.POINTER(KvPagedShape), ctypes.c_int, _vp, _vp, _vp,
                                      _vp, _vp, _i64, _vp, _vp, _vp, _i64, _vp, _sz, _vp]),
+    "quant_decode_attn": (ctypes.c_int, [ctypes.POINTER(KvPagedShape), ctypes.c_int, _vp, _vp, _vp,
+                                         _vp, _vp, _i64, _vp, _vp, _vp, _vp, _vp, _vp, _f32, _vp,
+                                         _vp, _sz, _vp]),
     "kv_rotary": (ctypes.c_int, [ctypes.POINTER(KvRotaryShape), ctypes.c_int, _vp, _i64, _vp, _i64,
                                  _vp, _vp, _i64, _vp, _vp, _i64, _vp, _i64, _vp]),
 }
@@ -556,6 +559,32 @@ def kv_quant_read(shape: KvPagedShape, format: int, k_pages, v_pages, k_scale, v
         ks, wp, wn, _stream_on(stream, dev))
     if st:
         raise KvError("kv_quant_read", st)
+
+
+def quant_decode_attn(shape: KvPagedShape, format: int, q, k_new, v_new, cu_add, slot_map, k_pages,
+                      v_pages, k_scale, v_scale, block_table, lens, softmax_scale: float, out, ws,
+                      stream=None) -> None:
+    """``paged_decode_attn`` over a cache in 8 bits (``kv_quant_write`` has the pools)."""
+    dev = _device(q, "q")
+    el, seqs, hkv, d, tables = _ROWS.get(shape.dtype), shape.seqs, shape.hkv, shape.d, shape.tables
+    n, nq, nk, pages = seqs * tables, seqs * shape.hq * d, seqs * hkv * d, shape.num_pages
+    heads, page = hkv // tables, shape.page
+    inner, blocks = heads * page * d, pages * heads * (page // 16)
+    apart = shape.page_stride or inner
+    wp, wn = _work(ws, dev)
+    st = lib().quant_decode_attn(
+        ctypes.byref(shape), format, _buf(q, el, nq, dev, "q"),
+        _buf(k_new, el, nk, dev, "k_new"), _buf(v_new, el, nk, dev, "v_new"),
+        _buf(cu_add, _I64, n + 1, dev, "cu_add"), _buf(slot_map, _I64, 0, dev, "slot_map"),
+        0 if slot_map is None else slot_map.numel(),
+        _code_pool(k_pages, format, inner, pages, apart, dev, "k_pages"),
+        _code_pool(v_pages, format, inner, pages, apart, dev, "v_pages"),
+        _buf(k_scale, _F32, blocks, dev, "k_scale"), _buf(v_scale, _F32, blocks, dev, "v_scale"),
+        _buf(block_table, _I32, n * shape.max_pages, dev, "block_table"),
+        _buf(lens, _I32, n, dev, "lens"), softmax_scale, _buf(out, el, nq, dev, "out"), wp, wn,
+        _stream_on(stream, dev))
+    if st:
+        raise KvError("quant_decode_attn", st)
 
 
 def kv_rotary(shape: KvRotaryShape, q, k, positions, inv_freq, q_out, k_out, n_rows=None,

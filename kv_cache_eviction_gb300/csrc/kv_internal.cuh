@@ -218,6 +218,12 @@ cudaError_t launch_quant_read(const PagedShape& s, int format, const void* kp, c
                               const int64_t* n_rows, void* k, void* v, int64_t dst_stride,
                               WsHeader* hdr, cudaStream_t st);
 
+cudaError_t launch_quant_decode(const PagedShape& s, int format, const void* q, const void* kn,
+                                const void* vn, const int64_t* cu, const int64_t* slots,
+                                int64_t slot_capacity, void* kp, void* vp, float* ks, float* vs,
+                                const int32_t* table, const int32_t* lens, float scale, void* out,
+                                char* ws, cudaStream_t st);
+
 // ----------------------------- rotary positions -----------------------------
 struct RotaryShape {
   int hq, hkv, d, rot, layout, dtype;

@@ -582,14 +582,16 @@ kv_status kv_paged_write(const kv_paged_shape* shape, const void* k, const void*
                                         static_cast<cudaStream_t>(stream)));
 }
 
-kv_status paged_decode_attn(const kv_paged_shape* shape, const void* q, const void* k_new,
-                            const void* v_new, const int64_t* cu_add, const int64_t* slot_map,
-                            int64_t slot_capacity, void* k_pages, void* v_pages,
-                            const int32_t* block_table, const int32_t* lens, float softmax_scale,
-                            void* out, void* ws, size_t ws_bytes, void* stream) {
-  PagedShape s;
-  const kv_status st = paged_shape_check(shape, &s);
-  if (st != KV_OK) return st;
+// What paged_decode_attn and quant_decode_attn check alike, after the shape.  *work is false where
+// there is nothing to do.
+static kv_status paged_decode_check(const PagedShape& s, const void* q, const void* k_new,
+                                    const void* v_new, const int64_t* cu_add,
+                                    const int64_t* slot_map, int64_t slot_capacity,
+                                    const void* k_pages, const void* v_pages,
+                                    const int32_t* block_table, const int32_t* lens,
+                                    float softmax_scale, const void* out, const void* ws,
+                                    size_t ws_bytes, bool* work) {
+  *work = false;
   if (ws == nullptr || !aligned16(ws)) return KV_ERR_INVALID_ARG;
   if ((k_new == nullptr) != (v_new == nullptr)) return KV_ERR_INVALID_ARG;
   if (!(std::fabs(softmax_scale) < 0x1p127f)) return KV_ERR_INVALID_ARG;   // times log2 e is finite
@@ -611,8 +613,47 @@ kv_status paged_decode_attn(const kv_paged_shape* shape, const void* q, const vo
       (int64_t)s.seqs * s.Hkv > (((int64_t)1 << 34) - 1) / ((int64_t)s.max_pages * s.page))
     return KV_ERR_UNSUPPORTED;
   if (ws_bytes < paged_decode_ws_bytes(s)) return KV_ERR_WORKSPACE;
+  *work = true;
+  return KV_OK;
+}
+
+kv_status paged_decode_attn(const kv_paged_shape* shape, const void* q, const void* k_new,
+                            const void* v_new, const int64_t* cu_add, const int64_t* slot_map,
+                            int64_t slot_capacity, void* k_pages, void* v_pages,
+                            const int32_t* block_table, const int32_t* lens, float softmax_scale,
+                            void* out, void* ws, size_t ws_bytes, void* stream) {
+  PagedShape s;
+  bool work;
+  kv_status st = paged_shape_check(shape, &s);
+  if (st != KV_OK) return st;
+  st = paged_decode_check(s, q, k_new, v_new, cu_add, slot_map, slot_capacity, k_pages, v_pages,
+                          block_table, lens, softmax_scale, out, ws, ws_bytes, &work);
+  if (st != KV_OK || !work) return st;
   return cuda_status(launch_paged_decode(s, q, k_new, v_new, cu_add, slot_map, slot_capacity,
                                          k_pages, v_pages, block_table, lens, softmax_scale, out,
+                                         static_cast<char*>(ws),
+                                         static_cast<cudaStream_t>(stream)));
+}
+
+kv_status quant_decode_attn(const kv_paged_shape* shape, int format, const void* q,
+                            const void* k_new, const void* v_new, const int64_t* cu_add,
+                            const int64_t* slot_map, int64_t slot_capacity, void* k_pages,
+                            void* v_pages, float* k_scale, float* v_scale,
+                            const int32_t* block_table, const int32_t* lens, float softmax_scale,
+                            void* out, void* ws, size_t ws_bytes, void* stream) {
+  PagedShape s;
+  bool work;
+  kv_status st = quant_shape_check(shape, &s);
+  if (st != KV_OK) return st;
+  if (format != KV_E4M3 && format != KV_INT8) return KV_ERR_INVALID_ARG;
+  if (s.seqs > 0 && (k_scale == nullptr || v_scale == nullptr)) return KV_ERR_INVALID_ARG;
+  if (!aligned_to(k_scale, 4) || !aligned_to(v_scale, 4)) return KV_ERR_INVALID_ARG;
+  st = paged_decode_check(s, q, k_new, v_new, cu_add, slot_map, slot_capacity, k_pages, v_pages,
+                          block_table, lens, softmax_scale, out, ws, ws_bytes, &work);
+  if (st != KV_OK || !work) return st;
+  return cuda_status(launch_quant_decode(s, format, q, k_new, v_new, cu_add, slot_map,
+                                         slot_capacity, k_pages, v_pages, k_scale, v_scale,
+                                         block_table, lens, softmax_scale, out,
                                          static_cast<char*>(ws),
                                          static_cast<cudaStream_t>(stream)));
 }

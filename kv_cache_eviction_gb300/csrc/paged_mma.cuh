@@ -210,6 +210,13 @@ struct Tile<__nv_bfloat16, H> : State<H * 4, 1> {
   static constexpr int NQ = H * 4;     // 32-bit words of q per lane
   uint32_t q[NQ];
 
+  // outputs of a lane: kWide columns from 4 kWide t + kWide (lane & 3) on, for t < kGroups
+  static constexpr int kWide = 2, kGroups = NT;
+  __device__ __forceinline__ void group(int t, float by, float (&x)[2]) const {
+    x[0] = this->o[t][0] * by;
+    x[1] = this->o[t][1] * by;
+  }
+
   // Words of q for query g = lane / 4 (zero past d and for g >= G).
   static __device__ __forceinline__ void load_q(const __nv_bfloat16* src, int G, int d,
                                                 uint32_t (&w)[NQ]) {
@@ -308,6 +315,12 @@ struct Tile<float, H> : State<H * 2, (H > 6 ? 1 : 4)> {
   static constexpr int D = H * 16;
   static constexpr int NQ = H * 4;
   uint32_t qh[NQ], ql[NQ];
+
+  static constexpr int kWide = 2, kGroups = NT;
+  __device__ __forceinline__ void group(int t, float by, float (&x)[2]) const {
+    x[0] = this->o[t][0] * by;
+    x[1] = this->o[t][1] * by;
+  }
 
   static __device__ __forceinline__ void load_q(const float* src, int G, int d,
                                                 uint32_t (&w)[NQ]) {

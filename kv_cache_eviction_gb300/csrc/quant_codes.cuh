@@ -44,6 +44,10 @@ struct E4M3 {
         : "=r"(lo), "=r"(hi)
         : "r"(w));
   }
+  // of codes 0, 2 and 1, 3
+  static __device__ __forceinline__ void columns(uint32_t w, uint32_t& even, uint32_t& odd) {
+    halves(__byte_perm(w, 0u, 0x3120), even, odd);
+  }
 };
 
 struct Int8 {
@@ -68,6 +72,11 @@ struct Int8 {
     w ^= 0x80808080u;
     lo = less(__byte_perm(w, 0x64646464u, 0x4140));
     hi = less(__byte_perm(w, 0x64646464u, 0x4342));
+  }
+  static __device__ __forceinline__ void columns(uint32_t w, uint32_t& even, uint32_t& odd) {
+    w ^= 0x80808080u;
+    even = less(__byte_perm(w, 0x64646464u, 0x4240));
+    odd = less(__byte_perm(w, 0x64646464u, 0x4341));
   }
 };
 

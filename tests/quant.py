@@ -141,3 +141,190 @@ class Pool:
             keep[:self.size[0] * self.strides[0]].as_strided(self.size, self.strides).fill_(False)
             a, b = self.flat[name].cpu().view(torch.uint8), self.host[name].view(torch.uint8)
             assert torch.equal(a[keep], b[keep]), name
+
+
+class QuantCache:
+    """A paged cache in 8 bits with the given rows per table, as tests.paged.Cache is one of rows:
+    pages dealt out in a random order; codes that are NaN (e4m3) in every row that no table holds,
+    and NaN for the scale of every block that holds none.  The last row of the tables in `new`
+    comes as k_new / v_new."""
+
+    def __init__(self, seqs, hkv, G, d, tables, page, lens, dtype, fmt, seed, new=None, spare=3,
+                 extra=0, first_page=0, temp=4.0, spread=1.0):
+        rng = np.random.default_rng(seed)
+        g = torch.Generator().manual_seed(seed)
+        self.seqs, self.hkv, self.G, self.d = seqs, hkv, G, d
+        self.tables, self.page, self.dtype, self.fmt = tables, page, dtype, fmt
+        self.dt = torch.bfloat16 if dtype == "bf16" else torch.float32
+        U, hp, nb = seqs * tables, hkv // tables, page // BLOCK
+        self.hp = hp
+        lens = [int(x) for x in lens]
+        assert len(lens) == U
+        new = [n > 0 for n in lens] if new is None else [bool(x) and n > 0
+                                                         for x, n in zip(new, lens)]
+        used = [-(-n // page) for n in lens]
+        self.max_pages = max(1, max(used))
+        num = sum(used) + spare
+        order = rng.permutation(num) + first_page
+        self.num_pages = num + first_page
+        table = rng.integers(0, self.num_pages, (U, self.max_pages))
+        at = 0
+        for u, n in enumerate(used):
+            table[u, :n] = order[at:at + n]
+            at += n
+        inner = hp * page * d
+        self.apart = inner + extra
+        self.shape = kv.KvPagedShape.of(seqs, hkv * G, hkv, d, tables, page, self.max_pages, dtype,
+                                        self.num_pages, self.apart if extra else 0)
+        tau = np.exp(rng.random((seqs, hkv * G, 1)) * np.log(8.0)) * temp / 8
+        self.q = (torch.randn(seqs, hkv * G, d, generator=g) * torch.tensor(tau)).to(self.dt)
+        fresh = {n: (torch.randn(seqs, hkv, d, generator=g) * torch.exp(
+            0.7 * torch.randn(seqs, hkv, 1, generator=g))).to(self.dt) for n in ("k", "v")}
+        self.k_new, self.v_new = fresh["k"], fresh["v"]
+        self.lens, self.new, self.table_host = lens, new, table
+        # the places of the rows held before the call: page, row
+        self.num, self.scale, codes = {}, {}, {}
+        for name in ("k", "v"):
+            x = rng.normal(size=(self.num_pages, hp, nb, BLOCK, d)) * np.exp(
+                spread * rng.normal(size=(self.num_pages, hp, nb, 1, 1)))
+            top = np.abs(x).max((3, 4))
+            s = np.exp2(np.ceil(np.log2(top / MOST[fmt])))
+            y = nearest(x / s[..., None, None], fmt).reshape(self.num_pages, hp, page, d)
+            held = np.zeros((self.num_pages, page), bool)
+            for u, n in enumerate(lens):
+                n -= new[u]
+                r = np.arange(n)
+                held[table[u, r // page], r % page] = True
+            if fmt == "e4m3":
+                y[~held[:, None].repeat(hp, 1)] = np.nan
+            s[~held.reshape(self.num_pages, 1, nb, BLOCK).any(3).repeat(hp, 1)] = np.nan
+            self.num[name], self.scale[name] = y, s
+        # the device's copy of that
+        self.pool, self.scale_dev = {}, {}
+        for name in ("k", "v"):
+            t = torch.tensor(self.num[name])
+            c = t.to(torch.int8) if fmt == "int8" else t.float().to(torch.float8_e4m3fn).view(torch.uint8)
+            flat = torch.full((self.num_pages * self.apart,), 77, dtype=c.dtype)
+            flat.as_strided(c.shape, (self.apart, page * d, d, 1)).copy_(c)
+            dev = flat.cuda()
+            dev = dev if fmt == "int8" else dev.view(torch.float8_e4m3fn)
+            self.pool[name] = (dev, dev.as_strided(c.shape, (self.apart, page * d, d, 1)))
+            self.scale_dev[name] = torch.tensor(self.scale[name]).float().cuda()
+        self.slots_host = [int(table[u, (n - 1) // page]) * page + (n - 1) % page
+                           for u, n in enumerate(lens) if new[u]]
+        cu = np.concatenate([[0], np.cumsum([int(x) for x in new])])
+        self.table = torch.tensor(table).to(torch.int32).cuda()
+        self.lens_t = torch.tensor(lens, dtype=torch.int32, device="cuda")
+        self.cu = torch.tensor(cu, dtype=torch.int64, device="cuda")
+        self.slots = torch.tensor(self.slots_host, dtype=torch.int64, device="cuda")
+        self.qd, self.knd, self.vnd = self.q.cuda(), self.k_new.cuda(), self.v_new.cuda()
+        self.softmax_scale = d ** -0.5
+
+    def args(self):
+        return (self.pool["k"][1], self.pool["v"][1], self.scale_dev["k"], self.scale_dev["v"])
+
+    def run(self, with_new=True, ws=None, out=None, stream=None):
+        out = torch.full((self.seqs, self.hkv * self.G, self.d), float("nan"), dtype=self.dt,
+                         device="cuda") if out is None else out
+        if ws is None:
+            n = kv.kv_paged_workspace_size(kv.KV_OP_QUANT_DECODE, self.shape)
+            ws = torch.zeros(n, dtype=torch.uint8, device="cuda")
+        x = (self.knd, self.vnd, self.cu, self.slots) if with_new else (None,) * 4
+        kv.quant_decode_attn(self.shape, FORMATS[self.fmt], self.qd, *x, *self.args(), self.table,
+                             self.lens_t, self.softmax_scale, out, ws, stream)
+        return out, ws
+
+    def put(self, skip=()):
+        """The new rows, as the definition stores them (tables in `skip` left out)."""
+        at = 0
+        for u, x in enumerate(self.new):
+            if not x:
+                continue
+            slot = self.slots_host[at]
+            at += 1
+            if u in skip:
+                continue
+            b, h0 = u // self.tables, (u % self.tables) * self.hp
+            for name, rows in (("k", self.k_new), ("v", self.v_new)):
+                put(self.num[name], self.scale[name],
+                    rows[b:b + 1, h0:h0 + self.hp].double().numpy(), [slot], self.fmt)
+
+    def check_pools(self):
+        """The device's codes and scales are the host's, and nothing between the pages changed."""
+        for name in ("k", "v"):
+            flat, pool = self.pool[name]
+            got, want = numbers(pool.contiguous(), self.fmt), self.num[name]
+            same = (got == want) | (np.isnan(got) & np.isnan(want))
+            assert same.all(), (name, int((~same).sum()), np.argwhere(~same)[:4])
+            assert np.array_equal(self.scale_dev[name].cpu().double().numpy(), self.scale[name],
+                                  equal_nan=True), name
+            gap = flat.view(torch.uint8).view(self.num_pages, self.apart)[:, self.hp * self.page * self.d:]
+            assert bool((gap == 77).all())
+
+    def rows(self, u, name):
+        """Table u's rows as the cache holds them, [heads of a page][rows][d] float64."""
+        n = self.lens[u]
+        pages = self.table_host[u, :-(-n // self.page)]
+        x = self.num[name][pages] * np.repeat(self.scale[name][pages], BLOCK, 2)[..., None]
+        return x.transpose(1, 0, 2, 3).reshape(self.hp, -1, self.d)[:, :n]
+
+    def expected(self, skip=()):
+        """(out, bound) in 64 bits over what the cache holds now, [seqs][hq][d]; `skip`: (table,
+        column) pairs whose rows are left out.
+
+        The bound, as in tests.paged: u = 2^-23 a step of a float32 sum; a score is a sum of d
+        products of exact factors (fp32 q held to 2^-22, taken as t = 2^-21), plus 2^-36 of q's largest
+        element for what fp16 cuts off below it, and two roundings for its scale; an error of a
+        score moves its weight by that share, above and below the fraction line; weights are held
+        to 2^-22 (2^-21 taken), sums of m of them n u each; two more roundings for V's scale in
+        every tile's sum; the last term is the output's rounding.
+
+        A weight w <= 1 (the largest being 1) is held as 2^14 w = hi + 2^-11 lo in fp16.  fp16's numbers
+        are 2^-24 apart at least: 2^14 w - hi is off by no more than 2^-25, lo holds 2^11 of that to
+        2^-25, so w is also off by 2^-25 2^-11 2^-14 = 2^-50 where that is more than 2^-22 w."""
+        seqs, hkv, G, d = self.seqs, self.hkv, self.G, self.d
+        out = np.zeros((seqs, hkv * G, d))
+        tol = np.zeros_like(out)
+        u23, t_p = 2.0 ** -23, 2.0 ** -21
+        t_z = 0.0 if self.dtype == "bf16" else 2.0 ** -21
+        half = torch.finfo(self.dt).eps / 2
+        q = self.q.double().numpy()
+        for tb, n in enumerate(self.lens):
+            keep = np.ones(n, bool)
+            for (a, c) in skip:
+                if a == tb:
+                    keep[c * self.page:(c + 1) * self.page] = False
+            if not keep.any():
+                continue
+            ks, vs = self.rows(tb, "k"), self.rows(tb, "v")
+            for h in range(self.hp):
+                g0 = (tb % self.tables) * self.hp + h
+                k, v = ks[h][keep], vs[h][keep]
+                for g in range(G):
+                    x = q[tb // self.tables, g0 * G + g]
+                    c = abs(self.softmax_scale)
+                    z = self.softmax_scale * (k @ x)
+                    e_z = (c * ((d + 2) * u23 + t_z) * (np.abs(k) @ np.abs(x)) +
+                           c * 2.0 ** -36 * np.abs(x).max() * np.abs(k).sum(1) +
+                           4 * u23 * (1 + np.abs(z - z.max())))
+                    p = np.exp(z - z.max())
+                    p /= p.sum()
+                    o = p @ v
+                    m = len(p)
+                    mag = p @ np.abs(v)
+                    tol[tb // self.tables, g0 * G + g] = (
+                        2 * (p * e_z) @ np.abs(v) + 2 * (p @ e_z) * mag +
+                        (2 * m * u23 + 66 * u23 + t_p) * mag + half * np.abs(o) + 1e-30 +
+                        2.0 ** -50 * p.max() * np.abs(v).sum(0))
+                    out[tb // self.tables, g0 * G + g] = o
+        return out, tol
+
+    def check(self, out, skip=()):
+        ref, tol = self.expected(skip)
+        got = out.double().cpu().numpy()
+        assert np.isfinite(got).all(), "not finite"
+        bad = np.abs(got - ref) > tol
+        if bad.any():
+            i = np.unravel_index(np.argmax(np.where(bad, np.abs(got - ref) / tol, 0)), ref.shape)
+            raise AssertionError("%d of %d off; worst at %s: got %r, expected %r +- %r" % (
+                int(bad.sum()), bad.size, i, got[i], ref[i], tol[i]))

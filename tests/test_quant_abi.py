@@ -43,6 +43,12 @@ def call_read(L, s, fmt=0, k=P, v=P, stride=0, slots=P, rows=10, n_rows=None, kp
                            k, v, stride, ws, n, None)
 
 
+def call_decode(L, s, fmt=0, q=P, kn=P, vn=P, cu=P, slots=P, cap=10, kp=P, vp=P, ks=P, vs=P, table=P,
+                lens=P, scale=0.1, out=P, ws=P, n=BIG):
+    return L.quant_decode_attn(ctypes.byref(s) if s else None, fmt, q, kn, vn, cu, slots, cap, kp,
+                               vp, ks, vs, table, lens, scale, out, ws, n, None)
+
+
 ROWS = ((call_write, kv.KV_OP_QUANT_WRITE), (call_read, kv.KV_OP_QUANT_READ))
 
 
@@ -51,7 +57,7 @@ ROWS = ((call_write, kv.KV_OP_QUANT_WRITE), (call_read, kv.KV_OP_QUANT_READ))
     dict(max_pages=0), dict(num_pages=0), dict(dtype=7), dict(page_stride=8 * 16 * 128 - 16),
     dict(page_stride=8 * 16 * 128 + 8), dict(page_stride=-16)])
 def test_invalid_shapes(L, bad):
-    for call, op in ROWS:
+    for call, op in ROWS + ((call_decode, kv.KV_OP_QUANT_DECODE),):
         assert call(L, shape(**bad)) == INV
         assert kv.kv_paged_workspace_size(op, shape(**bad)) == 0
 
@@ -61,7 +67,7 @@ def test_invalid_shapes(L, bad):
     dict(page=24), dict(page=512), dict(max_pages=1 << 28), dict(num_pages=1 << 31),
     dict(page_stride=1 << 40), dict(seqs=1 << 29)])
 def test_unsupported_shapes(L, far):
-    for call, op in ROWS:
+    for call, op in ROWS + ((call_decode, kv.KV_OP_QUANT_DECODE),):
         assert call(L, shape(**far)) == FAR
         assert kv.kv_paged_workspace_size(op, shape(**far)) == 0
 
@@ -70,7 +76,7 @@ def test_page_stride_is_in_bytes(L):
     """A stride of 16 bytes more than dense pages is a legal one for either row type."""
     for dtype in ("bf16", "f32"):
         s = shape(dtype=dtype, page_stride=8 * 16 * 128 + 16)
-        for call, op in ROWS:
+        for call, op in ROWS + ((call_decode, kv.KV_OP_QUANT_DECODE),):
             assert call(L, s, n=0) == kv.KV_ERR_WORKSPACE
 
 
@@ -97,6 +103,31 @@ def test_row_arguments(L):
         assert call(L, shape(seqs=0), 0, None, None, 0, None, 10, None, None, None, None,
                     None) == OK
         assert call(L, shape(seqs=0), rows=-1) == INV
+
+
+def test_decode_arguments(L):
+    s = shape()
+    assert call_decode(L, None) == INV
+    for fmt in (-1, 2):
+        assert call_decode(L, s, fmt=fmt) == INV
+    for arg in ("q", "kp", "vp", "ks", "vs", "table", "lens", "out", "ws"):
+        assert call_decode(L, s, **{arg: None}) == INV
+        assert call_decode(L, s, **{arg: ODD2}) == INV
+    for arg in ("q", "kp", "vp", "kn", "vn", "out", "cu", "slots"):
+        assert call_decode(L, s, **{arg: ODD4}) == INV
+    for arg in ("kn", "vn", "cu", "slots"):
+        assert call_decode(L, s, **{arg: None}) == INV
+    assert call_decode(L, s, cap=-1) == INV
+    for scale in (math.inf, math.nan, 2.0 ** 127, -2.0 ** 127):
+        assert call_decode(L, s, scale=scale) == INV
+    n = kv.kv_paged_workspace_size(kv.KV_OP_QUANT_DECODE, s)
+    assert call_decode(L, s, n=n - 1) == kv.KV_ERR_WORKSPACE
+    assert call_decode(L, s, scale=-1.7e38, n=n - 1) == kv.KV_ERR_WORKSPACE
+    assert call_decode(L, shape(seqs=1 << 11, max_pages=1 << 16)) == FAR     # 2^31 tiles of 8 rows
+    far = shape(seqs=kv.KV_PAGED_DECODE_MAX_TABLES + 1, max_pages=1, hkv=1, hq=1)
+    assert call_decode(L, far) == FAR
+    assert call_decode(L, shape(seqs=0), 0, None, None, None, None, None, 0, None, None, None, None,
+                       None, None, 0.1, None) == OK
 
 
 def rotary_shape(**kw):
@@ -155,6 +186,9 @@ def test_binding_refuses_host_tensors(L):
         kv.kv_quant_write(s, kv.KV_INT8, r, r, i, None, t, t, f, f, i)
     with pytest.raises(ValueError):
         kv.kv_quant_read(s, kv.KV_INT8, t, t, f, f, i, None, r, r, i)
+    with pytest.raises(ValueError):
+        kv.quant_decode_attn(s, kv.KV_INT8, r, None, None, None, None, t, t, f, f, i.int(), i.int(),
+                             0.1, r, i)
     with pytest.raises(ValueError):
         kv.kv_rotary(rotary_shape(), r, r, i.int(), f.double(), r, r)
 
