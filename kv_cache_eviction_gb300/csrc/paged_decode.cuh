@@ -30,7 +30,7 @@
 // are -inf and their values zeros.  No CTA waits for another.
 //
 // The kernel is written for two kinds of pool (Rows and Codes below): rows of q's type, and rows of 8-bit
-// codes with a scale for each block of 16 rows of a head, which is then a tile.
+// codes with a scale for each block of 16 rows of a head, two of which are a tile.
 #pragma once
 
 #include <cfloat>
@@ -114,7 +114,7 @@ struct Codes {
   using E = unsigned char;
   using F = F_;
   using Tl = qmma::Tile<T_, F_, H_>;
-  static constexpr int H = H_, kMaxStages = H_ == 1 ? 8 : sizeof(T_) == 2 ? 4 : 3;
+  static constexpr int H = H_, kMaxStages = 4;
   static constexpr int kNewRow = H_ * 64 * (int)sizeof(T_);
   static constexpr bool kCodes = true;
 };
@@ -206,15 +206,40 @@ __device__ __forceinline__ void seek(Window& w, uint32_t x, const PagedArgs& a, 
 // What a lane knows of one tile.
 struct Desc {
   int32_t unit;
-  int64_t at;            // element of the pool where the tile's first row begins; in pages of 8
-                         // rows, of its first 8
-  int64_t at2;           // of its second 8 rows
-  uint32_t mask;         // bits 0..15: rows that count; kFirst / kLast: the unit's first / last
-                         // tile; bits 24..27: its last row
+  int64_t at;            // element of the pool where the tile's first row begins; in pages of half
+                         // a tile, of its first half
+  int64_t at2;           // of its second half
+  uint32_t word;         // see Word
   int64_t slot;          // where the new row (the unit's last) goes, or -1
-  int64_t scale;         // the block's scales (pools of codes)
+  int64_t scale, scale2; // the blocks' scales (pools of codes)
 };
 constexpr uint32_t kFirst = 1u << 16, kLast = 1u << 17;
+// A tile's rows in a word: kFirst / kLast: the unit's first / last tile.  Tiles of up to 16 rows: bits
+// 0..15 rows that count, 24..27 the last row.  Of 32: bits 0..5 the number of rows, 18 and 19 halves
+// that do not count.
+template <int RT>
+struct Word {
+  static constexpr uint32_t kAll = RT == 32 ? ~0u : (1u << (RT & 31)) - 1u;
+  static __device__ __forceinline__ uint32_t of(int n) {
+    return RT == 32 ? (uint32_t)n : ((1u << n) - 1u) | (uint32_t)(n - 1) << 24;
+  }
+  static __device__ __forceinline__ uint32_t without(uint32_t w, bool lo, bool hi) {
+    if (RT == 32) return w | (lo ? 1u << 18 : 0u) | (hi ? 1u << 19 : 0u);
+    constexpr uint32_t low = (1u << (RT / 2)) - 1u;
+    return w & ~((lo ? low : 0u) | (hi ? kAll & ~low : 0u));
+  }
+  static __device__ __forceinline__ bool whole(uint32_t w) {
+    return RT == 32 ? (w & 0xC003Fu) == 32u : (w & kAll) == kAll;
+  }
+  static __device__ __forceinline__ uint32_t rows(uint32_t w) {
+    if (RT != 32) return w & kAll;
+    const uint32_t n = w & 63u, m = n == 32 ? ~0u : (1u << n) - 1u;
+    return m & ~((w >> 18 & 1 ? 0xFFFFu : 0u) | (w >> 19 & 1 ? 0xFFFF0000u : 0u));
+  }
+  static __device__ __forceinline__ int last(uint32_t w) {
+    return RT == 32 ? (int)(w & 63u) - 1 : (int)(w >> 24 & 15);
+  }
+};
 
 template <typename T>
 __device__ __forceinline__ void store2(T* p, float x, float y);
@@ -332,7 +357,8 @@ paged_decode_kernel(const __grid_constant__ PagedArgs a) {
   constexpr int RT = C::RT, S = C::kStages, D = Tl::D, H = P::H;
   constexpr int VE = 16 / (int)sizeof(E);   // elements of a piece of the pool
   constexpr int VN = 16 / (int)sizeof(T);   // and of a new row
-  static_assert(!P::kCodes || RT == quant::kBlock, "a tile is a block");
+  static_assert(!P::kCodes || RT == 2 * quant::kBlock, "a tile is two blocks");
+  using W = Word<RT>;
   extern __shared__ unsigned char dsm_raw[];
   PagedSmem<C, kPWarps>& sm = *reinterpret_cast<PagedSmem<C, kPWarps>*>(
       (reinterpret_cast<uintptr_t>(dsm_raw) + 1023) & ~(uintptr_t)1023);
@@ -477,7 +503,7 @@ paged_decode_kernel(const __grid_constant__ PagedArgs a) {
     const uint32_t x = x0 + lane;
     bool open = x < xe;
     nxt.unit = -1;
-    nxt.mask = 0;
+    nxt.word = 0;
     p_page = p_page2 = 0;
     p_c0 = p_c1 = 0;
 #pragma unroll 1
@@ -500,10 +526,10 @@ paged_decode_kernel(const __grid_constant__ PagedArgs a) {
         const int32_t* entry = a.table + (int64_t)u * a.max_pages + (r0 >> a.shift);
         p_page = entry[0];
         if (page < RT && nv > page) p_page2 = entry[1];
-        nxt.mask = ((1u << nv) - 1u) | (uint32_t)(nv - 1) << 24;
-        if (tt == 0) nxt.mask |= kFirst;
+        nxt.word = W::of(nv);
+        if (tt == 0) nxt.word |= kFirst;
         if (tt == (int)nt - 1) {
-          nxt.mask |= kLast;
+          nxt.word |= kLast;
           if (has_new) {
             p_c0 = a.cu[u];
             p_c1 = a.cu[u + 1];
@@ -530,12 +556,14 @@ paged_decode_kernel(const __grid_constant__ PagedArgs a) {
     const bool bad2 = p_page2 < 0 || p_page2 >= a.num_pages;
     nxt.at = (bad ? 0 : p_page) * a.page_stride + p_row * (int64_t)d;
     if (P::kCodes) {
-      nxt.scale = bad ? 0 : ((int64_t)p_page * a.Hp << (a.shift - 4)) + (p_row >> 4);
+      const int64_t blocks = (int64_t)a.Hp << (a.shift - 4);   // of a page
+      nxt.scale = (bad ? 0 : p_page * blocks) + (p_row >> 4);
+      nxt.scale2 = page < RT ? (bad2 ? 0 : p_page2 * blocks) + (p_row >> 4) : nxt.scale + 1;
       if (bad) nxt.at = -1;   // no row's place
+      if (bad2) nxt.at2 = -1;
     }
     nxt.at2 = (bad2 ? 0 : p_page2) * a.page_stride + p_row * (int64_t)d;
-    if (bad) nxt.mask &= page < RT ? ~0xFFu : ~0xFFFFu;
-    if (bad2) nxt.mask &= ~0xFF00u;
+    if (bad || bad2) nxt.word = W::without(nxt.word, bad, page < RT ? bad2 : bad);
     if (bad || bad2) raise_dev(a.hdr, DEV_PAGE_ID, (unsigned)nxt.unit);
     nxt.slot = -1;
     if (p_c1 > p_c0 && p_c1 > 0 && p_c1 <= a.slot_cap) nxt.slot = a.slots[p_c1 - 1];
@@ -548,15 +576,15 @@ paged_decode_kernel(const __grid_constant__ PagedArgs a) {
   const uint32_t to_v = ring_u + pmma::v_piece<RT, H>(lr, pc);
   const int64_t from = (int64_t)lr * d + pc * VE;
   auto issue = [&](const Desc& t, int src, int s) {
-    constexpr uint32_t kAll = (1u << RT) - 1u;
     const int64_t at = __shfl_sync(0xffffffffu, (long long)t.at, src) + from;
-    const uint32_t mask = __shfl_sync(0xffffffffu, t.mask, src);
+    const uint32_t word = __shfl_sync(0xffffffffu, t.word, src);
     const uint32_t dst = to + s * C::kStage, dst_v = to_v + s * C::kStage;
     const E* ks = (const E*)a.kp + at;
     const E* vs = (const E*)a.vp + at;
-    // in pages of 8 rows: from a row of the first 8 to one of the second
+    // in pages of half a tile: from a row of the first half to one of the second
     int64_t skip = 0;
-    if (page < RT) skip = __shfl_sync(0xffffffffu, (long long)(t.at2 - t.at), src) - 8 * (int64_t)d;
+    if (page < RT)
+      skip = __shfl_sync(0xffffffffu, (long long)(t.at2 - t.at), src) - RT / 2 * (int64_t)d;
     if (pc < pieces) {
       // (without odd half segments V's stage is K's with an offset)
       auto copy = [&](int i, const E* k, const E* v, int bytes) {
@@ -565,24 +593,25 @@ paged_decode_kernel(const __grid_constant__ PagedArgs a) {
         cp_async16(x, k, bytes);
         cp_async16(H % 2 == 0 ? x + C::kStage / 2 : (dst_v ^ flip) + row, v, bytes);
       };
-      if ((mask & kAll) == kAll) {
+      if (W::whole(word)) {
 #pragma unroll
         for (int i = 0; i < RT / C::kRows; ++i) {
-          const int64_t o = i * C::kRows * d + (i * C::kRows >= 8 ? skip : (int64_t)0);
+          const int64_t o = i * C::kRows * d + (i * C::kRows >= RT / 2 ? skip : (int64_t)0);
           copy(i, ks + o, vs + o, 16);
         }
       } else {
         // rows that do not count are not read: zeros
+        const uint32_t mask = W::rows(word);
 #pragma unroll
         for (int i = 0; i < RT / C::kRows; ++i) {
           const int r = i * C::kRows + lr, n = mask >> r & 1 ? 16 : 0;
-          const int64_t o = n == 0 ? -at : i * C::kRows * d + (r >= 8 ? skip : (int64_t)0);
+          const int64_t o = n == 0 ? -at : i * C::kRows * d + (r >= RT / 2 ? skip : (int64_t)0);
           copy(i, ks + o, vs + o, n);
         }
       }
     }
     const uint32_t beside = side_u + s * C::kBeside;
-    if (has_new && (mask & kLast)) {
+    if (has_new && (word & kLast)) {
       const int64_t u = __shfl_sync(0xffffffffu, t.unit, src);
       for (int p = lane; p < new_pieces; p += 32) {
         cp_async16(beside + p * 16, (const T*)a.kn + u * d + p * VN);
@@ -590,8 +619,11 @@ paged_decode_kernel(const __grid_constant__ PagedArgs a) {
       }
     }
     if (P::kCodes && lane == src) {
+      // (a second block that has no rows: its scales are in the pool, or page 0's, and not used)
       cp_async4(beside + 2 * C::kNewRow, a.ks + t.scale);
       cp_async4(beside + 2 * C::kNewRow + 4, a.vs + t.scale);
+      cp_async4(beside + 2 * C::kNewRow + 8, a.ks + t.scale2);
+      cp_async4(beside + 2 * C::kNewRow + 12, a.vs + t.scale2);
     }
   };
   int32_t unit_a = -1, unit_b = -1;
@@ -625,9 +657,9 @@ paged_decode_kernel(const __grid_constant__ PagedArgs a) {
     }
     const int src = i - cur0;
     if (src == 0) {
-      firsts = __ballot_sync(0xffffffffu, cur.mask & kFirst);
-      lasts = __ballot_sync(0xffffffffu, cur.mask & kLast);
-      cuts = __ballot_sync(0xffffffffu, (cur.mask & ((1u << RT) - 1u)) != (1u << RT) - 1u);
+      firsts = __ballot_sync(0xffffffffu, cur.word & kFirst);
+      lasts = __ballot_sync(0xffffffffu, cur.word & kLast);
+      cuts = __ballot_sync(0xffffffffu, !W::whole(cur.word));
     }
     const bool last = lasts >> src & 1;
     if (i == 0 || (firsts >> src & 1)) {
@@ -642,13 +674,13 @@ paged_decode_kernel(const __grid_constant__ PagedArgs a) {
     __syncwarp();
     {
       unsigned char* beside = side + s * C::kBeside;
-      float2 scales = make_float2(1.f, 1.f);
-      if (P::kCodes) scales = *reinterpret_cast<const float2*>(beside + 2 * C::kNewRow);
-      uint32_t mask = (1u << RT) - 1u;
+      float4 scales = make_float4(1.f, 1.f, 1.f, 1.f);   // K's and V's of the first block, the second
+      if (P::kCodes) scales = *reinterpret_cast<const float4*>(beside + 2 * C::kNewRow);
+      uint32_t mask = W::kAll;
       if ((cuts >> src & 1) || (has_new && last)) {
-        mask = __shfl_sync(0xffffffffu, cur.mask, src);
-        const int r = mask >> 24 & 15;   // the unit's last row, if this is its last tile
-        mask &= (1u << RT) - 1u;
+        mask = __shfl_sync(0xffffffffu, cur.word, src);
+        const int r = W::last(mask);   // the unit's last row, if this is its last tile
+        mask = W::rows(mask);
         unsigned char* st = ring + s * C::kStage;
         if (has_new && last) {
           const int64_t slot = __shfl_sync(0xffffffffu, (long long)cur.slot, src);
@@ -659,16 +691,24 @@ paged_decode_kernel(const __grid_constant__ PagedArgs a) {
                              (((int64_t)(unit % a.Hp) << a.shift) + (slot & (page - 1))) * d;
           if constexpr (P::kCodes) {
             // (only in its own block, whose scale and rows are at hand)
-            const int64_t tile_at = __shfl_sync(0xffffffffu, (long long)cur.at, src);
-            const int64_t sc = __shfl_sync(0xffffffffu, (long long)cur.scale, src);
-            if (in_pool && at == tile_at + r * d) {
-              mask |= 1u << r;
-              scales.x = put_row<T, typename P::F>(
-                  st, [](int row, int p) { return pmma::k_piece<RT, H>(row, p); }, beside,
-                  (unsigned char*)a.kp + tile_at, a.ks + sc, scales.x, r, d);
-              scales.y = put_row<T, typename P::F>(
-                  st, [](int row, int p) { return pmma::v_piece<RT, H>(row, p); },
-                  beside + C::kNewRow, (unsigned char*)a.vp + tile_at, a.vs + sc, scales.y, r, d);
+            const bool hi = r >= quant::kBlock;
+            const int rb = r & (quant::kBlock - 1), above = hi ? quant::kBlock : 0;
+            const int64_t block_at =
+                hi && page >= RT
+                    ? __shfl_sync(0xffffffffu, (long long)cur.at, src) + quant::kBlock * d
+                    : __shfl_sync(0xffffffffu, (long long)(hi ? cur.at2 : cur.at), src);
+            const int64_t sc =
+                __shfl_sync(0xffffffffu, (long long)(hi ? cur.scale2 : cur.scale), src);
+            if (in_pool && (mask >> r & 1) && at == block_at + rb * d) {
+              const float ks = put_row<T, typename P::F>(
+                  st, [=](int row, int p) { return pmma::k_piece<RT, H>(above + row, p); }, beside,
+                  (unsigned char*)a.kp + block_at, a.ks + sc, hi ? scales.z : scales.x, rb, d);
+              const float vs = put_row<T, typename P::F>(
+                  st, [=](int row, int p) { return pmma::v_piece<RT, H>(above + row, p); },
+                  beside + C::kNewRow, (unsigned char*)a.vp + block_at, a.vs + sc,
+                  hi ? scales.w : scales.y, rb, d);
+              (hi ? scales.z : scales.x) = ks;
+              (hi ? scales.w : scales.y) = vs;
             } else if (in_pool && lane == 0) {
               raise_dev(a.hdr, DEV_PAGE_ID, (unsigned)unit);
             }
@@ -685,7 +725,10 @@ paged_decode_kernel(const __grid_constant__ PagedArgs a) {
             }
           }
         }
-        if (P::kCodes && mask == 0) scales = make_float2(1.f, 1.f);   // no block at all
+        if (P::kCodes) {   // blocks of no rows: what was copied is no scale
+          if ((mask & 0xFFFFu) == 0) scales.x = scales.y = 1.f;
+          if (mask >> 16 == 0) scales.z = scales.w = 1.f;
+        }
         __syncwarp();
       }
       if constexpr (P::kCodes) att.tile(ring_u + s * C::kStage, mask, a.scale.c2, scales);

@@ -1,4 +1,4 @@
-// One warp's online softmax over tiles of 16 K and V rows of 8-bit codes (paged_mma.cuh has the idea
+// One warp's online softmax over tiles of 32 K and V rows of 8-bit codes (paged_mma.cuh has the idea
 // and the tile's layout): the warp matrix instructions in fp16.
 //
 // fp16 holds every code exactly, and the block's scales are factors of a tile's sums: of the scores
@@ -49,7 +49,7 @@ __device__ __forceinline__ void f16_split(float x, float y, uint32_t& hi, uint32
 
 template <typename T, typename F, int H>
 struct Tile : pmma::State<H * 8, 1> {
-  static constexpr int RT = 16;
+  static constexpr int RT = 32;
   static constexpr int NT = H * 8;
   static constexpr int D = H * 64;     // columns held (d rounded up; the rest is zero)
   static constexpr bool kWords = sizeof(T) == 2;
@@ -109,84 +109,87 @@ struct Tile : pmma::State<H * 8, 1> {
   }
 
   // One tile at shared address st (128-byte aligned); bit r of `mask`: row r counts (others hold
-  // zeros).  scales: of K's and V's codes.
-  __device__ __forceinline__ void tile(uint32_t st, uint32_t mask, float c2, float2 scales) {
+  // zeros).  scales: of K's and V's codes in the first block, and in the second.
+  __device__ __forceinline__ void tile(uint32_t st, uint32_t mask, float c2, const float4& scales) {
     const int lane = threadIdx.x & 31, c = lane & 3;
-    float s[2][2][4];
-#pragma unroll
-    for (int j = 0; j < 2; ++j)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) s[j][0][e] = s[j][1][e] = 0.f;
     const uint32_t ka = st + (lane & 7) * 128 + (((lane >> 3) ^ (lane & 7)) << 4);
-    uint32_t b[H][2][4];
-#pragma unroll
-    for (int kk = 0; kk < H; ++kk)
-#pragma unroll
-      for (int j = 0; j < 2; ++j) pmma::ldsm4(b[kk][j], (ka ^ (kk * 64)) + j * 1024);
-    // V too: rows 0..7 and 8..15 of two pieces at a time
     const uint32_t va = st + (lane & 15) * 128 + (((lane >> 4) ^ (lane & 7)) << 4) +
                         (H == 2 ? RT * 128 : 0);
-    uint32_t v[H * 2][4];
+    float z[4][2];
 #pragma unroll
-    for (int t = 0; t < H * 2; ++t) pmma::ldsm4_t(v[t], va ^ ((2 * t + (H == 1 ? 4 : 0)) * 16));
+    for (int j = 0; j < 4; ++j) {   // eight rows
+      float s[2][4];
 #pragma unroll
-    for (int kk = 0; kk < H; ++kk)
+      for (int e = 0; e < 4; ++e) s[0][e] = s[1][e] = 0.f;
+      uint32_t b[H][4];
 #pragma unroll
-      for (int m = 0; m < 4; ++m)
+      for (int kk = 0; kk < H; ++kk) pmma::ldsm4(b[kk], (ka ^ (kk * 64)) + j * 1024);
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
+      for (int kk = 0; kk < H; ++kk)
+#pragma unroll
+        for (int m = 0; m < 4; ++m) {
           const int i = 2 * (4 * kk + m);
           uint32_t lo, hi;
-          F::halves(b[kk][j][m], lo, hi);
-          mma_f16(s[j][m & 1], qh[i], kWords ? 0u : ql[i % (kWords ? 1 : NF)], qh[i + 1],
+          F::halves(b[kk][m], lo, hi);
+          mma_f16(s[m & 1], qh[i], kWords ? 0u : ql[i % (kWords ? 1 : NF)], qh[i + 1],
                   kWords ? 0u : ql[(i + 1) % (kWords ? 1 : NF)], lo, hi);
         }
-    const float by = scales.x * unit;
-    float z[2][2];
-#pragma unroll
-    for (int j = 0; j < 2; ++j)
+      const float by = (j < 2 ? scales.x : scales.z) * unit;
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        float x = s[j][0][e] + s[j][1][e];
-        if (!kWords) x = fmaf(s[j][0][2 + e] + s[j][1][2 + e], 0x1p-11f, x);
+        float x = s[0][e] + s[1][e];
+        if (!kWords) x = fmaf(s[0][2 + e] + s[1][2 + e], 0x1p-11f, x);
         z[j][e] = x * by;
       }
-    if (mask != 0xFFFFu) {
+    }
+    if (mask != 0xFFFFFFFFu) {
 #pragma unroll
-      for (int j = 0; j < 2; ++j)
+      for (int j = 0; j < 4; ++j)
 #pragma unroll
         for (int e = 0; e < 2; ++e)
           if (!(mask >> (8 * j + 2 * c + e) & 1)) z[j][e] = -INFINITY;
     }
-    this->raise(fmaxf(fmaxf(z[0][0], z[0][1]), fmaxf(z[1][0], z[1][1])), c2);
-    const float base = this->base();
-    uint32_t hi[2], lo[2];
-    float ps[2];
+    float top = fmaxf(z[0][0], z[0][1]);
 #pragma unroll
-    for (int j = 0; j < 2; ++j) {
+    for (int j = 1; j < 4; ++j) top = fmaxf(top, fmaxf(z[j][0], z[j][1]));
+    this->raise(top, c2);
+    const float base = this->base();
+    uint32_t hi[4], lo[4];
+    float ps = 0.f;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
       const float p0 = ptx::ex2((z[j][0] - base) * c2), p1 = ptx::ex2((z[j][1] - base) * c2);
-      ps[j] = p0 + p1;
+      ps += p0 + p1;
       f16_split(p0 * 16384.f, p1 * 16384.f, hi[j], lo[j]);
     }
-    this->add_l(ps[0] + ps[1]);
-    const float2 f1 = make_float2(scales.y * 0x1p-14f, scales.y * 0x1p-14f);
-    const float2 f2 = make_float2(scales.y * 0x1p-25f, scales.y * 0x1p-25f);
+    this->add_l(ps);
 #pragma unroll
-    for (int p = 0; p < H * 4; ++p) {
-      uint32_t e0, o0, e1, o1;
-      F::columns(v[p / 2][p % 2 * 2], e0, o0);
-      F::columns(v[p / 2][p % 2 * 2 + 1], e1, o1);
-      float d[2][4];
-      mma_f16_new(d[0], hi[0], lo[0], hi[1], lo[1], e0, e1);
-      mma_f16_new(d[1], hi[0], lo[0], hi[1], lo[1], o0, o1);
+    for (int b = 0; b < 2; ++b) {   // blocks
+      const float vs = b == 0 ? scales.y : scales.w;
+      const float2 f1 = make_float2(vs * 0x1p-14f, vs * 0x1p-14f);
+      const float2 f2 = make_float2(vs * 0x1p-25f, vs * 0x1p-25f);
+      // V: rows 0..7 and 8..15 of two pieces at a time
+      uint32_t v[H * 2][4];
 #pragma unroll
-      for (int x = 0; x < 2; ++x) {
-        float(&o)[2] = this->o[2 * p + x];
-        const float2 y = ptx::ffma2(make_float2(d[x][0], d[x][1]), f1,
-                                    ptx::ffma2(make_float2(d[x][2], d[x][3]), f2,
-                                               make_float2(o[0], o[1])));
-        o[0] = y.x;
-        o[1] = y.y;
+      for (int t = 0; t < H * 2; ++t)
+        pmma::ldsm4_t(v[t], (va ^ ((2 * t + (H == 1 ? 4 : 0)) * 16)) + b * 2048);
+#pragma unroll
+      for (int p = 0; p < H * 4; ++p) {
+        uint32_t e0, o0, e1, o1;
+        F::columns(v[p / 2][p % 2 * 2], e0, o0);
+        F::columns(v[p / 2][p % 2 * 2 + 1], e1, o1);
+        float d[2][4];
+        mma_f16_new(d[0], hi[2 * b], lo[2 * b], hi[2 * b + 1], lo[2 * b + 1], e0, e1);
+        mma_f16_new(d[1], hi[2 * b], lo[2 * b], hi[2 * b + 1], lo[2 * b + 1], o0, o1);
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          float(&o)[2] = this->o[2 * p + x];
+          const float2 y = ptx::ffma2(make_float2(d[x][0], d[x][1]), f1,
+                                      ptx::ffma2(make_float2(d[x][2], d[x][3]), f2,
+                                                 make_float2(o[0], o[1])));
+          o[0] = y.x;
+          o[1] = y.y;
+        }
       }
     }
   }
