@@ -631,7 +631,7 @@ KV_API kv_status kv_quant_read(const kv_paged_shape* shape, int format, const vo
  * above.  A table's slot has to be the place that its block table gives row lens - 1 (kv_page_map's
  * is): at any other one in the pool the row is not stored, and the error word is set (10).
  * Sums, the softmax and out before its rounding are float32 (fp32 q is held to 22 bits, the softmax
- * numerators to 22 bits or 2^-50 of the largest; bf16 q and the values are exact).  q, the values attended to and their scores
+ * numerators to 22 bits or 2^-39 of the largest; bf16 q and the values are exact).  q, the values attended to and their scores
  * have to be finite (a NaN among them makes the outputs it reaches NaN, an infinity may).  Every
  * result is the same in every run.
  */

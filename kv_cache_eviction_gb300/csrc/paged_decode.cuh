@@ -73,8 +73,10 @@ constexpr int kMinTiles = 4;
 // the workspace and a ticket cost 2 us, the tiles less than that.  16 / 24 / 32 / 48 tiles: 256 heads
 // of 128 rows 11.2 / 10.9 / 10.6 / 10.6 us; units of 500 rows (32 tiles), 8 of them 8.2 / 8.2 / 11.2 /
 // 11.2, 16 9.8 / 9.8 / 11.4 / 11.4, 64 11.6 / 11.7 / 11.7 / 13.2, 128 13.2 / 13.2 / 13.1 / 15.2;
-// units of 2000 rows level.
-constexpr int kSnapTiles = 24;
+// units of 2000 rows level.  (Tiles of 16 rows; in rows the same holds for those of 32: one sequence of
+// 500 rows 10.4 us with 24 of them, 8.8 with 12 or 8; 256 heads of 128 9.6, 9.6 and 11.8.)
+template <int RT>
+constexpr int kSnapTiles = RT == 32 ? 12 : 24;
 // Part of a unit in the workspace: max[8], sum[8], then o[G][D].
 constexpr int kPartHead = 16;
 constexpr int kPartFloats = kPartHead + 8 * 128;
@@ -107,15 +109,15 @@ struct Rows {
   static constexpr int kNewRow = H_ * 64;  // bytes of a new row beside a stage
   static constexpr bool kCodes = false;
 };
-// Pools of codes of the format F, for q, new rows and outputs of T.
-template <typename T_, typename F_, int H_>
+// Pools of codes of the format F, for q, new rows and outputs of T, in NP pieces of 16 columns.
+template <typename T_, typename F_, int NP>
 struct Codes {
   using T = T_;
   using E = unsigned char;
   using F = F_;
-  using Tl = qmma::Tile<T_, F_, H_>;
-  static constexpr int H = H_, kMaxStages = 4;
-  static constexpr int kNewRow = H_ * 64 * (int)sizeof(T_);
+  using Tl = qmma::Tile<T_, F_, NP>;
+  static constexpr int H = Tl::H, kMaxStages = 4;
+  static constexpr int kNewRow = NP * 16 * (int)sizeof(T_);
   static constexpr bool kCodes = true;
 };
 template <typename P_>
@@ -259,12 +261,6 @@ __device__ __forceinline__ void store4(__nv_bfloat16* p, const float4& v) {
   w.x = pmma::bf16x2_of(v.x, v.y);
   w.y = pmma::bf16x2_of(v.z, v.w);
   *reinterpret_cast<uint2*>(p) = w;
-}
-template <typename T>
-__device__ __forceinline__ void store(T* p, const float (&x)[2]) { store2(p, x[0], x[1]); }
-template <typename T>
-__device__ __forceinline__ void store(T* p, const float (&x)[4]) {
-  store4(p, make_float4(x[0], x[1], x[2], x[3]));
 }
 // 16 bytes from global to shared memory; `bytes` of them are read, the rest is zero.
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, int bytes = 16) {
@@ -452,7 +448,7 @@ paged_decode_kernel(const __grid_constant__ PagedArgs a) {
     const uint32_t nt = tiles_of<RT>(__shfl_sync(0xffffffffu, w.len, j));
     const uint32_t tb = __shfl_sync(0xffffffffu, w.end, j) - nt * a.Hp;
     const uint32_t lo = tb + (x - tb) / nt * nt;
-    if (nt > kSnapTiles) return x;
+    if (nt > kSnapTiles<RT>) return x;
     return x - lo <= lo + nt - x ? lo : lo + nt;
   };
   // the CTA that holds tile x of a unit that crosses CTAs
@@ -745,18 +741,18 @@ paged_decode_kernel(const __grid_constant__ PagedArgs a) {
     if (last || i == count - 1) {
       const int32_t unit = __shfl_sync(0xffffffffu, cur.unit, src);
       att.finish();
-      const int g = lane >> 2, col = Tl::kWide * (lane & 3);
       if (whole && last) {
-        if (g < G) {
-          const float inv = att.l != 0.f ? 1.f / att.l : 0.f;
-          T* dst = (T*)a.out + ((int64_t)unit * G + g) * d + col;
 #pragma unroll
-          for (int t = 0; t < Tl::kGroups; ++t)
-            if (4 * Tl::kWide * t < d) {
-              float x[Tl::kWide];
-              att.group(t, inv, x);
-              store(dst + 4 * Tl::kWide * t, x);
-            }
+        for (int e = 0; e < Tl::kQ; ++e) {
+          const int g = Tl::query(e);
+          if (g >= G) continue;
+          const float l = att.sum_of(e), inv = l != 0.f ? 1.f / l : 0.f;
+          T* dst = (T*)a.out + ((int64_t)unit * G + g) * d;
+#pragma unroll
+          for (int t = 0; t < Tl::kPairs; ++t) {
+            const float2 x = att.pair(t, e);
+            if (Tl::column(t) < d) store2(dst + Tl::column(t), x.x * inv, x.y * inv);
+          }
         }
       } else {
         // a part of the unit
@@ -766,16 +762,17 @@ paged_decode_kernel(const __grid_constant__ PagedArgs a) {
           unit_a = unit;
           open_a = !last;
         }
-        if (col == 0) {
-          sm.ml[warp][whole][g] = att.m;
-          sm.ml[warp][whole][8 + g] = att.l;
-        }
         float* dst = reinterpret_cast<float*>(sm.part4[warp][whole]);
 #pragma unroll
-        for (int t = 0; t < Tl::kGroups; ++t) {
-          float x[Tl::kWide];
-          att.group(t, 1.f, x);
-          store(dst + g * D + 4 * Tl::kWide * t + col, x);
+        for (int e = 0; e < Tl::kQ; ++e) {
+          const int g = Tl::query(e);
+          if (Tl::owns_sums()) {
+            sm.ml[warp][whole][g] = att.max_of(e);
+            sm.ml[warp][whole][8 + g] = att.sum_of(e);
+          }
+#pragma unroll
+          for (int t = 0; t < Tl::kPairs; ++t)
+            *reinterpret_cast<float2*>(dst + g * D + Tl::column(t)) = att.pair(t, e);
         }
       }
     }

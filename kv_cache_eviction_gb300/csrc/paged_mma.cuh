@@ -133,6 +133,14 @@ struct State {
   // sums of the last `held` tiles: [0..1] high rows, [2..3] low rows
   float acc[kHold > 1 ? NT : 1][4];
   int held;
+  // A lane's outputs: kQ queries, and for each kPairs pairs of neighbouring columns.
+  static constexpr int kQ = 1, kPairs = NT;
+  static __device__ __forceinline__ int query(int) { return (threadIdx.x & 31) >> 2; }
+  static __device__ __forceinline__ int column(int t) { return 8 * t + 2 * (threadIdx.x & 3); }
+  static __device__ __forceinline__ bool owns_sums() { return (threadIdx.x & 3) == 0; }
+  __device__ __forceinline__ float2 pair(int t, int) const { return make_float2(o[t][0], o[t][1]); }
+  __device__ __forceinline__ float max_of(int) const { return m; }
+  __device__ __forceinline__ float sum_of(int) const { return l; }
   __device__ __forceinline__ void begin() {
     m = -INFINITY;
     l = lc = 0.f;
@@ -209,13 +217,6 @@ struct Tile<__nv_bfloat16, H> : State<H * 4, 1> {
   static constexpr int D = H * 32;     // columns held (d rounded up; the rest is zero)
   static constexpr int NQ = H * 4;     // 32-bit words of q per lane
   uint32_t q[NQ];
-
-  // outputs of a lane: kWide columns from 4 kWide t + kWide (lane & 3) on, for t < kGroups
-  static constexpr int kWide = 2, kGroups = NT;
-  __device__ __forceinline__ void group(int t, float by, float (&x)[2]) const {
-    x[0] = this->o[t][0] * by;
-    x[1] = this->o[t][1] * by;
-  }
 
   // Words of q for query g = lane / 4 (zero past d and for g >= G).
   static __device__ __forceinline__ void load_q(const __nv_bfloat16* src, int G, int d,
@@ -315,12 +316,6 @@ struct Tile<float, H> : State<H * 2, (H > 6 ? 1 : 4)> {
   static constexpr int D = H * 16;
   static constexpr int NQ = H * 4;
   uint32_t qh[NQ], ql[NQ];
-
-  static constexpr int kWide = 2, kGroups = NT;
-  __device__ __forceinline__ void group(int t, float by, float (&x)[2]) const {
-    x[0] = this->o[t][0] * by;
-    x[1] = this->o[t][1] * by;
-  }
 
   static __device__ __forceinline__ void load_q(const float* src, int G, int d,
                                                 uint32_t (&w)[NQ]) {

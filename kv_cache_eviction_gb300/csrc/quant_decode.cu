@@ -5,7 +5,9 @@ namespace kv {
 namespace {
 template <typename T, typename F>
 cudaError_t by_width(const PagedShape& s, const PagedArgs& a, cudaStream_t st) {
-  return s.d <= 64 ? launch_t<Codes<T, F, 1>>(s, a, st) : launch_t<Codes<T, F, 2>>(s, a, st);
+  if (s.d <= 64)
+    return s.d <= 32 ? launch_t<Codes<T, F, 2>>(s, a, st) : launch_t<Codes<T, F, 4>>(s, a, st);
+  return s.d <= 96 ? launch_t<Codes<T, F, 6>>(s, a, st) : launch_t<Codes<T, F, 8>>(s, a, st);
 }
 }  // namespace
 

@@ -1,18 +1,23 @@
-// One warp's online softmax over tiles of 32 K and V rows of 8-bit codes (paged_mma.cuh has the idea
-// and the tile's layout): the warp matrix instructions in fp16.
+// One warp's online softmax over tiles of 32 K and V rows of 8-bit codes, for up to 8 query rows, on the
+// warp matrix instructions in fp16 (paged_mma.cuh has the sums and the tile's layout).
 //
 // fp16 holds every code exactly, and the block's scales are factors of a tile's sums: of the scores
 // (after the product with q) and of the outputs (when a tile's sums, which start from zero, are added
 // to o).  So the codes cost their conversion and nothing else.
 //   q is taken times a power of two that brings its largest element to 2^13..2^14, which fp16 holds to
-//     2^-24, 2^-37 of it; bf16's 8 bits are then exact, and fp32's are held as two fp16 (22 bits), the
-//     lower 2^11 times larger.
-//   p, at most 1, is taken 2^14 times as large and held as two fp16 in the same way.
+//     2^-24, 2^-37 of it; bf16's 8 bits are then exact, and fp32's are held as two fp16 (22 bits).
+//   p, at most 1, is taken 2^14 times as large and held as two fp16 as well: 22 bits, or 2^-39.
 //
+// m16n8k16's larger side is the codes': scores are K q^T (16 rows, 8 queries), outputs V^T p^T (16
+// columns, 8 queries).  With the queries on that side half of its rows stood empty (or held the lower
+// parts), and its four registers had to be put together for every product: 770 instructions a tile,
+// and 322 us on 2.1 GB.
 // K's words hold four columns of a row, 16 p + 4 c + 0..3 for lane c of 4: they are taken as columns
 // 2 c, 2 c + 1 and 2 c + 8, 2 c + 9 of the instruction, and q's likewise.  V's transposed load moves pairs
-// of columns, so a word has two rows of two columns: even and odd columns are products of their own, and
-// a lane ends with the outputs of four neighbouring columns.
+// of columns, so a word has two rows of two columns: rows 0..7 of V^T's 16 are the even ones of a piece,
+// 8..15 the odd ones.  A lane (4 g + c) has the scores of rows g and g + 8 for queries 2 c and 2 c + 1;
+// as right operand the second product wants rows 2 c and 2 c + 1 for query g: a transposition of 8 by
+// 8, movmatrix.
 #pragma once
 
 #include "paged_mma.cuh"
@@ -21,55 +26,71 @@
 namespace kv {
 namespace qmma {
 
-__device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
-                                        uint32_t a3, uint32_t b0, uint32_t b1) {
+__device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
+                                        uint32_t b1) {
   asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
       "{%8,%9}, {%0,%1,%2,%3};"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 // The same with sums that start from zero.
-__device__ __forceinline__ void mma_f16_new(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
-                                            uint32_t a3, uint32_t b0, uint32_t b1) {
+__device__ __forceinline__ void mma_f16_new(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
+                                            uint32_t b1) {
   asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
       "{%8,%9}, {%10,%10,%10,%10};"
       : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
-      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
+}
+// An 8 by 8 matrix of 16-bit elements, transposed: lane 4 g + c gives row g, columns 2 c and 2 c + 1.
+__device__ __forceinline__ uint32_t transposed(uint32_t x) {
+  uint32_t r;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
+  return r;
 }
 __device__ __forceinline__ uint32_t f16x2_of(float x, float y) {   // x in the low half
   const __half2 h = __floats2half2_rn(x, y);
   return *reinterpret_cast<const uint32_t*>(&h);
 }
-// x, y = hi + 2^-11 lo, both pairs of fp16
+// x, y = hi + lo, both pairs of fp16
 __device__ __forceinline__ void f16_split(float x, float y, uint32_t& hi, uint32_t& lo) {
   hi = f16x2_of(x, y);
   const float2 h = quant::floats_of(hi);
-  lo = f16x2_of((x - h.x) * 2048.f, (y - h.y) * 2048.f);
+  lo = f16x2_of(x - h.x, y - h.y);
 }
 
-template <typename T, typename F, int H>
-struct Tile : pmma::State<H * 8, 1> {
+// NP: pieces of 16 columns, even.
+template <typename T, typename F, int NP>
+struct Tile {
   static constexpr int RT = 32;
-  static constexpr int NT = H * 8;
-  static constexpr int D = H * 64;     // columns held (d rounded up; the rest is zero)
+  static constexpr int H = NP <= 4 ? 1 : 2;   // 64-byte parts of a row in a stage
+  static constexpr int D = NP * 16;           // columns held (d rounded up; the rest is zero)
   static constexpr bool kWords = sizeof(T) == 2;
-  static constexpr int NQ = H * (kWords ? 8 : 16);   // 32-bit words of q per lane, as loaded
-  static constexpr int NF = H * 8;                   // and as pairs of fp16
-  uint32_t qh[NF], ql[kWords ? 1 : NF];
-  float unit;        // what a score of qh, ql and codes counts for
+  static constexpr int NQ = NP * (kWords ? 2 : 4);   // 32-bit words of q per lane, as loaded
+  static constexpr int NL = kWords ? 1 : 2 * NP;     // words of its lower part
+  uint32_t qh[2 * NP], ql[NL];
+  // of queries 2 c and 2 c + 1: what a score of qh, ql and codes counts for, running maximum, this
+  // lane's share of the sum, and what its rounding has added
+  float unit[2], m[2], l[2], lc[2];
+  float o[NP][4];   // columns 16 p + 2 g (both queries), and 16 p + 2 g + 1
 
-  static constexpr int kWide = 4, kGroups = NT / 2;
-  __device__ __forceinline__ void group(int t, float by, float (&x)[4]) const {
-    x[0] = this->o[2 * t][0] * by;
-    x[1] = this->o[2 * t + 1][0] * by;
-    x[2] = this->o[2 * t][1] * by;
-    x[3] = this->o[2 * t + 1][1] * by;
+  // A lane's outputs: kQ queries, and for each kPairs pairs of neighbouring columns.
+  static constexpr int kQ = 2, kPairs = NP;
+  static __device__ __forceinline__ int query(int e) { return 2 * (threadIdx.x & 3) + e; }
+  static __device__ __forceinline__ int column(int t) {
+    return 16 * t + 2 * ((threadIdx.x & 31) >> 2);
   }
+  static __device__ __forceinline__ bool owns_sums() { return (threadIdx.x & 31) < 4; }
+  __device__ __forceinline__ float2 pair(int t, int e) const {
+    return make_float2(o[t][e], o[t][2 + e]);
+  }
+  __device__ __forceinline__ float max_of(int e) const { return m[e]; }
+  __device__ __forceinline__ float sum_of(int e) const { return l[e]; }
 
+  // q of query lane / 4: columns 16 p + 4 c + 0..3 (zero past d and for queries from G on).
   static __device__ __forceinline__ void load_q(const T* src, int G, int d, uint32_t (&w)[NQ]) {
     const int lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
 #pragma unroll
-    for (int p = 0; p < H * 4; ++p) {
+    for (int p = 0; p < NP; ++p) {
       const bool in = g < G && 16 * p < d;
       const T* at = src + g * d + 16 * p + 4 * c;
       if (kWords) {
@@ -92,103 +113,144 @@ struct Tile : pmma::State<H * 8, 1> {
     };
     float top = 0.f;
 #pragma unroll
-    for (int i = 0; i < 2 * NF; ++i) top = fmaxf(top, fabsf(at(i)));
+    for (int i = 0; i < 4 * NP; ++i) top = fmaxf(top, fabsf(at(i)));
     top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
     top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-    // 2^13 <= top * by < 2^14; by within 2^-114..2^120
+    // 2^13 <= top * by < 2^14, by between 2^-115 and 2^120
     int e = (int)(__float_as_uint(top) >> 23);
     e = e < 20 ? 20 : e;
     const float by = __uint_as_float((uint32_t)(267 - e) << 23) * (sc.flip ? -1.f : 1.f);
-    unit = __uint_as_float((uint32_t)(e - 13) << 23);
+    const float one = __uint_as_float((uint32_t)(e - 13) << 23);
 #pragma unroll
-    for (int i = 0; i < NF; ++i) {
+    for (int x = 0; x < 2; ++x) unit[x] = __shfl_sync(0xffffffffu, one, 4 * query(x));
+#pragma unroll
+    for (int i = 0; i < 2 * NP; ++i) {
       const float x = at(2 * i) * by, y = at(2 * i + 1) * by;
       if (kWords) qh[i] = f16x2_of(x, y);
-      else f16_split(x, y, qh[i], ql[i % (kWords ? 1 : NF)]);
+      else f16_split(x, y, qh[i], ql[i % NL]);
     }
+  }
+  __device__ __forceinline__ void begin() {
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      m[e] = -INFINITY;
+      l[e] = lc[e] = 0.f;
+    }
+#pragma unroll
+    for (int p = 0; p < NP; ++p) o[p][0] = o[p][1] = o[p][2] = o[p][3] = 0.f;
+  }
+  // After the last tile: the sums whole in every lane of a query.
+  __device__ __forceinline__ void finish() {
+#pragma unroll
+    for (int e = 0; e < 2; ++e)
+#pragma unroll
+      for (int s = 4; s < 32; s <<= 1) l[e] += __shfl_xor_sync(0xffffffffu, l[e], s);
   }
 
   // One tile at shared address st (128-byte aligned); bit r of `mask`: row r counts (others hold
   // zeros).  scales: of K's and V's codes in the first block, and in the second.
   __device__ __forceinline__ void tile(uint32_t st, uint32_t mask, float c2, const float4& scales) {
-    const int lane = threadIdx.x & 31, c = lane & 3;
-    const uint32_t ka = st + (lane & 7) * 128 + (((lane >> 3) ^ (lane & 7)) << 4);
-    const uint32_t va = st + (lane & 15) * 128 + (((lane >> 4) ^ (lane & 7)) << 4) +
-                        (H == 2 ? RT * 128 : 0);
-    float z[4][2];
+    const int lane = threadIdx.x & 31, g = lane >> 2;
+    // K and V: rows 0..7 and 8..15 of a block, of two pieces at a time
+    const uint32_t ka = st + (lane & 15) * 128 + (((lane >> 4) ^ (lane & 7)) << 4);
+    const uint32_t va = H == 2 ? ka + RT * 128 : ka ^ 64u;
+    float z[2][4];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {   // eight rows
+    for (int b = 0; b < 2; ++b) {
       float s[2][4];
 #pragma unroll
-      for (int e = 0; e < 4; ++e) s[0][e] = s[1][e] = 0.f;
-      uint32_t b[H][4];
+      for (int p = 0; p < NP; p += 2) {
+        uint32_t w[4];
+        pmma::ldsm4(w, (ka ^ (p * 16)) + b * 2048);
 #pragma unroll
-      for (int kk = 0; kk < H; ++kk) pmma::ldsm4(b[kk], (ka ^ (kk * 64)) + j * 1024);
-#pragma unroll
-      for (int kk = 0; kk < H; ++kk)
-#pragma unroll
-        for (int m = 0; m < 4; ++m) {
-          const int i = 2 * (4 * kk + m);
-          uint32_t lo, hi;
-          F::halves(b[kk][m], lo, hi);
-          mma_f16(s[m & 1], qh[i], kWords ? 0u : ql[i % (kWords ? 1 : NF)], qh[i + 1],
-                  kWords ? 0u : ql[(i + 1) % (kWords ? 1 : NF)], lo, hi);
+        for (int x = 0; x < 2; ++x) {
+          uint32_t a[4];
+          F::halves(w[2 * x], a[0], a[2]);
+          F::halves(w[2 * x + 1], a[1], a[3]);
+          if (p == 0) mma_f16_new(s[x], a, qh[2 * x], qh[2 * x + 1]);
+          else mma_f16(s[x], a, qh[2 * (p + x)], qh[2 * (p + x) + 1]);
+          if (!kWords) mma_f16(s[x], a, ql[2 * (p + x) % NL], ql[(2 * (p + x) + 1) % NL]);
         }
-      const float by = (j < 2 ? scales.x : scales.z) * unit;
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        float x = s[0][e] + s[1][e];
-        if (!kWords) x = fmaf(s[0][2 + e] + s[1][2 + e], 0x1p-11f, x);
-        z[j][e] = x * by;
       }
+      const float ks = b == 0 ? scales.x : scales.z;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) z[b][i] = (s[0][i] + s[1][i]) * (ks * unit[i & 1]);
     }
     if (mask != 0xFFFFFFFFu) {
 #pragma unroll
-      for (int j = 0; j < 4; ++j)
+      for (int b = 0; b < 2; ++b)
 #pragma unroll
-        for (int e = 0; e < 2; ++e)
-          if (!(mask >> (8 * j + 2 * c + e) & 1)) z[j][e] = -INFINITY;
+        for (int i = 0; i < 4; ++i)
+          if (!(mask >> (16 * b + 8 * (i >> 1) + g) & 1)) z[b][i] = -INFINITY;
     }
-    float top = fmaxf(z[0][0], z[0][1]);
+    float mt[2];
 #pragma unroll
-    for (int j = 1; j < 4; ++j) top = fmaxf(top, fmaxf(z[j][0], z[j][1]));
-    this->raise(top, c2);
-    const float base = this->base();
-    uint32_t hi[4], lo[4];
-    float ps = 0.f;
+    for (int e = 0; e < 2; ++e) {
+      mt[e] = fmaxf(fmaxf(z[0][e], z[0][2 + e]), fmaxf(z[1][e], z[1][2 + e]));
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const float p0 = ptx::ex2((z[j][0] - base) * c2), p1 = ptx::ex2((z[j][1] - base) * c2);
-      ps += p0 + p1;
-      f16_split(p0 * 16384.f, p1 * 16384.f, hi[j], lo[j]);
+      for (int s = 4; s < 32; s <<= 1) mt[e] = fmaxf(mt[e], __shfl_xor_sync(0xffffffffu, mt[e], s));
     }
-    this->add_l(ps);
+    if (__any_sync(0xffffffffu, mt[0] > m[0] || mt[1] > m[1])) {
+      float a[2];
 #pragma unroll
-    for (int b = 0; b < 2; ++b) {   // blocks
-      const float vs = b == 0 ? scales.y : scales.w;
-      const float2 f1 = make_float2(vs * 0x1p-14f, vs * 0x1p-14f);
-      const float2 f2 = make_float2(vs * 0x1p-25f, vs * 0x1p-25f);
-      // V: rows 0..7 and 8..15 of two pieces at a time
-      uint32_t v[H * 2][4];
+      for (int e = 0; e < 2; ++e) {
+        const float mn = fmaxf(m[e], mt[e]);
+        a[e] = mn > m[e] ? ptx::ex2((m[e] - mn) * c2) : 1.f;   // 0 while m is -inf
+        m[e] = mn;
+        l[e] *= a[e];
+        lc[e] *= a[e];
+      }
 #pragma unroll
-      for (int t = 0; t < H * 2; ++t)
-        pmma::ldsm4_t(v[t], (va ^ ((2 * t + (H == 1 ? 4 : 0)) * 16)) + b * 2048);
+      for (int p = 0; p < NP; ++p)
 #pragma unroll
-      for (int p = 0; p < H * 4; ++p) {
-        uint32_t e0, o0, e1, o1;
-        F::columns(v[p / 2][p % 2 * 2], e0, o0);
-        F::columns(v[p / 2][p % 2 * 2 + 1], e1, o1);
-        float d[2][4];
-        mma_f16_new(d[0], hi[2 * b], lo[2 * b], hi[2 * b + 1], lo[2 * b + 1], e0, e1);
-        mma_f16_new(d[1], hi[2 * b], lo[2 * b], hi[2 * b + 1], lo[2 * b + 1], o0, o1);
+        for (int i = 0; i < 4; ++i) o[p][i] *= a[i & 1];
+    }
+    uint32_t hi[2][2], lo[2][2];
+    float ps[2] = {0.f, 0.f};
+#pragma unroll
+    for (int b = 0; b < 2; ++b)
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        float p[2];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const float base = m[e] == -INFINITY ? 0.f : m[e];
+          p[e] = ptx::ex2((z[b][2 * r + e] - base) * c2);
+          ps[e] += p[e];
+        }
+        f16_split(p[0] * 16384.f, p[1] * 16384.f, hi[b][r], lo[b][r]);
+        hi[b][r] = transposed(hi[b][r]);
+        lo[b][r] = transposed(lo[b][r]);
+      }
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {   // (a compensated sum, as paged_mma.cuh's)
+      const float x = ps[e] - lc[e], s = l[e] + x;
+      lc[e] = (s - l[e]) - x;
+      l[e] = s;
+    }
+#pragma unroll
+    for (int b = 0; b < 2; ++b) {
+      const float vs = (b == 0 ? scales.y : scales.w) * 0x1p-14f;
+      const float2 f = make_float2(vs, vs);
+#pragma unroll
+      for (int p = 0; p < NP; p += 2) {
+        uint32_t w[4];
+        pmma::ldsm4_t(w, (va ^ (p * 16)) + b * 2048);
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
-          float(&o)[2] = this->o[2 * p + x];
-          const float2 y = ptx::ffma2(make_float2(d[x][0], d[x][1]), f1,
-                                      ptx::ffma2(make_float2(d[x][2], d[x][3]), f2,
-                                                 make_float2(o[0], o[1])));
-          o[0] = y.x;
-          o[1] = y.y;
+          uint32_t a[4];
+          F::columns(w[2 * x], a[0], a[1]);
+          F::columns(w[2 * x + 1], a[2], a[3]);
+          float d[4];
+          mma_f16_new(d, a, hi[b][0], hi[b][1]);
+          mma_f16(d, a, lo[b][0], lo[b][1]);
+          float(&y)[4] = o[p + x];
+          const float2 u = ptx::ffma2(make_float2(d[0], d[1]), f, make_float2(y[0], y[1]));
+          const float2 v = ptx::ffma2(make_float2(d[2], d[3]), f, make_float2(y[2], y[3]));
+          y[0] = u.x;
+          y[1] = u.y;
+          y[2] = v.x;
+          y[3] = v.y;
         }
       }
     }

@@ -279,9 +279,9 @@ class QuantCache:
         to 2^-22 (2^-21 taken), sums of m of them n u each; two more roundings for V's scale in
         every tile's sum; the last term is the output's rounding.
 
-        A weight w <= 1 (the largest being 1) is held as 2^14 w = hi + 2^-11 lo in fp16.  fp16's numbers
-        are 2^-24 apart at least: 2^14 w - hi is off by no more than 2^-25, lo holds 2^11 of that to
-        2^-25, so w is also off by 2^-25 2^-11 2^-14 = 2^-50 where that is more than 2^-22 w."""
+        A weight w <= 1 (the largest being 1) is held as 2^14 w = hi + lo in fp16.  fp16's numbers are
+        2^-24 apart at least: where 2^14 w - hi is no more than 2^-25 * 2^12, lo holds it to 2^-25 only,
+        so w is also off by 2^-25 2^-14 = 2^-39."""
         seqs, hkv, G, d = self.seqs, self.hkv, self.G, self.d
         out = np.zeros((seqs, hkv * G, d))
         tol = np.zeros_like(out)
@@ -315,7 +315,7 @@ class QuantCache:
                     tol[tb // self.tables, g0 * G + g] = (
                         2 * (p * e_z) @ np.abs(v) + 2 * (p @ e_z) * mag +
                         (2 * m * u23 + 66 * u23 + t_p) * mag + half * np.abs(o) + 1e-30 +
-                        2.0 ** -50 * p.max() * np.abs(v).sum(0))
+                        2.0 ** -39 * p.max() * np.abs(v).sum(0))
                     out[tb // self.tables, g0 * G + g] = o
         return out, tol
 
