@@ -304,41 +304,53 @@ __device__ __forceinline__ void merge_parts(const float (&m)[kB], const float (&
   }
 }
 
-// A new row beside a stage, as row r of the block in that stage and in the pool, both for K or both
-// for V (quant_codes.cuh has the numbers).  `piece(r, p)`: byte of the stage where a piece lies; `pool`:
-// the block's first row; `old`: the block's scale, returned as it is afterwards.
-template <typename T, typename F, typename At>
-__device__ __forceinline__ float put_row(unsigned char* stage, At piece, const unsigned char* fresh,
-                                         unsigned char* pool, float* scale, float old, int r,
-                                         int d) {
-  const int lane = threadIdx.x & 31, pieces = d / 16;
+// A new row beside a stage (K's at `fresh`, V's kNewRow behind it), as row r of a block (quant_codes.cuh
+// has the numbers): in the stage, where the block's rows begin `above` rows down, and in the pools at
+// `at`.  scale: the block's, K's and V's; returned as they are afterwards.  K by the warp's first half, V
+// by the other.
+template <typename C>
+__device__ __forceinline__ float2 put_rows(unsigned char* stage, int above,
+                                           const unsigned char* fresh, const PagedArgs& a,
+                                           int64_t at, int64_t scale_at, float2 scale, int r) {
+  using T = typename C::P::T;
+  using F = typename C::P::F;
+  const int lane = threadIdx.x & 31, part = lane & 15, pieces = a.d / 16;
+  const bool v = lane >= 16;
+  unsigned char* pool = (unsigned char*)(v ? a.vp : a.kp) + at;
+  auto place = [&](int row, int p) {
+    return reinterpret_cast<uint4*>(stage + (v ? pmma::v_piece<C::RT, C::H>(above + row, p)
+                                               : pmma::k_piece<C::RT, C::H>(above + row, p)));
+  };
   quant::Piece<T> x;
   uint32_t top = 0;
-  if (lane < pieces) {
+  if (part < pieces) {
 #pragma unroll
     for (int i = 0; i < quant::Piece<T>::kLoads; ++i)
-      x.w[i] = reinterpret_cast<const uint4*>(fresh)[lane * quant::Piece<T>::kLoads + i];
+      x.w[i] = reinterpret_cast<const uint4*>(fresh + (v ? C::kNewRow : 0))
+          [part * quant::Piece<T>::kLoads + i];
     top = x.top(0u);
   }
-  top = __reduce_max_sync(0xffffffffu, top);
-  if (r == 0) old = 0.f;   // the block is begun anew
+#pragma unroll
+  for (int o = 1; o < 8; o <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+  top = __shfl_sync(0xffffffffu, top, lane & 16);
+  const float old = r == 0 ? 0.f : v ? scale.y : scale.x;   // (a block that is begun anew has none)
   const float now = fmaxf(quant::scale_for<F>(top), old), inv = 1.f / now;
   if (now > old) {
-    for (int i = lane; i < r * pieces; i += 32) {
-      const int row = i / pieces, p = i - row * pieces;
-      uint4* at = reinterpret_cast<uint4*>(stage + piece(row, p));
-      const uint4 c = quant::again<F>(*at, old * inv);
-      *at = c;
+    for (int i = part; i < r * pieces; i += 16) {
+      const int row = i / pieces;
+      uint4* from = place(row, i - row * pieces);
+      const uint4 c = quant::again<F>(*from, old * inv);
+      *from = c;
       reinterpret_cast<uint4*>(pool)[i] = c;
     }
-    if (lane == 0) *scale = now;
+    if (part == 0) (v ? a.vs : a.ks)[scale_at] = now;
   }
-  if (lane < pieces) {
+  if (part < pieces) {
     const uint4 c = quant::encode<F>(x, inv);
-    *reinterpret_cast<uint4*>(stage + piece(r, lane)) = c;
-    reinterpret_cast<uint4*>(pool + r * d)[lane] = c;
+    *place(r, part) = c;
+    reinterpret_cast<uint4*>(pool + r * a.d)[part] = c;
   }
-  return now;
+  return make_float2(__shfl_sync(0xffffffffu, now, 0), __shfl_sync(0xffffffffu, now, 16));
 }
 
 // kPWarps: warps of a CTA.
@@ -696,15 +708,12 @@ paged_decode_kernel(const __grid_constant__ PagedArgs a) {
             const int64_t sc =
                 __shfl_sync(0xffffffffu, (long long)(hi ? cur.scale2 : cur.scale), src);
             if (in_pool && (mask >> r & 1) && at == block_at + rb * d) {
-              const float ks = put_row<T, typename P::F>(
-                  st, [=](int row, int p) { return pmma::k_piece<RT, H>(above + row, p); }, beside,
-                  (unsigned char*)a.kp + block_at, a.ks + sc, hi ? scales.z : scales.x, rb, d);
-              const float vs = put_row<T, typename P::F>(
-                  st, [=](int row, int p) { return pmma::v_piece<RT, H>(above + row, p); },
-                  beside + C::kNewRow, (unsigned char*)a.vp + block_at, a.vs + sc,
-                  hi ? scales.w : scales.y, rb, d);
-              (hi ? scales.z : scales.x) = ks;
-              (hi ? scales.w : scales.y) = vs;
+              const float2 now =
+                  put_rows<C>(st, above, beside, a, block_at, sc,
+                              hi ? make_float2(scales.z, scales.w) : make_float2(scales.x, scales.y),
+                              rb);
+              (hi ? scales.z : scales.x) = now.x;
+              (hi ? scales.w : scales.y) = now.y;
             } else if (in_pool && lane == 0) {
               raise_dev(a.hdr, DEV_PAGE_ID, (unsigned)unit);
             }
@@ -872,6 +881,76 @@ paged_decode_kernel(const __grid_constant__ PagedArgs a) {
     __threadfence();
   }
   __syncthreads();
+  if constexpr (P::kCodes) {
+    // The parts come through the rings, which are free now: many at a time with little code.  (Few CTAs
+    // get here, so its instructions are not at hand: 16 unrolled loads, as below, took 4 us.)
+    const int part4s = (kPartHead + G * D) / 4;   // 16-byte pieces of a part
+    const int room = kPWarps * S * C::kStage / 16 / part4s;
+    constexpr int kSlices = 8 * (D / 4) > kPThreads ? 8 * (D / 4) / kPThreads : 1;   // of a thread
+    const uint32_t to = ptx::smem_u32(sm.ring);
+    const float* in = reinterpret_cast<const float*>(sm.ring);
+#pragma unroll 1
+    for (int y = 0; y < 2; ++y) {
+      if (!sm.won[y]) continue;
+      float M[kSlices], L[kSlices];
+      float4 acc[kSlices];
+#pragma unroll
+      for (int j = 0; j < kSlices; ++j) {
+        M[j] = -INFINITY;
+        L[j] = 0.f;
+        acc[j] = make_float4(0.f, 0.f, 0.f, 0.f);
+      }
+#pragma unroll 1
+      for (int k0 = 0; k0 < parts[y]; k0 += room) {
+        const int n = min(room, parts[y] - k0);
+        for (int k = warp; k < n; k += kPWarps) {
+          // (the unit is the second of its first CTA)
+          const int slot = 2 * (first[y] + k0 + k) + (k0 + k == 0 ? 1 : 0);
+          const float* W = a.part + (int64_t)slot * kPartFloats + lane * 4;
+          const uint32_t dst = to + (k * part4s + lane) * 16;
+#pragma unroll 4
+          for (int i = 0; i < part4s - lane; i += 32) cp_async16(dst + i * 16, W + i * 4);
+        }
+        cp_async_commit();
+        cp_async_wait<0>();
+        __syncthreads();
+#pragma unroll
+        for (int j = 0; j < kSlices; ++j) {
+          const int idx = tid + j * kPThreads, g = idx / (D / 4);
+          if (idx >= nsl) continue;
+          float mn = M[j];
+#pragma unroll 8
+          for (int k = 0; k < n; ++k) mn = fmaxf(mn, in[k * part4s * 4 + g]);
+          const float base = mn == -INFINITY ? 0.f : mn;
+          const float f = ptx::ex2((M[j] - base) * a.scale.c2);   // 0 while M is -inf
+          M[j] = mn;
+          L[j] *= f;
+          acc[j] = make_float4(acc[j].x * f, acc[j].y * f, acc[j].z * f, acc[j].w * f);
+#pragma unroll 4
+          for (int k = 0; k < n; ++k) {
+            const float* W = in + k * part4s * 4;
+            const float w = ptx::ex2((W[g] - base) * a.scale.c2);
+            const float4 o = *reinterpret_cast<const float4*>(W + kPartHead + idx * 4);
+            L[j] = fmaf(W[8 + g], w, L[j]);
+            acc[j].x = fmaf(o.x, w, acc[j].x);
+            acc[j].y = fmaf(o.y, w, acc[j].y);
+            acc[j].z = fmaf(o.z, w, acc[j].z);
+            acc[j].w = fmaf(o.w, w, acc[j].w);
+          }
+        }
+        __syncthreads();
+      }
+#pragma unroll
+      for (int j = 0; j < kSlices; ++j) {
+        const int idx = tid + j * kPThreads, g = idx / (D / 4), col = (idx - g * (D / 4)) * 4;
+        if (idx >= nsl || col >= d) continue;
+        const float inv = L[j] != 0.f ? 1.f / L[j] : 0.f;
+        store4((T*)a.out + ((int64_t)units[y] * G + g) * d + col,
+               make_float4(acc[j].x * inv, acc[j].y * inv, acc[j].z * inv, acc[j].w * inv));
+      }
+    }
+    return;
+  }
   // groups of threads take the parts in turn, and their sums are added in order
   const int groups = nsl < kPThreads ? kPThreads / nsl : 1;
 #pragma unroll 1
