@@ -321,14 +321,16 @@ __device__ __forceinline__ float2 put_rows(unsigned char* stage, int above,
     return reinterpret_cast<uint4*>(stage + (v ? pmma::v_piece<C::RT, C::H>(above + row, p)
                                                : pmma::k_piece<C::RT, C::H>(above + row, p)));
   };
-  quant::Piece<T> x;
+  // (16 elements of a lane: what makes a piece of codes)
+  constexpr int kLoads = (int)sizeof(T);
+  quant::Piece<T> x[kLoads];
   uint32_t top = 0;
-  if (part < pieces) {
 #pragma unroll
-    for (int i = 0; i < quant::Piece<T>::kLoads; ++i)
-      x.w[i] = reinterpret_cast<const uint4*>(fresh + (v ? C::kNewRow : 0))
-          [part * quant::Piece<T>::kLoads + i];
-    top = x.top(0u);
+  for (int i = 0; i < kLoads; ++i) {
+    x[i].w = make_uint4(0u, 0u, 0u, 0u);
+    if (part < pieces)
+      x[i].w = reinterpret_cast<const uint4*>(fresh + (v ? C::kNewRow : 0))[part * kLoads + i];
+    top = x[i].finite_top(top);
   }
 #pragma unroll
   for (int o = 1; o < 8; o <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
@@ -346,7 +348,11 @@ __device__ __forceinline__ float2 put_rows(unsigned char* stage, int above,
     if (part == 0) (v ? a.vs : a.ks)[scale_at] = now;
   }
   if (part < pieces) {
-    const uint4 c = quant::encode<F>(x, inv);
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      w[i] = x[4 * i / quant::Piece<T>::kN].template codes<F>(4 * i % quant::Piece<T>::kN, inv, false);
+    const uint4 c = make_uint4(w[0], w[1], w[2], w[3]);
     *place(r, part) = c;
     reinterpret_cast<uint4*>(pool + r * a.d)[part] = c;
   }

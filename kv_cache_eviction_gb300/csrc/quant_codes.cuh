@@ -22,6 +22,8 @@ namespace quant {
 constexpr int kBlock = 16;     // rows
 constexpr int kLeast = -96;
 
+// Formats: pack4 takes any float, pack4_held only what is within the code's range (after a scale_for of
+// a maximum that is finite).
 struct E4M3 {
   // 448 = 0.875 * 2^9: a mantissa past 0.875 (1.75 as 1.m) needs a step more
   static constexpr int kTopExp = 9;
@@ -34,6 +36,10 @@ struct E4M3 {
   }
   static __device__ __forceinline__ uint32_t pack4(float x, float y, float z, float w) {
     return pack2(x, y) | pack2(z, w) << 16;
+  }
+  static __device__ __forceinline__ uint32_t pack4_held(float x, float y, float z, float w,
+                                                        float by) {
+    return pack4(x * by, y * by, z * by, w * by);
   }
   // the numbers of a word's codes 0, 1 and 2, 3
   static __device__ __forceinline__ void halves(uint32_t w, uint32_t& lo, uint32_t& hi) {
@@ -62,6 +68,14 @@ struct Int8 {
     asm("cvt.pack.sat.s8.s32.b32 %0, %1, %2, %3;" : "=r"(r) : "r"(b), "r"(a), "r"(hi));
     return r;
   }
+  // x times `by` in the last places of 1.5 * 2^23, rounded there: its low byte is the code
+  static __device__ __forceinline__ uint32_t pack4_held(float x, float y, float z, float w,
+                                                        float by) {
+    constexpr float kBase = 12582912.f;
+    const uint32_t a = __float_as_uint(fmaf(x, by, kBase)), b = __float_as_uint(fmaf(y, by, kBase));
+    const uint32_t c = __float_as_uint(fmaf(z, by, kBase)), d = __float_as_uint(fmaf(w, by, kBase));
+    return __byte_perm(__byte_perm(a, b, 0x0040), __byte_perm(c, d, 0x0040), 0x5410);
+  }
   // code + 128 in the last places of 1024: less 1152 it is the code, exactly
   static __device__ __forceinline__ uint32_t less(uint32_t x) {
     uint32_t r;
@@ -82,12 +96,6 @@ struct Int8 {
 
 __device__ __forceinline__ float2 floats_of(uint32_t h2) {
   return __half22float2(*reinterpret_cast<const __half2*>(&h2));
-}
-
-// Bits of the larger of m and |x|, non-finite ones left out (m: bits of a finite magnitude).
-__device__ __forceinline__ uint32_t finite_max(uint32_t m, float x) {
-  const uint32_t u = __float_as_uint(x) & 0x7FFFFFFFu;
-  return u < 0x7F800000u && u > m ? u : m;
 }
 
 // The scale of a block whose largest finite magnitude has the bits `top`.
@@ -112,56 +120,46 @@ __device__ __forceinline__ uint4 again(uint4 c, float by) {
   return c;
 }
 
-// 16 elements of a row, as loaded.
+// 16 bytes of a row: kN elements.
 template <typename T>
-struct Piece;
-template <>
-struct Piece<float> {
-  static constexpr int kLoads = 4;   // of 16 bytes
-  uint4 w[kLoads];
-  __device__ __forceinline__ float at(int i) const {
-    return __uint_as_float(reinterpret_cast<const uint32_t*>(w)[i]);
+struct Piece {
+  static constexpr int kN = 16 / (int)sizeof(T);
+  uint4 w;
+  __device__ __forceinline__ uint32_t word(int i) const {
+    return i == 0 ? w.x : i == 1 ? w.y : i == 2 ? w.z : w.w;
   }
+  __device__ __forceinline__ float at(int i) const {
+    if (sizeof(T) == 4) return __uint_as_float(word(i));
+    return __uint_as_float(i & 1 ? word(i / 2) & 0xFFFF0000u : word(i / 2) << 16);
+  }
+  // The largest of m and the magnitudes' bits, infinities and NaN among them: kInf and more.  (Of
+  // bf16, two magnitudes side by side in m; see whole().)
   __device__ __forceinline__ uint32_t top(uint32_t m) const {
 #pragma unroll
-    for (int i = 0; i < 16; ++i) m = finite_max(m, at(i));
+    for (int i = 0; i < 4; ++i)
+      m = sizeof(T) == 4 ? max(m, word(i) & 0x7FFFFFFFu) : __vmaxu2(m, word(i) & 0x7FFF7FFFu);
     return m;
   }
-};
-template <>
-struct Piece<__nv_bfloat16> {
-  static constexpr int kLoads = 2;
-  uint4 w[kLoads];
-  __device__ __forceinline__ float at(int i) const {
-    const uint32_t x = reinterpret_cast<const uint32_t*>(w)[i >> 1];
-    return __uint_as_float(i & 1 ? x & 0xFFFF0000u : x << 16);
+  static __device__ __forceinline__ uint32_t whole(uint32_t m) {
+    return sizeof(T) == 4 ? m : max(m << 16, m & 0xFFFF0000u);
   }
-  __device__ __forceinline__ uint32_t top(uint32_t m) const {
-    // both halves at a time; one by one where a half is not finite
-    uint32_t p = 0;
+  // The same without infinities and NaN.
+  __device__ __forceinline__ uint32_t finite_top(uint32_t m) const {
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-      p = __vmaxu2(p, reinterpret_cast<const uint32_t*>(w)[i] & 0x7FFF7FFFu);
-    const uint32_t lo = p << 16, hi = p & 0xFFFF0000u, x = lo > hi ? lo : hi;
-    if (x < 0x7F800000u) return x > m ? x : m;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const uint32_t y = reinterpret_cast<const uint32_t*>(w)[i];
-      m = finite_max(finite_max(m, __uint_as_float(y << 16)), __uint_as_float(y & 0xFFFF0000u));
+    for (int i = 0; i < kN; ++i) {
+      const uint32_t u = __float_as_uint(at(i)) & 0x7FFFFFFFu;
+      m = u < 0x7F800000u && u > m ? u : m;
     }
     return m;
   }
+  // Four codes from element i on, x times `inv`.  held: every element is finite and in range.
+  template <typename F>
+  __device__ __forceinline__ uint32_t codes(int i, float inv, bool held) const {
+    if (held) return F::pack4_held(at(i), at(i + 1), at(i + 2), at(i + 3), inv);
+    return F::pack4(at(i) * inv, at(i + 1) * inv, at(i + 2) * inv, at(i + 3) * inv);
+  }
 };
-template <typename F, typename T>
-__device__ __forceinline__ uint4 encode(const Piece<T>& x, float inv) {
-  uint4 c;
-  uint32_t* w = reinterpret_cast<uint32_t*>(&c);
-#pragma unroll
-  for (int i = 0; i < 4; ++i)
-    w[i] = F::pack4(x.at(4 * i) * inv, x.at(4 * i + 1) * inv, x.at(4 * i + 2) * inv,
-                    x.at(4 * i + 3) * inv);
-  return c;
-}
+constexpr uint32_t kInf = 0x7F800000u;
 
 }  // namespace quant
 }  // namespace kv

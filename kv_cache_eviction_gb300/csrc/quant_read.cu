@@ -7,7 +7,7 @@ namespace kv {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kPieces = 4;   // pieces of 16 codes of K (and of V) of a lane at a time
+constexpr int kPieces = 4;   // 16-byte pieces of K's rows (and of V's) of a lane at a time
 
 struct QReadArgs {
   const unsigned char *kp, *vp;
@@ -19,43 +19,52 @@ struct QReadArgs {
   int64_t rows, dst_vec, page_stride, num_slots;   // dst_vec: 16-byte pieces from row to row
   int per_row, pad_shift;    // pieces of a row, and log2 of its padded pieces (7: whole groups)
   int Hp, d, shift;
+  int dvec, div_dvec;        // pieces of a head's row; x / dvec = x * div_dvec >> 20
+};
+
+// kN codes: those of 16 bytes of a row.
+template <typename T>
+struct Code;
+template <>
+struct Code<__nv_bfloat16> {
+  uint2 w;
+  __device__ __forceinline__ void load(const unsigned char* p) {
+    w = *reinterpret_cast<const uint2*>(p);
+  }
+  template <typename F>
+  __device__ __forceinline__ uint4 row(float s) const {
+    auto two = [&](uint32_t h) {
+      const float2 x = quant::floats_of(h);
+      const __nv_bfloat162 y = __floats2bfloat162_rn(x.x * s, x.y * s);
+      return *reinterpret_cast<const uint32_t*>(&y);
+    };
+    uint32_t a, b, c, d;
+    F::halves(w.x, a, b);
+    F::halves(w.y, c, d);
+    return make_uint4(two(a), two(b), two(c), two(d));
+  }
+};
+template <>
+struct Code<float> {
+  uint32_t w;
+  __device__ __forceinline__ void load(const unsigned char* p) {
+    w = *reinterpret_cast<const uint32_t*>(p);
+  }
+  template <typename F>
+  __device__ __forceinline__ uint4 row(float s) const {
+    uint32_t a, b;
+    F::halves(w, a, b);
+    const float2 x = quant::floats_of(a), y = quant::floats_of(b);
+    return make_uint4(__float_as_uint(x.x * s), __float_as_uint(x.y * s), __float_as_uint(y.x * s),
+                      __float_as_uint(y.y * s));
+  }
 };
 
 template <typename T, typename F>
-__device__ __forceinline__ void put(uint4* dst, uint4 c, float s) {
-  const uint32_t* w = reinterpret_cast<const uint32_t*>(&c);
-#pragma unroll
-  for (int i = 0; i < 4; i += (sizeof(T) == 2 ? 2 : 1)) {
-    uint4 o;
-    uint32_t* x = reinterpret_cast<uint32_t*>(&o);
-    uint32_t lo, hi;
-    F::halves(w[i], lo, hi);
-    float2 a = quant::floats_of(lo), b = quant::floats_of(hi);
-    if (sizeof(T) == 4) {
-      o = make_uint4(__float_as_uint(a.x * s), __float_as_uint(a.y * s), __float_as_uint(b.x * s),
-                     __float_as_uint(b.y * s));
-      dst[i] = o;
-    } else {
-      auto two = [&](float p, float q) {
-        const __nv_bfloat162 y = __floats2bfloat162_rn(p * s, q * s);
-        return *reinterpret_cast<const uint32_t*>(&y);
-      };
-      x[0] = two(a.x, a.y);
-      x[1] = two(b.x, b.y);
-      F::halves(w[i + 1 < 4 ? i + 1 : i], lo, hi);
-      a = quant::floats_of(lo);
-      b = quant::floats_of(hi);
-      x[2] = two(a.x, a.y);
-      x[3] = two(b.x, b.y);
-      dst[i / 2] = o;
-    }
-  }
-}
-
-template <typename T, typename F>
-__global__ void __launch_bounds__(kThreads) quant_read_kernel(const __grid_constant__ QReadArgs a) {
-  constexpr int kOut = (int)sizeof(T);   // 16-byte pieces out of a piece of 16 codes
-  const int lane = threadIdx.x & 31, page = 1 << a.shift, dv = a.d / 16;
+__global__ void __launch_bounds__(kThreads, 4)
+quant_read_kernel(const __grid_constant__ QReadArgs a) {
+  constexpr int kN = 16 / (int)sizeof(T);   // codes of a piece
+  const int lane = threadIdx.x & 31, page = 1 << a.shift;
   ptx::griddep_launch_dependents();
   ptx::griddep_wait();   // nothing of the call before is read or written until it ends
   int64_t rows = a.rows;
@@ -65,7 +74,7 @@ __global__ void __launch_bounds__(kThreads) quant_read_kernel(const __grid_const
   const int64_t step = (int64_t)gridDim.x * (kThreads / 32) * in_group;
   for (int64_t row0 = warp * in_group; row0 < rows; row0 += step) {
     for (int x0 = 0; x0 < a.per_row; x0 += 128) {
-      uint4 kc[kPieces], vc[kPieces];
+      Code<T> kc[kPieces], vc[kPieces];
       float ks[kPieces], vs[kPieces];
       bool in[kPieces];
 #pragma unroll
@@ -79,11 +88,12 @@ __global__ void __launch_bounds__(kThreads) quant_read_kernel(const __grid_const
           in[j] = slot >= 0 && slot < a.num_slots;
           if (in[j]) {
             const int64_t pg = slot >> a.shift;
-            const int r = (int)(slot & (page - 1)), h = x / dv;
-            const int64_t at = pg * a.page_stride + ((int64_t)h * page + r) * a.d + (x - h * dv) * 16;
+            const int r = (int)(slot & (page - 1)), h = x * a.div_dvec >> 20;
+            const int64_t at =
+                pg * a.page_stride + ((int64_t)h * page + r) * a.d + (x - h * a.dvec) * kN;
             const int64_t sc = (pg * a.Hp + h) * (page / quant::kBlock) + r / quant::kBlock;
-            kc[j] = *reinterpret_cast<const uint4*>(a.kp + at);
-            vc[j] = *reinterpret_cast<const uint4*>(a.vp + at);
+            kc[j].load(a.kp + at);
+            vc[j].load(a.vp + at);
             ks[j] = a.ks[sc];
             vs[j] = a.vs[sc];
           } else if (slot != -1) {
@@ -97,8 +107,8 @@ __global__ void __launch_bounds__(kThreads) quant_read_kernel(const __grid_const
         const int i = lane + 32 * j;
         const int64_t row = row0 + (i >> a.pad_shift);
         const int x = x0 + (i & ((1 << a.pad_shift) - 1));
-        put<T, F>(a.k + row * a.dst_vec + x * kOut, kc[j], ks[j]);
-        put<T, F>(a.v + row * a.dst_vec + x * kOut, vc[j], vs[j]);
+        a.k[row * a.dst_vec + x] = kc[j].template row<F>(ks[j]);
+        a.v[row * a.dst_vec + x] = vc[j].template row<F>(vs[j]);
       }
     }
   }
@@ -128,12 +138,16 @@ cudaError_t launch_quant_read(const PagedShape& s, int format, const void* kp, c
                               WsHeader* hdr, cudaStream_t st) {
   int shift = 0;
   while ((1 << shift) < s.page) ++shift;
-  const int per_row = s.Hp() * (s.d / 16);
+  const int dvec = s.d * s.esize() / 16, per_row = s.Hp() * dvec;
   int pad = 0;
   while (pad < 7 && (1 << pad) < per_row) ++pad;
+  // x / dvec by a product: x < 256 * 32, and the product is too large by less than dvec / 2^20 a
+  // unit, so the quotient is exact (8192 * 32 < 2^20)
+  const int div = ((1 << 20) + dvec - 1) / dvec;
   const QReadArgs a{(const unsigned char*)kp, (const unsigned char*)vp, ks, vs, slots, n_rows,
                     (uint4*)k, (uint4*)v, hdr, rows, dst_stride * s.esize() / 16, s.page_stride,
-                    s.num_pages << shift, per_row, pad, s.Hp(), s.d, shift};
+                    s.num_pages << shift, per_row, pad, s.Hp(), s.d, shift, dvec,
+                    div};
   if (s.dtype == KV_BF16)
     return format == KV_E4M3 ? launch<__nv_bfloat16, quant::E4M3>(a, st)
                              : launch<__nv_bfloat16, quant::Int8>(a, st);

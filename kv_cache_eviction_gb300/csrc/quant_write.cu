@@ -11,7 +11,9 @@ namespace kv {
 namespace {
 
 using quant::Piece;
-constexpr int kThreads = 256;
+constexpr int kThreads = 128;
+// CTAs of an SM: as many as the pieces in registers allow
+constexpr int resident(int pieces) { return pieces <= 4 ? 8 : pieces <= 8 ? 6 : 3; }
 
 struct QWriteArgs {
   const uint4* src[2];     // k, v
@@ -21,36 +23,48 @@ struct QWriteArgs {
   const int64_t* n_rows;
   WsHeader* hdr;
   int64_t rows, src_vec, page_stride, num_slots;   // src_vec: 16-byte pieces from row to row
-  int Hp, d, shift, window_shift;
+  int Hp, d, shift, window_shift, pieces;          // pieces: of a head's row
 };
 
-template <typename T, typename F>
-__global__ void __launch_bounds__(kThreads) quant_write_kernel(const __grid_constant__ QWriteArgs a) {
-  constexpr int kPer = Piece<T>::kLoads;
-  constexpr int kPieces = quant::kBlock * 8 / 32;    // of a lane: a block of rows of up to 128
-  const int lane = threadIdx.x & 31;
-  const int page = 1 << a.shift, dv = a.d / 16, window = 1 << a.window_shift;
+// KP: pieces of a lane, for 16 rows of a head of up to 2 KP pieces.
+template <typename T, typename F, int KP>
+__global__ void __launch_bounds__(kThreads, resident(KP))
+quant_write_kernel(const __grid_constant__ QWriteArgs a) {
+  constexpr int kN = Piece<T>::kN;
+  constexpr int kLanes = 2 * KP, kStep = 32 / kLanes;   // lanes of a row, rows at a time
+  const int lane = threadIdx.x & 31, lr = lane / kLanes, lp = lane % kLanes;
+  const int page = 1 << a.shift, window = 1 << a.window_shift, pairs = a.Hp * 2;
   ptx::griddep_launch_dependents();
   ptx::griddep_wait();   // nothing of the call before is read or written until it ends
   int64_t rows = a.rows;
   if (a.n_rows != nullptr) rows = min(rows, *a.n_rows);
-  const int64_t items = cdiv(rows, window) * a.Hp * 2;
-  const int64_t step = (int64_t)gridDim.x * (kThreads / 32);
-  for (int64_t it = (int64_t)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5); it < items;
-       it += step) {
-    const int t = (int)(it & 1);
-    const int64_t win = (it >> 1) / a.Hp;
-    const int h = (int)((it >> 1) - win * a.Hp);
-    const int64_t i0 = win << a.window_shift;
-    // lane i: the slot of row i0 + i, for the window and the 15 rows behind it; lane 31: that of
-    // the row before
+  // a warp's items: windows of rows, and of each the pairs (head, K or V)
+  const int warps = (int)gridDim.x * (kThreads / 32);
+  const int me = (int)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
+  const int win_step = warps / pairs, pair_step = warps - win_step * pairs;
+  int64_t win = me / pairs;
+  int pair = me - (int)win * pairs;
+  // lane i: the slot of row i0 + i, for the window and the 15 rows behind it; lane 31: that of the
+  // row before.  (-1 outside the rows)
+  auto load_slot = [&](int64_t i0) {
     const int64_t row = lane == 31 ? i0 - 1 : i0 + lane;
-    int64_t slot = -1;
-    if (row >= 0 && row < rows && (lane == 31 || lane < window + 15)) slot = a.slots[row];
+    return row >= 0 && row < rows && (lane == 31 || lane < window + 15) ? a.slots[row] : (int64_t)-1;
+  };
+  int64_t next = load_slot(win << a.window_shift);
+  while ((win << a.window_shift) < rows) {
+    const int t = pair & 1, h = pair >> 1;
+    const int64_t i0 = win << a.window_shift, slot = next;
+    win += win_step;
+    pair += pair_step;
+    if (pair >= pairs) {
+      pair -= pairs;
+      ++win;
+    }
+    next = load_slot(win << a.window_shift);   // (its latency beside this item's work)
     const bool ok = slot >= 0 && slot < a.num_slots;
     if (!ok && slot != -1 && lane < window && h == 0 && t == 0)
-      raise_dev(a.hdr, DEV_PAGE_ID, (unsigned)row);
-    int64_t before = __shfl_sync(0xffffffffu, (long long)slot, (lane + 31) & 31);
+      raise_dev(a.hdr, DEV_PAGE_ID, (unsigned)(i0 + lane));
+    const int64_t before = __shfl_sync(0xffffffffu, (long long)slot, (lane + 31) & 31);
     const bool goes_on = ok && lane < 31 && (slot & (quant::kBlock - 1)) != 0 && before == slot - 1;
     const uint32_t more = __ballot_sync(0xffffffffu, goes_on);
     uint32_t starts = __ballot_sync(0xffffffffu, ok && !goes_on && lane < window);
@@ -58,48 +72,61 @@ __global__ void __launch_bounds__(kThreads) quant_write_kernel(const __grid_cons
       const int s = __ffs(starts) - 1;
       const int n = __ffs(~(more >> s >> 1));   // rows of the run (at most 16, within lanes 0..30)
       const int64_t slot0 = __shfl_sync(0xffffffffu, (long long)slot, s);
+      const bool mine = lp < a.pieces;
+      Piece<T> x[KP];
+      const uint4* src = a.src[t] + (i0 + s + lr) * a.src_vec + h * a.pieces + lp;
+#pragma unroll
+      for (int j = 0; j < KP; ++j) {
+        x[j].w = make_uint4(0u, 0u, 0u, 0u);
+        if (mine && lr + j * kStep < n) x[j].w = src[j * kStep * a.src_vec];
+      }
       const int first = (int)(slot0 & (quant::kBlock - 1));
       const int64_t pg = slot0 >> a.shift;
       const int r = (int)(slot0 & (page - 1));
-      unsigned char* dst = a.pool[t] + pg * a.page_stride + ((int64_t)h * page + r) * a.d;
       float* sc = a.scale[t] + (pg * a.Hp + h) * (page / quant::kBlock) + r / quant::kBlock;
       const float old = first > 0 ? *sc : 0.f;
-      const uint4* src = a.src[t] + (i0 + s) * a.src_vec + h * (dv * kPer);
-      Piece<T> x[kPieces];
+      unsigned char* dst = a.pool[t] + pg * a.page_stride + ((int64_t)h * page + r) * a.d;
       uint32_t top = 0;
 #pragma unroll
-      for (int j = 0; j < kPieces; ++j) {
-        const int p = lane + 32 * j, pr = p / dv;
-        if (pr < n) {
-          const uint4* from = src + pr * a.src_vec + (p - pr * dv) * kPer;
+      for (int j = 0; j < KP; ++j) top = x[j].top(top);
+      top = __reduce_max_sync(0xffffffffu, Piece<T>::whole(top));
+      const bool finite = top < quant::kInf;
+      if (!finite) {
+        top = 0;
 #pragma unroll
-          for (int k = 0; k < kPer; ++k) x[j].w[k] = from[k];
-        }
+        for (int j = 0; j < KP; ++j) top = x[j].finite_top(top);
+        top = __reduce_max_sync(0xffffffffu, top);
       }
-#pragma unroll
-      for (int j = 0; j < kPieces; ++j)
-        if ((lane + 32 * j) / dv < n) top = x[j].top(top);
-      top = __reduce_max_sync(0xffffffffu, top);
       const float now = fmaxf(quant::scale_for<F>(top), old), inv = 1.f / now;
       if (now > old) {
         // (the run's rows are contiguous in the pool, and so are those before it)
-        for (int p = lane; p < first * dv; p += 32) {
+        for (int p = lane; p < first * (a.d / 16); p += 32) {
           uint4* at = reinterpret_cast<uint4*>(dst - first * a.d) + p;
           *at = quant::again<F>(*at, old * inv);
         }
         if (lane == 0) *sc = now;
       }
+      dst += lr * a.d + lp * kN;
+      auto put = [&](bool held) {
 #pragma unroll
-      for (int j = 0; j < kPieces; ++j) {
-        const int p = lane + 32 * j;
-        if (p / dv < n) reinterpret_cast<uint4*>(dst)[p] = quant::encode<F>(x[j], inv);
-      }
+        for (int j = 0; j < KP; ++j) {
+          if (!mine || lr + j * kStep >= n) continue;
+          unsigned char* at = dst + j * kStep * a.d;
+          if (kN == 8)
+            *reinterpret_cast<uint2*>(at) = make_uint2(x[j].template codes<F>(0, inv, held),
+                                                       x[j].template codes<F>(4 % kN, inv, held));
+          else
+            *reinterpret_cast<uint32_t*>(at) = x[j].template codes<F>(0, inv, held);
+        }
+      };
+      if (finite) put(true);
+      else put(false);
     }
   }
 }
 
-template <typename T, typename F>
-cudaError_t launch(const PagedShape& s, QWriteArgs& a, cudaStream_t st) {
+template <typename T, typename F, int KP>
+cudaError_t launch_kp(const PagedShape& s, QWriteArgs& a, cudaStream_t st) {
   // rows of a window: 16, or fewer where that leaves warps without work
   const int64_t want = (int64_t)num_sms() * 32;
   a.window_shift = 4;
@@ -107,8 +134,9 @@ cudaError_t launch(const PagedShape& s, QWriteArgs& a, cudaStream_t st) {
     --a.window_shift;
   const int64_t items = cdiv(a.rows, (int64_t)1 << a.window_shift) * s.Hp() * 2;
   int64_t grid = cdiv(items, kThreads / 32);
-  const bool full = grid >= (int64_t)num_sms() * 4;
-  if (grid > (int64_t)num_sms() * 8) grid = (int64_t)num_sms() * 8;
+  const int64_t most = (int64_t)num_sms() * resident(KP);
+  const bool full = grid >= most;
+  if (full) grid = most;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3((unsigned)grid);
   cfg.blockDim = dim3(kThreads);
@@ -116,9 +144,16 @@ cudaError_t launch(const PagedShape& s, QWriteArgs& a, cudaStream_t st) {
   cudaLaunchAttribute attr[1] = {pdl_attribute()};
   cfg.attrs = attr;
   cfg.numAttrs = full ? 1 : 0;
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, quant_write_kernel<T, F>, a);
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, quant_write_kernel<T, F, KP>, a);
   if (e == cudaSuccess) count_launches(1);
   return e;
+}
+
+template <typename T, typename F>
+cudaError_t launch(const PagedShape& s, QWriteArgs& a, cudaStream_t st) {
+  constexpr int kMost = 16 * 128 / 32 / Piece<T>::kN;   // at d = 128
+  if (s.d <= 32) return launch_kp<T, F, kMost / 4>(s, a, st);
+  return s.d <= 64 ? launch_kp<T, F, kMost / 2>(s, a, st) : launch_kp<T, F, kMost>(s, a, st);
 }
 }  // namespace
 
@@ -130,7 +165,7 @@ cudaError_t launch_quant_write(const PagedShape& s, int format, const void* k, c
   while ((1 << shift) < s.page) ++shift;
   QWriteArgs a{{(const uint4*)k, (const uint4*)v}, {(unsigned char*)kp, (unsigned char*)vp},
                {ks, vs}, slots, n_rows, hdr, rows, src_stride * s.esize() / 16, s.page_stride,
-               s.num_pages << shift, s.Hp(), s.d, shift, 0};
+               s.num_pages << shift, s.Hp(), s.d, shift, 0, s.d * s.esize() / 16};
   if (s.dtype == KV_BF16)
     return format == KV_E4M3 ? launch<__nv_bfloat16, quant::E4M3>(s, a, st)
                              : launch<__nv_bfloat16, quant::Int8>(s, a, st);
