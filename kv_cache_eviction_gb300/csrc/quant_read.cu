@@ -6,7 +6,7 @@
 namespace kv {
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 128;
 constexpr int kPieces = 4;   // 16-byte pieces of K's rows (and of V's) of a lane at a time
 
 struct QReadArgs {
@@ -17,7 +17,7 @@ struct QReadArgs {
   uint4 *k, *v;
   WsHeader* hdr;
   int64_t rows, dst_vec, page_stride, num_slots;   // dst_vec: 16-byte pieces from row to row
-  int per_row, pad_shift;    // pieces of a row, and log2 of its padded pieces (7: whole groups)
+  int per_row, pad_shift;    // pieces of a row, and log2 of its padded pieces (a group's, at most)
   int Hp, d, shift;
   int dvec, div_dvec;        // pieces of a head's row; x / dvec = x * div_dvec >> 20
 };
@@ -61,7 +61,7 @@ struct Code<float> {
 };
 
 template <typename T, typename F>
-__global__ void __launch_bounds__(kThreads, 4)
+__global__ void __launch_bounds__(kThreads, 8)
 quant_read_kernel(const __grid_constant__ QReadArgs a) {
   constexpr int kN = 16 / (int)sizeof(T);   // codes of a piece
   const int lane = threadIdx.x & 31, page = 1 << a.shift;
@@ -69,36 +69,42 @@ quant_read_kernel(const __grid_constant__ QReadArgs a) {
   ptx::griddep_wait();   // nothing of the call before is read or written until it ends
   int64_t rows = a.rows;
   if (a.n_rows != nullptr) rows = min(rows, *a.n_rows);
-  const int in_group = 128 >> a.pad_shift;   // rows
+  constexpr int kGroup = 32 * kPieces;            // pieces at a time
+  const int in_group = kGroup >> a.pad_shift;     // rows, at most 32
   const int64_t warp = (int64_t)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
   const int64_t step = (int64_t)gridDim.x * (kThreads / 32) * in_group;
+  // lane i: the slot of the group's row i, -1 outside the rows
+  auto load_slot = [&](int64_t row0) {
+    return lane < in_group && row0 + lane < rows ? a.slots[row0 + lane] : (int64_t)-1;
+  };
+  int64_t next = load_slot(warp * in_group);
   for (int64_t row0 = warp * in_group; row0 < rows; row0 += step) {
-    for (int x0 = 0; x0 < a.per_row; x0 += 128) {
+    int64_t slot = next;
+    next = load_slot(row0 + step);   // (its latency beside this group's)
+    if (slot < 0 || slot >= a.num_slots) {
+      if (slot != -1) raise_dev(a.hdr, DEV_PAGE_ID, (unsigned)(row0 + lane));
+      slot = -1;
+    }
+    for (int x0 = 0; x0 < a.per_row; x0 += kGroup) {
       Code<T> kc[kPieces], vc[kPieces];
       float ks[kPieces], vs[kPieces];
       bool in[kPieces];
 #pragma unroll
       for (int j = 0; j < kPieces; ++j) {
         const int i = lane + 32 * j;
-        const int64_t row = row0 + (i >> a.pad_shift);
         const int x = x0 + (i & ((1 << a.pad_shift) - 1));
-        in[j] = false;
-        if (x < a.per_row && row < rows) {
-          const int64_t slot = a.slots[row];
-          in[j] = slot >= 0 && slot < a.num_slots;
-          if (in[j]) {
-            const int64_t pg = slot >> a.shift;
-            const int r = (int)(slot & (page - 1)), h = x * a.div_dvec >> 20;
-            const int64_t at =
-                pg * a.page_stride + ((int64_t)h * page + r) * a.d + (x - h * a.dvec) * kN;
-            const int64_t sc = (pg * a.Hp + h) * (page / quant::kBlock) + r / quant::kBlock;
-            kc[j].load(a.kp + at);
-            vc[j].load(a.vp + at);
-            ks[j] = a.ks[sc];
-            vs[j] = a.vs[sc];
-          } else if (slot != -1) {
-            raise_dev(a.hdr, DEV_PAGE_ID, (unsigned)row);
-          }
+        const int64_t s = __shfl_sync(0xffffffffu, (long long)slot, i >> a.pad_shift);
+        in[j] = x < a.per_row && s >= 0;
+        if (in[j]) {
+          const int64_t pg = s >> a.shift;
+          const int r = (int)(s & (page - 1)), h = x * a.div_dvec >> 20;
+          const int64_t at =
+              pg * a.page_stride + ((int64_t)h * page + r) * a.d + (x - h * a.dvec) * kN;
+          const int64_t sc = (pg * a.Hp + h) * (page / quant::kBlock) + r / quant::kBlock;
+          kc[j].load(a.kp + at);
+          vc[j].load(a.vp + at);
+          ks[j] = a.ks[sc];
+          vs[j] = a.vs[sc];
         }
       }
 #pragma unroll
@@ -116,8 +122,10 @@ quant_read_kernel(const __grid_constant__ QReadArgs a) {
 
 template <typename T, typename F>
 cudaError_t launch(const QReadArgs& a, cudaStream_t st) {
-  int64_t grid = cdiv(a.rows, (int64_t)(128 >> a.pad_shift) * (kThreads / 32));
-  const int64_t most = (int64_t)num_sms() * 8;
+  int64_t grid = cdiv(a.rows, (int64_t)(32 * kPieces >> a.pad_shift) * (kThreads / 32));
+  // (many small CTAs even out what the SMs get through: 131072 rows 121.6 us; 122.9 with 32 of twice the
+  // threads, 130.6 with 8, 126.2 without a limit)
+  const int64_t most = (int64_t)num_sms() * 64;
   if (grid > most) grid = most;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3((unsigned)grid);
@@ -139,8 +147,8 @@ cudaError_t launch_quant_read(const PagedShape& s, int format, const void* kp, c
   int shift = 0;
   while ((1 << shift) < s.page) ++shift;
   const int dvec = s.d * s.esize() / 16, per_row = s.Hp() * dvec;
-  int pad = 0;
-  while (pad < 7 && (1 << pad) < per_row) ++pad;
+  int pad = 0;   // a group has at most 32 rows
+  while ((32 * kPieces >> pad) > 32 || ((32 * kPieces >> pad) > 1 && (1 << pad) < per_row)) ++pad;
   // x / dvec by a product: x < 256 * 32, and the product is too large by less than dvec / 2^20 a
   // unit, so the quotient is exact (8192 * 32 < 2^20)
   const int div = ((1 << 20) + dvec - 1) / dvec;

@@ -9,14 +9,23 @@
 // to its nearest quarter turn before it becomes a float, which then has it to 2^-27 of a turn.
 //
 // A warp takes a row: a lane's pairs are the same ones in every head, so their sines and cosines are
-// worked out once a row, and heads follow each other.  Rows of small calls are split by heads.
+// worked out once a row, shared by the lanes of the heads that it turns at a time.  Rows of small calls
+// are split by heads.  On GB300: 131072 rows of 32 + 8 heads of 128 bf16 (2.7 GB read and written)
+// 412 us, 6.5 TB/s or 0.96 of the measured copy rate; 20011 fp32 rows of 8 heads of 80, 24 columns of them
+// turned, 21.5 us (24.4 with the other columns copied one after the other); 64 rows 2.6 us (3.7 with
+// every lane working out all of its pairs' sines).
 #include "kv_internal.cuh"
 #include "tc_ptx.cuh"
 
 namespace kv {
 namespace {
 
-constexpr int kThreads = 256;
+// Small CTAs, and more of them than are resident, even out what the SMs get through.  131072 rows / 20011
+// fp32 rows, us: 128 CTAs of two warps 412 / 21.5, 64 of four 413 / 23.0, 16 of four 447 / 22.8, 8 of
+// eight 442 / 21.4.  (Heads loaded ahead of the one that is turned: 447 / 24.0.  One head at a time instead
+// of four unrolled: 462 / 22.4.)
+constexpr int kThreads = 64;
+constexpr int kGrid = 128;      // CTAs of an SM, at most
 constexpr uint64_t kInvTwoPi = 0x28be60db9391054aull;   // 2^64 / 2 pi
 
 struct RotaryArgs {
@@ -98,8 +107,9 @@ __device__ __forceinline__ void sincos_turns(uint32_t t, float& s, float& c) {
   if ((quarter + 1) & 2) c = -c;
 }
 
-// V: pairs of a lane.
-template <typename T, int V, bool kHalf>
+// V: pairs of a lane.  kOwn: those whose sines it works out; the lanes that have the same pairs of
+// other heads give it the rest.
+template <typename T, int V, bool kHalf, int kOwn>
 __global__ void __launch_bounds__(kThreads) rotary_kernel(const __grid_constant__ RotaryArgs a) {
   const int lane = threadIdx.x & 31;
   ptx::griddep_launch_dependents();
@@ -110,80 +120,94 @@ __global__ void __launch_bounds__(kThreads) rotary_kernel(const __grid_constant_
   const int sub = lane >> a.lph_shift, heads_at_once = 32 >> a.lph_shift;
   const int heads = a.hq + a.hkv, i0 = chunk * V;   // the lane's pairs
   const bool turns_any = i0 < half;
-  uint64_t f[V];
+  uint64_t f[kOwn];
 #pragma unroll
-  for (int i = 0; i < V; ++i) f[i] = turns_any ? fraction(a.freq[i0 + i]) : 0ull;
+  for (int i = 0; i < kOwn; ++i)
+    f[i] = turns_any ? fraction(a.freq[i0 + (sub & (V / kOwn - 1)) * kOwn + i]) : 0ull;
   // columns of the two loads
   const int c0 = kHalf ? i0 : 2 * i0, c1 = kHalf ? i0 + half : 2 * i0 + V;
   const int64_t items = rows * a.parts;
   const int64_t step = (int64_t)gridDim.x * (kThreads / 32);
-  for (int64_t it = (int64_t)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5); it < items;
-       it += step) {
-    const int64_t row = a.parts == 1 ? it : it / a.parts;
+  int64_t it = (int64_t)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
+  auto row_of = [&](int64_t x) { return a.parts == 1 ? x : x / a.parts; };
+  int32_t next = it < items ? a.pos[row_of(it)] : -1;   // (under way beside a row's work)
+  for (; it < items; it += step) {
+    const int64_t row = row_of(it);
     const int part = (int)(it - row * a.parts);
-    const int32_t pos = a.pos[row];
+    const int32_t pos = next;
+    next = it + step < items ? a.pos[row_of(it + step)] : -1;
     if (pos < 0) continue;
-    float s[V], c[V];
-#pragma unroll
-    for (int i = 0; i < V; ++i) {
-      sincos_turns(turns((uint32_t)pos, f[i]), s[i], c[i]);
-      s[i] *= a.back ? -a.magnitude : a.magnitude;
-      c[i] *= a.magnitude;
-    }
     const T* q = (const T*)a.q + row * a.q_stride;
     const T* k = (const T*)a.k + row * a.k_stride;
     T* qo = (T*)a.q_out + row * a.qo_stride;
     T* ko = (T*)a.k_out + row * a.ko_stride;
-#pragma unroll 4
-    for (int h = part * heads_at_once + sub; h < heads; h += a.parts * heads_at_once) {
-      const T* src = h < a.hq ? q + h * a.d : k + (h - a.hq) * a.d;
-      T* dst = h < a.hq ? qo + h * a.d : ko + (h - a.hq) * a.d;
-      if (turns_any) {
-        Vec<T, V> x, y, u, w;
-        x.load(src + c0);
-        y.load(src + c1);
+    auto from = [&](int h) { return h < a.hq ? q + h * a.d : k + (h - a.hq) * a.d; };
+    auto to = [&](int h) { return h < a.hq ? qo + h * a.d : ko + (h - a.hq) * a.d; };
+    int h = part * heads_at_once + sub;
+    float s[V], c[V];
+    {
+      float so[kOwn], co[kOwn];
 #pragma unroll
-        for (int i = 0; i < V; i += 2) {
-          if (kHalf) {
-            const float a0 = x.get(i), b0 = y.get(i), a1 = x.get(i + 1), b1 = y.get(i + 1);
-            u.set2(i, a0 * c[i] - b0 * s[i], a1 * c[i + 1] - b1 * s[i + 1]);
-            w.set2(i, a0 * s[i] + b0 * c[i], a1 * s[i + 1] + b1 * c[i + 1]);
-          } else {
-            // pair i / 2 of the first load, and of the second
-            const int j = i / 2, m = V / 2 + j;
-            const float a0 = x.get(i), b0 = x.get(i + 1), a1 = y.get(i), b1 = y.get(i + 1);
-            u.set2(i, a0 * c[j] - b0 * s[j], a0 * s[j] + b0 * c[j]);
-            w.set2(i, a1 * c[m] - b1 * s[m], a1 * s[m] + b1 * c[m]);
-          }
+      for (int i = 0; i < kOwn; ++i) {
+        sincos_turns(turns((uint32_t)pos, f[i]), so[i], co[i]);
+        so[i] *= a.back ? -a.magnitude : a.magnitude;
+        co[i] *= a.magnitude;
+      }
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        const int src = (i / kOwn << a.lph_shift) + chunk;
+        s[i] = kOwn == V ? so[i % kOwn] : __shfl_sync(0xffffffffu, so[i % kOwn], src);
+        c[i] = kOwn == V ? co[i % kOwn] : __shfl_sync(0xffffffffu, co[i % kOwn], src);
+      }
+    }
+#pragma unroll 4
+    for (; h < heads; h += a.parts * heads_at_once) {
+      if (!turns_any) continue;
+      Vec<T, V> x, y, u, w;
+      x.load(from(h) + c0);
+      y.load(from(h) + c1);
+#pragma unroll
+      for (int i = 0; i < V; i += 2) {
+        if (kHalf) {
+          const float a0 = x.get(i), b0 = y.get(i), a1 = x.get(i + 1), b1 = y.get(i + 1);
+          u.set2(i, a0 * c[i] - b0 * s[i], a1 * c[i + 1] - b1 * s[i + 1]);
+          w.set2(i, a0 * s[i] + b0 * c[i], a1 * s[i + 1] + b1 * c[i + 1]);
+        } else {
+          const int j = i / 2, m = V / 2 + j;
+          const float a0 = x.get(i), b0 = x.get(i + 1), a1 = y.get(i), b1 = y.get(i + 1);
+          u.set2(i, a0 * c[j] - b0 * s[j], a0 * s[j] + b0 * c[j]);
+          w.set2(i, a1 * c[m] - b1 * s[m], a1 * s[m] + b1 * c[m]);
         }
-        u.store(dst + c0);
-        w.store(dst + c1);
       }
-      if (h < a.hq ? a.q_copy : a.k_copy) {
-        constexpr int kE = 16 / (int)sizeof(T);
-        for (int x = a.rot + chunk * kE; x < a.d; x += kE << a.lph_shift)
-          *reinterpret_cast<uint4*>(dst + x) = *reinterpret_cast<const uint4*>(src + x);
+      u.store(to(h) + c0);
+      w.store(to(h) + c1);
+    }
+    // the columns that stay: four pieces of 16 bytes of a lane at a time
+    constexpr int kE = 16 / (int)sizeof(T);
+    const int first = a.q_copy ? 0 : a.hq, last = a.k_copy ? heads : a.hq;   // heads with such
+    if (first >= last) continue;
+    const int per = (a.d - a.rot) / kE, all = (last - first) * per;
+    for (int p0 = part * 128 + lane; p0 < all; p0 += a.parts * 128) {
+      uint4 z[4];
+      int at[4], head[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int p = p0 + 32 * j, n = p / per;
+        head[j] = p < all ? first + n : -1;
+        at[j] = a.rot + (p - n * per) * kE;
+        if (p < all) z[j] = *reinterpret_cast<const uint4*>(from(head[j]) + at[j]);
       }
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        if (head[j] >= 0) *reinterpret_cast<uint4*>(to(head[j]) + at[j]) = z[j];
     }
   }
 }
 
-template <typename T, int V, bool kHalf>
-cudaError_t launch(RotaryArgs& a, cudaStream_t st) {
-  const int chunks = (a.rot / 2 + V - 1) / V;
-  a.lph_shift = 0;
-  while ((1 << a.lph_shift) < chunks) ++a.lph_shift;
-  const int at_once = 32 >> a.lph_shift;
-  const int passes = (a.hq + a.hkv + at_once - 1) / at_once;
-  // parts of a row: until there is a warp for every scheduler's eight
-  const int64_t want = (int64_t)num_sms() * 32;
-  a.parts = 1;
-  if (a.rows < want) {
-    const int64_t p = want / a.rows;
-    a.parts = (int)(p < passes ? p : passes);
-  }
+template <typename T, int V, bool kHalf, int kOwn>
+cudaError_t launch_own(const RotaryArgs& a, cudaStream_t st) {
   int64_t grid = cdiv(a.rows * a.parts, kThreads / 32);
-  const int64_t most = (int64_t)num_sms() * 8;
+  const int64_t most = (int64_t)num_sms() * kGrid;
   if (grid > most) grid = most;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3((unsigned)grid);
@@ -192,9 +216,28 @@ cudaError_t launch(RotaryArgs& a, cudaStream_t st) {
   cudaLaunchAttribute attr[1] = {pdl_attribute()};
   cfg.attrs = attr;
   cfg.numAttrs = grid == most ? 1 : 0;
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, rotary_kernel<T, V, kHalf>, a);
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, rotary_kernel<T, V, kHalf, kOwn>, a);
   if (e == cudaSuccess) count_launches(1);
   return e;
+}
+template <typename T, int V, bool kHalf>
+cudaError_t launch(RotaryArgs& a, cudaStream_t st) {
+  const int chunks = (a.rot / 2 + V - 1) / V;
+  a.lph_shift = 0;
+  while ((1 << a.lph_shift) < chunks) ++a.lph_shift;
+  const int at_once = 32 >> a.lph_shift;
+  const int passes = (a.hq + a.hkv + at_once - 1) / at_once;
+  // parts of a row: until every SM has 32 warps
+  const int64_t want = (int64_t)num_sms() * 32;
+  a.parts = 1;
+  if (a.rows < want) {
+    const int64_t p = want / a.rows;
+    a.parts = (int)(p < passes ? p : passes);
+  }
+  // the sines of V pairs shared by the lanes of `at_once` heads
+  if (V <= at_once) return launch_own<T, V, kHalf, 1>(a, st);
+  if (V == 2 * at_once) return launch_own<T, V, kHalf, 2>(a, st);
+  return launch_own<T, V, kHalf, 4>(a, st);
 }
 }  // namespace
 
