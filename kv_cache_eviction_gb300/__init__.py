@@ -10,6 +10,7 @@ is not on a CUDA device, the call raises.
 from __future__ import annotations
 
 import ctypes
+import importlib
 import os
 from typing import Optional
 
@@ -340,6 +341,26 @@ _ROWS = {}
 _CODES = {}   # types that the codes of a format may come as
 
 
+# csrc/binding.cpp as a module, once torch is there: it checks a call's tensors and calls the C
+# function, or returns None for the code below to do it.  None: not built, calls go through ctypes.
+_quick = None
+_FAST_CALLS = ("kv_quant_write", "kv_quant_read", "quant_decode_attn", "kv_rotary")
+
+
+def _init_fast() -> None:
+    global _quick
+    if not os.path.exists(os.path.join(_HERE, "_fast.so")):
+        return
+    try:
+        fast = importlib.import_module("._fast", __package__)
+    except ImportError as e:       # (built for another torch or Python)
+        import warnings
+        warnings.warn("kv_cache_eviction_gb300: _fast.so does not load (%s): build again" % e)
+        return
+    fast.bind(*(ctypes.cast(getattr(lib(), f), _vp).value for f in _FAST_CALLS))
+    _quick = fast
+
+
 def _init_torch() -> None:
     global _I32, _I64, _F32, _F64, _device_now, _stream_now
     import torch
@@ -349,6 +370,7 @@ def _init_torch() -> None:
     _stream_now = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
         lambda dev: torch.cuda.current_stream(dev).cuda_stream)
     torch.cuda.init()   # (current_device() would ask for it on every call)
+    _init_fast()
     _device_now = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 
 
@@ -517,6 +539,13 @@ def kv_quant_write(shape: KvPagedShape, format: int, k, v, slot_map, n_rows, k_p
     """``kv_paged_write`` into a cache in 8 bits: ``k_pages`` / ``v_pages`` hold codes (float8 e4m3
     or uint8 for KV_E4M3, int8 for KV_INT8), ``k_scale`` / ``v_scale`` [num_pages][heads per
     page][page / 16] float32 the scales of their blocks of 16 rows."""
+    if _quick is not None:
+        st = _quick.kv_quant_write(shape, format, k, v, slot_map, n_rows, k_pages, v_pages,
+                                   k_scale, v_scale, ws, stream)
+        if st == 0:
+            return
+        if st is not None:
+            raise KvError("kv_quant_write", st)
     dev = _device(k, "k")
     heads, pages = shape.hkv // shape.tables, shape.num_pages
     el, row, inner = _ROWS.get(shape.dtype), heads * shape.d, heads * shape.d * shape.page
@@ -541,6 +570,13 @@ def kv_quant_read(shape: KvPagedShape, format: int, k_pages, v_pages, k_scale, v
                   n_rows, k, v, ws, stream=None) -> None:
     """Rows of a cache in 8 bits as values, into rows ``k`` and ``v`` ([n][heads per page][d], rows
     may lie apart).  ``n_rows`` (a device int64, or None): rows from there on are left out."""
+    if _quick is not None:
+        st = _quick.kv_quant_read(shape, format, k_pages, v_pages, k_scale, v_scale, slot_map,
+                                  n_rows, k, v, ws, stream)
+        if st == 0:
+            return
+        if st is not None:
+            raise KvError("kv_quant_read", st)
     dev = _device(k, "k")
     heads, pages = shape.hkv // shape.tables, shape.num_pages
     el, row, inner = _ROWS.get(shape.dtype), heads * shape.d, heads * shape.d * shape.page
@@ -565,6 +601,14 @@ def quant_decode_attn(shape: KvPagedShape, format: int, q, k_new, v_new, cu_add,
                       v_pages, k_scale, v_scale, block_table, lens, softmax_scale: float, out, ws,
                       stream=None) -> None:
     """``paged_decode_attn`` over a cache in 8 bits (``kv_quant_write`` has the pools)."""
+    if _quick is not None:
+        st = _quick.quant_decode_attn(shape, format, q, k_new, v_new, cu_add, slot_map, k_pages,
+                                      v_pages, k_scale, v_scale, block_table, lens, softmax_scale,
+                                      out, ws, stream)
+        if st == 0:
+            return
+        if st is not None:
+            raise KvError("quant_decode_attn", st)
     dev = _device(q, "q")
     el, seqs, hkv, d, tables = _ROWS.get(shape.dtype), shape.seqs, shape.hkv, shape.d, shape.tables
     n, nq, nk, pages = seqs * tables, seqs * shape.hq * d, seqs * hkv * d, shape.num_pages
@@ -594,6 +638,12 @@ def kv_rotary(shape: KvRotaryShape, q, k, positions, inv_freq, q_out, k_out, n_r
     alone), ``inv_freq`` [rot / 2] float64 on the device (``kv_rotary_inv_freq``).  ``back``:
     turned back, which is the gradient.  ``n_rows`` (a device int64, or None): rows from there on
     are left out."""
+    if _quick is not None:
+        st = _quick.kv_rotary(shape, q, k, positions, inv_freq, q_out, k_out, n_rows, back, stream)
+        if st == 0:
+            return
+        if st is not None:
+            raise KvError("kv_rotary", st)
     dev = _device(positions, "positions")
     el, n, sides = _ROWS.get(shape.dtype), None, []
     for heads, pair in ((shape.hq, ((q, "q"), (q_out, "q_out"))),

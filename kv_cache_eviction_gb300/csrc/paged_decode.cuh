@@ -892,7 +892,7 @@ paged_decode_kernel(const __grid_constant__ PagedArgs a) {
     // get here, so its instructions are not at hand: 16 unrolled loads, as below, took 4 us.)
     const int part4s = (kPartHead + G * D) / 4;   // 16-byte pieces of a part
     const int room = kPWarps * S * C::kStage / 16 / part4s;
-    constexpr int kSlices = 8 * (D / 4) > kPThreads ? 8 * (D / 4) / kPThreads : 1;   // of a thread
+    constexpr int kSlices = (8 * (D / 4) + kPThreads - 1) / kPThreads;   // of a thread, at most
     const uint32_t to = ptx::smem_u32(sm.ring);
     const float* in = reinterpret_cast<const float*>(sm.ring);
 #pragma unroll 1

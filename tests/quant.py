@@ -1,4 +1,4 @@
-"""Test helpers of the cache in 8 bits: its codes and block scales by their definition, in 64 bits."""
+"""Test helpers of the cache in 8 bits: codes and block scales by their definition, in 64 bits."""
 from __future__ import annotations
 
 import numpy as np
@@ -101,7 +101,8 @@ class Pool:
         self.fmt, self.page_stride = fmt, (heads * page * d + extra if extra else 0)
         apart, inner = heads * page * d + extra, heads * page * d
         self.size, self.strides = (num, heads, page, d), (apart, page * d, d, 1)
-        self.flat, self.host, self.num, self.scale, self.dev, self.scale_dev = {}, {}, {}, {}, {}, {}
+        self.flat, self.host, self.num = {}, {}, {}
+        self.scale, self.dev, self.scale_dev = {}, {}, {}
         for name in ("k", "v"):
             flat = random_codes((num * apart + 64,), fmt, g)
             self.host[name] = flat
@@ -203,7 +204,8 @@ class QuantCache:
         self.pool, self.scale_dev = {}, {}
         for name in ("k", "v"):
             t = torch.tensor(self.num[name])
-            c = t.to(torch.int8) if fmt == "int8" else t.float().to(torch.float8_e4m3fn).view(torch.uint8)
+            c = t.to(torch.int8) if fmt == "int8" else t.float().to(torch.float8_e4m3fn).view(
+                torch.uint8)
             flat = torch.full((self.num_pages * self.apart,), 77, dtype=c.dtype)
             flat.as_strided(c.shape, (self.apart, page * d, d, 1)).copy_(c)
             dev = flat.cuda()
@@ -258,8 +260,8 @@ class QuantCache:
             assert same.all(), (name, int((~same).sum()), np.argwhere(~same)[:4])
             assert np.array_equal(self.scale_dev[name].cpu().double().numpy(), self.scale[name],
                                   equal_nan=True), name
-            gap = flat.view(torch.uint8).view(self.num_pages, self.apart)[:, self.hp * self.page * self.d:]
-            assert bool((gap == 77).all())
+            gap = flat.view(torch.uint8).view(self.num_pages, self.apart)
+            assert bool((gap[:, self.hp * self.page * self.d:] == 77).all())
 
     def rows(self, u, name):
         """Table u's rows as the cache holds them, [heads of a page][rows][d] float64."""

@@ -19,6 +19,7 @@ def built():
     from kv_cache_eviction_gb300 import _build
     _build.build()
     kv.lib()
+    kv._init_torch()
 
 
 def i64(x):
@@ -48,8 +49,8 @@ def runs(rng, num, page, rows):
 
 def rows_of(seed, n, heads, d, dtype):
     g = torch.Generator().manual_seed(seed)
-    x = torch.randn(2, n, heads, d, generator=g) * torch.exp(2 * torch.randn(2, n, 1, 1, generator=g))
-    return x.to(DT[dtype])
+    size = lambda: torch.exp(2 * torch.randn(2, n, 1, 1, generator=g))
+    return (torch.randn(2, n, heads, d, generator=g) * size()).to(DT[dtype])
 
 
 def write(pool, shape, k, v, slots, n_rows=None, ws=None, stream=None):
@@ -117,7 +118,8 @@ def special_rows(dtype):
             # halves between neighbouring codes of both formats, odd and even
             np.concatenate([np.arange(31) + 0.5, [127.0], (np.arange(32) + 8.5) / 16])]
     rows += [np.concatenate([[m], np.full(d - 1, 0.5)]) for m in
-             (447, 448, 448.5, 449, 450, 127, 127.25, 127.5, 128, 1.75, 1.7578125, 1.984375, 1.9921875)]
+             (447, 448, 448.5, 449, 450, 127, 127.25, 127.5, 128, 1.75, 1.7578125, 1.984375,
+              1.9921875)]
     return torch.tensor(np.array(rows)).to(DT[dtype])
 
 
@@ -319,3 +321,87 @@ def test_compacted_rows_of_head_tables():
         assert kv.kv_check_device_status(wm) == 0
         pool.put(*x.double().numpy(), slots.cpu().numpy())
         pool.check()
+
+
+def each_call(fmt="int8", dtype="bf16"):
+    """The four calls on small tensors: name, function and arguments."""
+    pool = Pool(6, 2, 16, 32, fmt, 30)
+    s = shape_of(pool, dtype)
+    s.seqs, s.max_pages = 3, 2
+    x = rows_of(31, 9, 2, 32, dtype).cuda()
+    ws = workspace(kv.KV_OP_QUANT_DECODE, s)
+    table = torch.tensor([[0, 1], [2, 3], [4, 5]], dtype=torch.int32, device="cuda")
+    lens = torch.tensor([20, 1, 32], dtype=torch.int32, device="cuda")
+    cu, slots = i64([0, 1, 2, 3]), i64([19, 32, 95])
+    rot = kv.KvRotaryShape.of(2, 2, 32, 16, kv.KV_ROTARY_HALF, dtype)
+    freq = kv.kv_rotary_inv_freq(16)[0].cuda()
+    f = FORMATS[fmt]
+    out = lambda n: torch.zeros(n, 2, 32, dtype=DT[dtype], device="cuda")
+    return [("kv_quant_write", kv.kv_quant_write,
+             [s, f, x[0], x[1], i64(np.arange(9) + 20), None, *pool.args(), ws]),
+            ("kv_quant_read", kv.kv_quant_read,
+             [s, f, *pool.args(), i64(np.arange(9)), i64([8]), out(9), out(9), ws]),
+            ("quant_decode_attn", kv.quant_decode_attn,
+             [s, f, x[0, :3].clone(), x[0, 3:6].clone(), x[1, :3].clone(), cu, slots, *pool.args(),
+              table, lens, 0.3, out(3), ws]),
+            ("kv_rotary", kv.kv_rotary,
+             [rot, x[0], x[1], torch.arange(9, dtype=torch.int32, device="cuda"), freq, out(9),
+              out(9)])]
+
+
+@pytest.mark.parametrize("fmt", ["e4m3", "int8"])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_both_ways_of_the_binding(monkeypatch, fmt, dtype):
+    """The binding's common case in C++ and its Python code do the same."""
+    if kv._quick is None:
+        pytest.skip("_fast.so is not built")
+    got = []
+    for quick in (kv._quick, None):
+        monkeypatch.setattr(kv, "_quick", quick)
+        side = torch.cuda.Stream()
+        for stream in (None, side, side.cuda_stream):
+            side.wait_stream(torch.cuda.current_stream())
+            calls = each_call(fmt, dtype)
+            torch.cuda.synchronize()
+            for name, call, args in calls:
+                call(*args, stream=stream)
+            torch.cuda.synchronize()
+            got.append([t.view(torch.uint8).cpu() for _, _, args in calls for t in args
+                        if isinstance(t, torch.Tensor)])
+    for other in got[1:]:
+        assert len(other) == len(got[0])
+        assert all(torch.equal(a, b) for a, b in zip(got[0], other))
+
+
+def test_binding_refuses_wrong_tensors(monkeypatch):
+    """Types, sizes, strides and host tensors: refused alike both ways, and nothing is run."""
+    quick = kv._quick
+    for way in (quick, None):
+        monkeypatch.setattr(kv, "_quick", way)
+        for name, call, args in each_call():
+            tensors = [i for i, t in enumerate(args) if isinstance(t, torch.Tensor)]
+            before = kv.kv_kernel_launches()
+            for i in tensors:
+                t = args[i]
+                wrong = [t.cpu(), t.to(torch.float16)]
+                if t.numel() > 1 and not (name == "quant_decode_attn" and i == 6):
+                    wrong.append(t[:-1])      # (a shorter slot_map is a legal one there)
+                if t.numel() > 1 and t.dim() == 1 and not (name == "quant_decode_attn" and i == 6):
+                    wrong.append(torch.cat([t, t])[::2])
+                for w in wrong:
+                    if i == len(args) - 1 and name != "kv_rotary" and w.is_cuda:
+                        continue              # (ws may be of any type; its size is C's to check)
+                    with pytest.raises((ValueError, kv.KvError)):
+                        call(*args[:i], w, *args[i + 1:])
+            assert kv.kv_kernel_launches() == before
+            # what the C function refuses: a workspace too small, no frequencies; and a format
+            # that there is none of
+            bad = list(args)
+            bad[-1 if name != "kv_rotary" else 4] = args[-1][:100] if name != "kv_rotary" else None
+            with pytest.raises(kv.KvError):
+                call(*bad)
+            if name != "kv_rotary":
+                with pytest.raises((ValueError, kv.KvError)):
+                    call(args[0], 7, *args[2:])
+            assert kv.kv_kernel_launches() == before
+    torch.cuda.synchronize()

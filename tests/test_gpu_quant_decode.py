@@ -35,8 +35,8 @@ def finish(c, out, ws):
 
 @pytest.mark.parametrize("kind", list(LENS))
 @pytest.mark.parametrize("fmt,dtype,d,G,page,tables", [
-    ("e4m3", "bf16", 128, 4, 16, 1), ("int8", "bf16", 128, 8, 64, 1), ("e4m3", "bf16", 64, 1, 16, 1),
-    ("int8", "f32", 128, 2, 16, 1), ("e4m3", "bf16", 128, 4, 32, 4), ("e4m3", "f32", 80, 3, 16, 4),
+    ("e4m3", "bf16", 128, 4, 16, 1), ("int8", "bf16", 128, 8, 64, 1),
+    ("e4m3", "bf16", 64, 1, 16, 1), ("int8", "f32", 128, 2, 16, 1), ("e4m3", "bf16", 128, 4, 32, 4), ("e4m3", "f32", 80, 3, 16, 4),
     ("int8", "bf16", 80, 5, 256, 1), ("e4m3", "bf16", 16, 7, 16, 1), ("e4m3", "f32", 64, 8, 128, 1),
     ("int8", "f32", 32, 6, 128, 4), ("int8", "bf16", 48, 3, 32, 4), ("e4m3", "f32", 112, 4, 64, 1)])
 def test_decode(kind, fmt, dtype, d, G, page, tables):
@@ -86,6 +86,18 @@ def test_many_tiles_a_warp(fmt, dtype, d, G, lens):
     finish(c, out, ws)
     for _ in range(5):
         assert torch.equal(out, c.run(ws=ws)[0])
+
+
+@pytest.mark.parametrize("G", [1, 3, 5, 6, 7, 8])
+@pytest.mark.parametrize("d", [16, 32, 48, 64, 80, 96, 112, 128])
+def test_every_width_over_many_ctas(d, G):
+    """Units whose parts go through the workspace, at every width and group size: few long units on
+    CTAs of eight warps, and more, with shorter tables, on CTAs of four."""
+    fmt, dtype = ("e4m3", "int8")[G % 2], ("bf16", "f32")[d // 16 % 2]
+    for hkv, lens in ((1, [40001]), (8, [3001, 17, 900, 0, 2500, 1200])):
+        c = QuantCache(len(lens), hkv, G, d, 1, 32, lens, dtype, fmt, d + G)
+        out, ws = c.run()
+        finish(c, out, ws)
 
 
 @pytest.mark.parametrize("extra", [16, 128, 4096])
@@ -209,7 +221,8 @@ def test_slots_elsewhere(fmt):
     for slot, code in ((-1, 0), (-2, ERR_ID), (10 ** 9, ERR_ID), (1 << 62, ERR_ID),
                        ("next", ERR_ID), ("block", ERR_ID)):
         c = QuantCache(3, 2, 4, 64, 1, 32, [50, 40, 37], "bf16", fmt, 9, new=[0, 0, 0], spare=2)
-        own = [int(c.table_host[u, (n - 1) // 32]) * 32 + (n - 1) % 32 for u, n in enumerate(c.lens)]
+        own = [int(c.table_host[u, (n - 1) // 32]) * 32 + (n - 1) % 32
+               for u, n in enumerate(c.lens)]
         if slot == "next":
             slot = own[1] + 1
         if slot == "block":
@@ -329,8 +342,8 @@ def test_serving_steps_captured():
     x = qkv.cuda()
     pos = dev(np.concatenate([np.arange(m) for m in n]), i32)
     kv.kv_rotary(rot, x[:, :hq], x[:, hq:hq + hkv], pos, fd, x[:, :hq], x[:, hq:hq + hkv])
-    kv.kv_quant_write(shape, kv.KV_E4M3, x[:, hq:hq + hkv], x[:, hq + hkv:], slots, cu[seqs:], kp, vp,
-                      ks, vs, ws)
+    kv.kv_quant_write(shape, kv.KV_E4M3, x[:, hq:hq + hkv], x[:, hq + hkv:], slots, cu[seqs:],
+                      kp, vp, ks, vs, ws)
     s = slots.cpu().numpy()
     for name, rows in (("k", x[:, hq:hq + hkv]), ("v", x[:, hq + hkv:])):
         put(*host[name], rows.double().cpu().numpy(), s, fmt)

@@ -182,7 +182,8 @@ def test_many_rows_and_captured():
     x = torch.randn(rows, h, d, generator=torch.Generator().manual_seed(1)).bfloat16()
     freq = kv.kv_rotary_inv_freq(d)[0]
     s = kv.KvRotaryShape.of(h, 0, d, d, kv.KV_ROTARY_HALF, "bf16")
-    xd, out, fd = x.cuda(), torch.zeros(rows, h, d, dtype=torch.bfloat16, device="cuda"), freq.cuda()
+    xd, fd = x.cuda(), freq.cuda()
+    out = torch.zeros_like(xd)
     pos = dev(np.zeros(rows), torch.int32)
     side = torch.cuda.Stream()
     side.wait_stream(torch.cuda.current_stream())

@@ -43,8 +43,8 @@ def call_read(L, s, fmt=0, k=P, v=P, stride=0, slots=P, rows=10, n_rows=None, kp
                            k, v, stride, ws, n, None)
 
 
-def call_decode(L, s, fmt=0, q=P, kn=P, vn=P, cu=P, slots=P, cap=10, kp=P, vp=P, ks=P, vs=P, table=P,
-                lens=P, scale=0.1, out=P, ws=P, n=BIG):
+def call_decode(L, s, fmt=0, q=P, kn=P, vn=P, cu=P, slots=P, cap=10, kp=P, vp=P, ks=P, vs=P,
+                table=P, lens=P, scale=0.1, out=P, ws=P, n=BIG):
     return L.quant_decode_attn(ctypes.byref(s) if s else None, fmt, q, kn, vn, cu, slots, cap, kp,
                                vp, ks, vs, table, lens, scale, out, ws, n, None)
 
@@ -139,8 +139,8 @@ def rotary_shape(**kw):
 A, B, C, D = (ctypes.c_void_p(x << 32) for x in (1, 2, 3, 4))
 
 
-def call_rotary(L, s, back=0, q=A, qs=0, k=B, ks=0, pos=P, freq=P, rows=10, n_rows=None, qo=C, qos=0,
-                ko=D, kos=0):
+def call_rotary(L, s, back=0, q=A, qs=0, k=B, ks=0, pos=P, freq=P, rows=10, n_rows=None, qo=C,
+                qos=0, ko=D, kos=0):
     return L.kv_rotary(ctypes.byref(s) if s else None, back, q, qs, k, ks, pos, freq, rows, n_rows,
                        qo, qos, ko, kos, None)
 
@@ -214,7 +214,8 @@ def test_the_definitions_own_pieces():
     t = c.view(torch.float8_e4m3fn).double().numpy()
     assert np.array_equal(E4M3, t, equal_nan=True)
     rng = np.random.default_rng(1)
-    x = np.concatenate([rng.normal(size=500) * np.exp(rng.uniform(-8, 6, 500)), np.arange(-40, 40) / 512])
+    x = np.concatenate([rng.normal(size=500) * np.exp(rng.uniform(-8, 6, 500)),
+                        np.arange(-40, 40) / 512])
     fine = np.unique(E4M3[~np.isnan(E4M3)])
     for all_, fmt in ((fine, "e4m3"), (np.arange(-127.0, 128), "int8")):
         y = nearest(x, fmt)
