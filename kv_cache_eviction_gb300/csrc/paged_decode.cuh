@@ -278,6 +278,11 @@ __device__ __forceinline__ void cp_async_wait() {   // all groups but the last N
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
+__device__ __forceinline__ uint32_t atomic_add_acq_rel(uint32_t* p, uint32_t x) {
+  uint32_t r;
+  asm volatile("atom.add.acq_rel.gpu.global.u32 %0, [%1], %2;" : "=r"(r) : "l"(p), "r"(x) : "memory");
+  return r;
+}
 // Merge of up to kB parts (max of q . k, sum, 4 outputs each; max -inf: none) into (M, L, acc).
 // (A part whose every score is a NaN has max -inf too, and a sum and outputs of NaN: with factors
 // of 0, not left out, they stay.)
@@ -471,6 +476,8 @@ paged_decode_kernel(const __grid_constant__ PagedArgs a) {
   };
   // the CTA that holds tile x of a unit that crosses CTAs
   auto cta_of = [&](uint32_t x) {
+    if (P::kCodes && total < 1u << 23)   // (a quarter of the instructions; Ne < 2^9)
+      return (int)(((x + 1) * Ne + total - 1) / total) - 1;
     return (int)((((uint64_t)x + 1) * Ne + total - 1) / total) - 1;
   };
   // the CTA's ends: with few tables every warp finds both, else two warps find one each
@@ -873,6 +880,103 @@ paged_decode_kernel(const __grid_constant__ PagedArgs a) {
     parts[y] = units[y] >= 0 ? cta_of(ends.y - 1) - first[y] + 1 : 0;
   }
   __syncthreads();   // the CTA's parts are written
+  if constexpr (P::kCodes) {
+    // (a thread for each: the release of the CTA's parts and the acquiring of the others' in one)
+    if (tid < 2) {
+      const int32_t un = tid == 0 ? units[0] : units[1];
+      const int at = tid == 0 ? first[0] : first[1], of = tid == 0 ? parts[0] : parts[1];
+      sm.won[tid] = un >= 0 && atomic_add_acq_rel(&a.tick[at], 1u) == (uint32_t)of - 1;
+      if (sm.won[tid]) a.tick[at] = 0u;
+    }
+    __syncthreads();
+    const int n0 = sm.won[0] ? parts[0] : 0, n1 = sm.won[1] ? parts[1] : 0;
+    if (n0 + n1 == 0) return;
+    // The parts come through the rings, which are free now: many at a time, of both units at once, with
+    // little code.  (Few CTAs get here, so its instructions are not at hand; one unit after the other,
+    // 8 ragged sequences of 2000 rows took 18.8 us.)
+    const int part4s = (kPartHead + G * D) / 4;   // 16-byte pieces of a part
+    int room = kPWarps * S * C::kStage / 16 / part4s;   // parts
+    if (n0 > 0 && n1 > 0) room /= 2;
+    constexpr int kSlices = (8 * (D / 4) + kPThreads - 1) / kPThreads;   // of a thread, at most
+    const uint32_t to = ptx::smem_u32(sm.ring);
+    const float* ring_f = reinterpret_cast<const float*>(sm.ring);
+    float M[2][kSlices], L[2][kSlices];
+    float4 acc[2][kSlices];
+#pragma unroll
+    for (int y = 0; y < 2; ++y)
+#pragma unroll
+      for (int j = 0; j < kSlices; ++j) {
+        M[y][j] = -INFINITY;
+        L[y][j] = 0.f;
+        acc[y][j] = make_float4(0.f, 0.f, 0.f, 0.f);
+      }
+#pragma unroll 1
+    for (int k0 = 0; k0 < max(n0, n1); k0 += room) {
+      // parts k0.. of the first unit at the ring's beginning, of the second behind them
+      const int c0 = max(min(room, n0 - k0), 0), c1 = max(min(room, n1 - k0), 0);
+#pragma unroll 1
+      for (int k = warp; k < c0 + c1; k += kPWarps) {
+        const int y = k >= c0, of = k0 + (y ? k - c0 : k);
+        // (the unit is the second of its first CTA)
+        const int slot = 2 * ((y ? first[1] : first[0]) + of) + (of == 0 ? 1 : 0);
+        const float* W = a.part + (int64_t)slot * kPartFloats + lane * 4;
+        const uint32_t dst = to + (k * part4s + lane) * 16;
+#pragma unroll 4
+        for (int i = 0; i < part4s - lane; i += 32) cp_async16(dst + i * 16, W + i * 4);
+      }
+      cp_async_commit();
+      cp_async_wait<0>();
+      __syncthreads();
+#pragma unroll
+      for (int y = 0; y < 2; ++y) {
+        const int n = y ? c1 : c0;
+        const float* in = ring_f + (y ? c0 * part4s * 4 : 0);
+        if (n == 0) continue;
+#pragma unroll
+        for (int j = 0; j < kSlices; ++j) {
+          const int idx = tid + j * kPThreads, g = idx / (D / 4);
+          if (idx >= nsl) continue;
+          float mn = M[y][j];
+#pragma unroll 4
+          for (int k = 0; k < n; ++k) mn = fmaxf(mn, in[k * part4s * 4 + g]);
+          const float base = mn == -INFINITY ? 0.f : mn;
+          const float f = ptx::ex2((M[y][j] - base) * a.scale.c2);   // 0 while M is -inf
+          float4 o = acc[y][j];
+          float l = L[y][j] * f;
+          o = make_float4(o.x * f, o.y * f, o.z * f, o.w * f);
+#pragma unroll 4
+          for (int k = 0; k < n; ++k) {
+            const float* W = in + k * part4s * 4;
+            const float w = ptx::ex2((W[g] - base) * a.scale.c2);
+            const float4 x = *reinterpret_cast<const float4*>(W + kPartHead + idx * 4);
+            l = fmaf(W[8 + g], w, l);
+            o.x = fmaf(x.x, w, o.x);
+            o.y = fmaf(x.y, w, o.y);
+            o.z = fmaf(x.z, w, o.z);
+            o.w = fmaf(x.w, w, o.w);
+          }
+          M[y][j] = mn;
+          L[y][j] = l;
+          acc[y][j] = o;
+        }
+      }
+      __syncthreads();
+    }
+#pragma unroll
+    for (int y = 0; y < 2; ++y) {
+      if ((y ? n1 : n0) == 0) continue;
+#pragma unroll
+      for (int j = 0; j < kSlices; ++j) {
+        const int idx = tid + j * kPThreads, g = idx / (D / 4), col = (idx - g * (D / 4)) * 4;
+        if (idx >= nsl || col >= d) continue;
+        const float inv = L[y][j] != 0.f ? 1.f / L[y][j] : 0.f;
+        store4((T*)a.out + ((int64_t)units[y] * G + g) * d + col,
+               make_float4(acc[y][j].x * inv, acc[y][j].y * inv, acc[y][j].z * inv,
+                           acc[y][j].w * inv));
+      }
+    }
+    return;
+  }
   if (tid == 0) {
     __threadfence();
     uint32_t drawn[2] = {0, 0};
@@ -887,76 +991,6 @@ paged_decode_kernel(const __grid_constant__ PagedArgs a) {
     __threadfence();
   }
   __syncthreads();
-  if constexpr (P::kCodes) {
-    // The parts come through the rings, which are free now: many at a time with little code.  (Few CTAs
-    // get here, so its instructions are not at hand: 16 unrolled loads, as below, took 4 us.)
-    const int part4s = (kPartHead + G * D) / 4;   // 16-byte pieces of a part
-    const int room = kPWarps * S * C::kStage / 16 / part4s;
-    constexpr int kSlices = (8 * (D / 4) + kPThreads - 1) / kPThreads;   // of a thread, at most
-    const uint32_t to = ptx::smem_u32(sm.ring);
-    const float* in = reinterpret_cast<const float*>(sm.ring);
-#pragma unroll 1
-    for (int y = 0; y < 2; ++y) {
-      if (!sm.won[y]) continue;
-      float M[kSlices], L[kSlices];
-      float4 acc[kSlices];
-#pragma unroll
-      for (int j = 0; j < kSlices; ++j) {
-        M[j] = -INFINITY;
-        L[j] = 0.f;
-        acc[j] = make_float4(0.f, 0.f, 0.f, 0.f);
-      }
-#pragma unroll 1
-      for (int k0 = 0; k0 < parts[y]; k0 += room) {
-        const int n = min(room, parts[y] - k0);
-        for (int k = warp; k < n; k += kPWarps) {
-          // (the unit is the second of its first CTA)
-          const int slot = 2 * (first[y] + k0 + k) + (k0 + k == 0 ? 1 : 0);
-          const float* W = a.part + (int64_t)slot * kPartFloats + lane * 4;
-          const uint32_t dst = to + (k * part4s + lane) * 16;
-#pragma unroll 4
-          for (int i = 0; i < part4s - lane; i += 32) cp_async16(dst + i * 16, W + i * 4);
-        }
-        cp_async_commit();
-        cp_async_wait<0>();
-        __syncthreads();
-#pragma unroll
-        for (int j = 0; j < kSlices; ++j) {
-          const int idx = tid + j * kPThreads, g = idx / (D / 4);
-          if (idx >= nsl) continue;
-          float mn = M[j];
-#pragma unroll 8
-          for (int k = 0; k < n; ++k) mn = fmaxf(mn, in[k * part4s * 4 + g]);
-          const float base = mn == -INFINITY ? 0.f : mn;
-          const float f = ptx::ex2((M[j] - base) * a.scale.c2);   // 0 while M is -inf
-          M[j] = mn;
-          L[j] *= f;
-          acc[j] = make_float4(acc[j].x * f, acc[j].y * f, acc[j].z * f, acc[j].w * f);
-#pragma unroll 4
-          for (int k = 0; k < n; ++k) {
-            const float* W = in + k * part4s * 4;
-            const float w = ptx::ex2((W[g] - base) * a.scale.c2);
-            const float4 o = *reinterpret_cast<const float4*>(W + kPartHead + idx * 4);
-            L[j] = fmaf(W[8 + g], w, L[j]);
-            acc[j].x = fmaf(o.x, w, acc[j].x);
-            acc[j].y = fmaf(o.y, w, acc[j].y);
-            acc[j].z = fmaf(o.z, w, acc[j].z);
-            acc[j].w = fmaf(o.w, w, acc[j].w);
-          }
-        }
-        __syncthreads();
-      }
-#pragma unroll
-      for (int j = 0; j < kSlices; ++j) {
-        const int idx = tid + j * kPThreads, g = idx / (D / 4), col = (idx - g * (D / 4)) * 4;
-        if (idx >= nsl || col >= d) continue;
-        const float inv = L[j] != 0.f ? 1.f / L[j] : 0.f;
-        store4((T*)a.out + ((int64_t)units[y] * G + g) * d + col,
-               make_float4(acc[j].x * inv, acc[j].y * inv, acc[j].z * inv, acc[j].w * inv));
-      }
-    }
-    return;
-  }
   // groups of threads take the parts in turn, and their sums are added in order
   const int groups = nsl < kPThreads ? kPThreads / nsl : 1;
 #pragma unroll 1
