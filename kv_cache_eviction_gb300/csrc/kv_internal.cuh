@@ -218,6 +218,7 @@ cudaError_t launch_quant_read(const PagedShape& s, int format, const void* kp, c
                               const int64_t* n_rows, void* k, void* v, int64_t dst_stride,
                               WsHeader* hdr, cudaStream_t st);
 
+size_t quant_decode_ws_bytes(const PagedShape& s);
 cudaError_t launch_quant_decode(const PagedShape& s, int format, const void* q, const void* kn,
                                 const void* vn, const int64_t* cu, const int64_t* slots,
                                 int64_t slot_capacity, void* kp, void* vp, float* ks, float* vs,

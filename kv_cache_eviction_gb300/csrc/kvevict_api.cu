@@ -511,7 +511,7 @@ size_t kv_paged_workspace_size(int op, const kv_paged_shape* shape) {
   PagedShape s;
   if (op >= KV_OP_QUANT_WRITE && op <= KV_OP_QUANT_DECODE) {
     if (quant_shape_check(shape, &s) != KV_OK) return 0;
-    return op == KV_OP_QUANT_DECODE ? paged_decode_ws_bytes(s) : kWsHeader;
+    return op == KV_OP_QUANT_DECODE ? quant_decode_ws_bytes(s) : kWsHeader;
   }
   if (paged_shape_check(shape, &s) != KV_OK) return 0;
   switch (op) {
@@ -590,7 +590,7 @@ static kv_status paged_decode_check(const PagedShape& s, const void* q, const vo
                                     const void* k_pages, const void* v_pages,
                                     const int32_t* block_table, const int32_t* lens,
                                     float softmax_scale, const void* out, const void* ws,
-                                    size_t ws_bytes, bool* work) {
+                                    size_t ws_bytes, size_t ws_needed, bool* work) {
   *work = false;
   if (ws == nullptr || !aligned16(ws)) return KV_ERR_INVALID_ARG;
   if ((k_new == nullptr) != (v_new == nullptr)) return KV_ERR_INVALID_ARG;
@@ -612,7 +612,7 @@ static kv_status paged_decode_check(const PagedShape& s, const void* q, const vo
   if (s.U() > KV_PAGED_DECODE_MAX_TABLES ||
       (int64_t)s.seqs * s.Hkv > (((int64_t)1 << 34) - 1) / ((int64_t)s.max_pages * s.page))
     return KV_ERR_UNSUPPORTED;
-  if (ws_bytes < paged_decode_ws_bytes(s)) return KV_ERR_WORKSPACE;
+  if (ws_bytes < ws_needed) return KV_ERR_WORKSPACE;
   *work = true;
   return KV_OK;
 }
@@ -627,7 +627,8 @@ kv_status paged_decode_attn(const kv_paged_shape* shape, const void* q, const vo
   kv_status st = paged_shape_check(shape, &s);
   if (st != KV_OK) return st;
   st = paged_decode_check(s, q, k_new, v_new, cu_add, slot_map, slot_capacity, k_pages, v_pages,
-                          block_table, lens, softmax_scale, out, ws, ws_bytes, &work);
+                          block_table, lens, softmax_scale, out, ws, ws_bytes,
+                          paged_decode_ws_bytes(s), &work);
   if (st != KV_OK || !work) return st;
   return cuda_status(launch_paged_decode(s, q, k_new, v_new, cu_add, slot_map, slot_capacity,
                                          k_pages, v_pages, block_table, lens, softmax_scale, out,
@@ -649,7 +650,8 @@ kv_status quant_decode_attn(const kv_paged_shape* shape, int format, const void*
   if (s.seqs > 0 && (k_scale == nullptr || v_scale == nullptr)) return KV_ERR_INVALID_ARG;
   if (!aligned_to(k_scale, 4) || !aligned_to(v_scale, 4)) return KV_ERR_INVALID_ARG;
   st = paged_decode_check(s, q, k_new, v_new, cu_add, slot_map, slot_capacity, k_pages, v_pages,
-                          block_table, lens, softmax_scale, out, ws, ws_bytes, &work);
+                          block_table, lens, softmax_scale, out, ws, ws_bytes,
+                          quant_decode_ws_bytes(s), &work);
   if (st != KV_OK || !work) return st;
   return cuda_status(launch_quant_decode(s, format, q, k_new, v_new, cu_add, slot_map,
                                          slot_capacity, k_pages, v_pages, k_scale, v_scale,

@@ -3,7 +3,7 @@
 
 namespace kv {
 
-size_t paged_decode_ws_bytes(const PagedShape&) { return ws_bytes(); }
+size_t paged_decode_ws_bytes(const PagedShape&) { return ws_bytes(kMaxCtas); }
 
 cudaError_t launch_paged_decode(const PagedShape& s, const void* q, const void* kn, const void* vn,
                                 const int64_t* cu, const int64_t* slots, int64_t slot_capacity,

@@ -65,6 +65,7 @@ constexpr int kSmWarps = 8;
 // rows and few are held: 8 units of 500 rows 8.4 / 8.5, of 2000 12.6 / 9.5, 40 units of 500 11.3 / 11.4.
 constexpr int kLongUnits = 38;
 constexpr int kMaxCtas = 320;
+constexpr int kMaxCtasOfCodes = 480;
 constexpr int kRingBytes = 20 * 1024;   // of a warp, at most (and four tiles)
 // Tiles per CTA at least: a small call runs on as few CTAs as that allows.  One tile a warp: one
 // sequence of 500 rows 8.2 us; with two 8.9, with four 11.2.
@@ -107,6 +108,7 @@ struct Rows {
   using Tl = pmma::Tile<T_, H_>;
   static constexpr int H = H_, kMaxStages = 4;
   static constexpr int kNewRow = H_ * 64;  // bytes of a new row beside a stage
+  static constexpr int kWarps = kSmWarps;  // of an SM, in CTAs of four
   static constexpr bool kCodes = false;
 };
 // Pools of codes of the format F, for q, new rows and outputs of T, in NP pieces of 16 columns.
@@ -116,7 +118,8 @@ struct Codes {
   using E = unsigned char;
   using F = F_;
   using Tl = qmma::Tile<T_, F_, NP>;
-  static constexpr int H = Tl::H, kMaxStages = 4;
+  static constexpr int kWarps = NP <= 4 ? 12 : kSmWarps;
+  static constexpr int H = Tl::H, kMaxStages = NP <= 4 ? 3 : 4;
   static constexpr int kNewRow = NP * 16 * (int)sizeof(T_);
   static constexpr bool kCodes = true;
 };
@@ -366,7 +369,7 @@ __device__ __forceinline__ float2 put_rows(unsigned char* stage, int above,
 
 // kPWarps: warps of a CTA.
 template <typename P, int kPWarps>
-__global__ void __launch_bounds__(kPWarps * 32, kSmWarps / kPWarps)
+__global__ void __launch_bounds__(kPWarps * 32, P::kWarps / kPWarps)
 paged_decode_kernel(const __grid_constant__ PagedArgs a) {
   constexpr int kPThreads = kPWarps * 32;
   using C = Cfg<P>;
@@ -1054,12 +1057,12 @@ paged_decode_kernel(const __grid_constant__ PagedArgs a) {
 // ------------------------------------- host side ----------------------------------------
 
 constexpr size_t kTickBytes = 2048;
-static_assert(kMaxCtas * sizeof(uint32_t) <= kTickBytes, "tickets");
+static_assert(kMaxCtasOfCodes * sizeof(uint32_t) <= kTickBytes, "tickets");
 
 template <typename P, int kPWarps>
 cudaError_t launch_w(const PagedShape& s, const PagedArgs& a, int64_t tiles, cudaStream_t st) {
   using C = Cfg<P>;
-  constexpr int per_sm = kSmWarps / kPWarps;
+  constexpr int per_sm = P::kWarps / kPWarps;
   constexpr size_t smem = sizeof(PagedSmem<C, kPWarps>) + 1024;
   static_assert(per_sm * (smem + 1024) <= 228 * 1024 && smem <= 227 * 1024, "CTAs per SM");
   static std::atomic<int> slot[kMaxDevices];
@@ -1072,7 +1075,8 @@ cudaError_t launch_w(const PagedShape& s, const PagedArgs& a, int64_t tiles, cud
   // no more CTAs than the tables could ever fill
   int64_t grid = cdiv(tiles, kMinTiles);
   if (grid > per_sm * num_sms()) grid = per_sm * num_sms();
-  if (grid > kMaxCtas) grid = kMaxCtas;
+  constexpr int64_t most = P::kCodes ? kMaxCtasOfCodes : kMaxCtas;
+  if (grid > most) grid = most;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3((unsigned)grid);
   cfg.blockDim = dim3(kPWarps * 32);
@@ -1098,8 +1102,8 @@ cudaError_t launch_t(const PagedShape& s, const PagedArgs& a, cudaStream_t st) {
   return few_long ? launch_w<P, 8>(s, a, tiles, st) : launch_w<P, 4>(s, a, tiles, st);
 }
 
-size_t ws_bytes() {
-  return kWsHeader + kTickBytes + (size_t)2 * kMaxCtas * kPartFloats * sizeof(float);
+size_t ws_bytes(int ctas) {
+  return kWsHeader + kTickBytes + (size_t)2 * ctas * kPartFloats * sizeof(float);
 }
 
 PagedArgs args(const PagedShape& s, const void* q, const void* kn, const void* vn,

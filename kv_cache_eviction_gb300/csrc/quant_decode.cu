@@ -11,6 +11,8 @@ cudaError_t by_width(const PagedShape& s, const PagedArgs& a, cudaStream_t st) {
 }
 }  // namespace
 
+size_t quant_decode_ws_bytes(const PagedShape&) { return ws_bytes(kMaxCtasOfCodes); }
+
 cudaError_t launch_quant_decode(const PagedShape& s, int format, const void* q, const void* kn,
                                 const void* vn, const int64_t* cu, const int64_t* slots,
                                 int64_t slot_capacity, void* kp, void* vp, float* ks, float* vs,
