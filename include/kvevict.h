@@ -668,7 +668,9 @@ typedef struct {
  * q, k      rows of [hq][d], [hkv][d] dtype, q_stride / k_stride elements apart (0 means dense), so
  *           that they may be parts of a fused projection's rows; NULL for 0 heads
  * q_out, k_out the same with strides of their own.  q_out may be q with the same stride, and k_out k;
- *           other overlaps of an input's rows with its output are refused (KV_ERR_INVALID_ARG)
+ *           other overlaps of the range from q's (k's) first row to its last with that of q_out (k_out)
+ *           are refused (KV_ERR_INVALID_ARG), and neither output's rows lie over the other's, or over
+ *           the other's input
  * positions [rows] int32, inv_freq [rot / 2] float64 (below 2^52)
  * rows, n_rows as in kv_paged_write
  * Limits: d a multiple of 8 up to 256, rot a multiple of 8, hq and hkv up to 4096.  No workspace.

@@ -760,12 +760,13 @@ kv_status kv_rotary(const kv_rotary_shape* shape, int back, const void* q, int64
     if (x.heads == 0) continue;
     if (x.in == nullptr || x.out == nullptr || !aligned16(x.in) || !aligned16(x.out))
       return KV_ERR_INVALID_ARG;
-    // in place, or apart from the rows that are read
-    const char *p = static_cast<const char*>(x.in), *o = static_cast<const char*>(x.out);
+    // in place, or apart from the rows that are read (counted in elements: no overflow)
     const int64_t row = (int64_t)x.heads * s.d;
-    const int64_t in_bytes = ((rows - 1) * *x.in_stride + row) * s.esize();
-    const int64_t out_bytes = ((rows - 1) * *x.out_stride + row) * s.esize();
-    if (p == o ? *x.in_stride != *x.out_stride && rows > 1 : p < o + out_bytes && o < p + in_bytes)
+    const int64_t in_rows = (rows - 1) * *x.in_stride + row;
+    const int64_t out_rows = (rows - 1) * *x.out_stride + row;
+    const int64_t ahead = ((int64_t)reinterpret_cast<uintptr_t>(x.out) -
+                           (int64_t)reinterpret_cast<uintptr_t>(x.in)) / s.esize();
+    if (ahead == 0 ? *x.in_stride != *x.out_stride && rows > 1 : ahead < in_rows && -ahead < out_rows)
       return KV_ERR_INVALID_ARG;
   }
   return cuda_status(launch_rotary(s, back != 0, q, q_stride, k, k_stride, positions, inv_freq,

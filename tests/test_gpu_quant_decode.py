@@ -445,3 +445,85 @@ def test_shared_workspace_two_graphs_and_streams():
         c.check(out)
         c.check_pools()
     assert torch.equal(third, outs[0])
+
+
+@pytest.mark.parametrize("fmt", ["e4m3", "int8"])
+def test_evicted_cache_into_8_bits(fmt):
+    """kv_compact_streaming's rows, their keys turned to positions within the cache, stored as
+    codes in head tables and attended to: against 64 bits at each step."""
+    from kv_cache_eviction_gb300 import workloads as W
+    layers, hq, hkv, d, n, page = 2, 8, 2, 128, 700, 32
+    wl = W.Workload(name="evicted", batch=1, layers=layers, hq=hq, hkv=hkv, d=d, n=n, w=32, pool=7,
+                    dtype="bf16", temp=(0.5, 8.0), seed=23)
+    shape = kv.KvShape.from_workload(wl)
+    inp = W.make_batch(wl, device="cuda")
+    budget = torch.tensor([[[150, 333], [32, 408]]], dtype=torch.int32, device="cuda")
+    cap = int(budget.sum())
+    kept = torch.full((cap,), -7, dtype=torch.int32, device="cuda")
+    cu = torch.empty(1, layers, hkv + 1, dtype=torch.int64, device="cuda")
+    lens = torch.empty(1, layers, hkv, dtype=torch.int32, device="cuda")
+    kf, vf = (torch.zeros(cap, d, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    ws = torch.zeros(256, dtype=torch.uint8, device="cuda")
+    kv.kv_compact_streaming(shape, inp["k"], inp["v"], 4, budget, 0, kept, cu, lens, kf, vf, cap, ws)
+    assert kv.kv_check_device_status(ws) == 0
+
+    # keys from their positions in the text to those in the cache
+    rows = lens.flatten().tolist()
+    new = np.concatenate([np.arange(m) for m in rows])
+    back = kept.cpu().numpy() - new
+    assert (back >= 0).all() and (back > 0).any()
+    freq = kv.kv_rotary_inv_freq(d, 500000.0)[0]
+    rot = kv.KvRotaryShape.of(0, 1, d, d, kv.KV_ROTARY_HALF, "bf16")
+    was = kf.double().cpu().numpy()
+    k3 = kf.view(cap, 1, d)
+    kv.kv_rotary(rot, None, k3, torch.tensor(back, dtype=torch.int32, device="cuda"), freq.cuda(),
+                 None, k3, back=True)
+    t = back[:, None] * freq.numpy()
+    a, b = was[:, :d // 2], was[:, d // 2:]
+    turned = np.concatenate([a * np.cos(t) + b * np.sin(t), b * np.cos(t) - a * np.sin(t)], 1)
+    assert (np.abs(kf.double().cpu().numpy() - turned) <=
+            2.0 ** -8 * np.abs(turned) + 2.0 ** -20 * (np.abs(was).max() + 1)).all()
+
+    # into the pages: a sequence of head tables for each layer
+    cols, num = ceil_div(max(rows), page), sum(ceil_div(m, page) for m in rows) + 5
+    ps = kv.KvPagedShape.of(layers, hq, hkv, d, hkv, page, cols, "bf16", num)
+    i32 = lambda x: torch.tensor(np.asarray(x), dtype=torch.int32, device="cuda")
+    i64 = lambda x: torch.tensor(np.asarray(x), dtype=torch.int64, device="cuda")
+    ws = workspace(kv.KV_OP_QUANT_DECODE, ps)
+    plens, ring = i32([0] * 4), i32(np.random.default_rng(1).permutation(num))
+    state, table = i64([0, num]), i32(np.zeros((4, cols)))
+    cu_add, slots = i64([0] * 5), i64([-1] * cap)
+    kv.kv_page_map(ps, plens, lens.flatten(), ring, state, table, plens, state, cu_add, slots, ws)
+    kp, vp = (torch.zeros(num, 1, page, d, dtype=torch.int8, device="cuda") for _ in range(2))
+    if fmt == "e4m3":
+        kp, vp = kp.view(torch.float8_e4m3fn), vp.view(torch.float8_e4m3fn)
+    ks, vs = (torch.zeros(num, 1, page // 16, device="cuda") for _ in range(2))
+    f = FORMATS[fmt]
+    kv.kv_quant_write(ps, f, k3, vf.view(cap, 1, d), slots, cu_add[4:], kp, vp, ks, vs, ws)
+    kr, vr = (torch.zeros(cap, 1, d, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    kv.kv_quant_read(ps, f, kp, vp, ks, vs, slots, None, kr, vr, ws)
+    q = torch.randn(layers, hq, d, generator=torch.Generator().manual_seed(2)).bfloat16().cuda()
+    out = torch.zeros_like(q)
+    kv.quant_decode_attn(ps, f, q, None, None, None, None, kp, vp, ks, vs, table, plens, d ** -0.5,
+                         out, ws)
+    assert kv.kv_check_device_status(ws) == 0
+    at = np.concatenate([[0], np.cumsum(rows)])
+    for u in range(4):
+        seg = slice(at[u], at[u + 1])
+        k, v = (x[seg, 0].double().cpu().numpy() for x in (kr, vr))
+        for x, y in ((k, kf), (v, vf)):     # a rounding of the block's code for every value
+            orig = y[seg].double().cpu().numpy()
+            for r0 in range(0, len(x), BLOCK):
+                o = orig[r0:r0 + BLOCK]
+                lim = (np.maximum(2.0 ** -4 * np.abs(o), 2.0 ** -10 * 2 * np.abs(o).max() / 448)
+                       if fmt == "e4m3" else np.abs(o).max() / 127)
+                assert (np.abs(x[r0:r0 + BLOCK] - o) <= lim).all()
+        for g in range(hq // hkv):
+            h = (u % hkv) * (hq // hkv) + g
+            z = k @ q[u // hkv, h].double().cpu().numpy() * d ** -0.5
+            p = np.exp(z - z.max())
+            p /= p.sum()
+            want, mag = p @ v, p @ np.abs(v)
+            tol = (2.0 ** -8 * np.abs(want) + mag * 2.0 ** -23 * (
+                4 * (d + 10) * (1 + np.abs(z).max() * 8) + 3 * len(z)))
+            assert (np.abs(out[u // hkv, h].double().cpu().numpy() - want) <= tol).all()

@@ -171,6 +171,10 @@ def test_rotary_refusals(L):
         assert call_rotary(L, s, qo=at(A, -far)) == INV
     assert call_rotary(L, s, ko=at(B, 16)) == INV
     assert call_rotary(L, s, qo=A, qos=32 * 128 + 8) == INV
+    # ranges of 2^62 elements are no overflow
+    big = dict(rows=(1 << 31) - 1, qs=1 << 31, qos=1 << 31)
+    assert call_rotary(L, s, qo=at(A, 1 << 60), **big) == INV
+    assert call_rotary(L, s, qo=at(A, 16), **big) == INV
     # nothing to do; no k, no q
     assert call_rotary(L, s, 0, None, 0, None, 0, None, None, 0, None, None, 0, None, 0) == OK
     assert call_rotary(L, rotary_shape(hkv=0), k=None, ko=None, rows=0) == OK
