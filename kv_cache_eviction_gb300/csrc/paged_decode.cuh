@@ -29,8 +29,13 @@
 // Rows past a table's last one, and rows of pages outside the pool, are masked: their scores
 // are -inf and their values zeros.  No CTA waits for another.
 //
-// The kernel is written for two kinds of pool (Rows and Codes below): rows of q's type, and rows of 8-bit
-// codes with a scale for each block of 16 rows of a head, two of which are a tile.
+// The kernel is written for two kinds of pool (Rows and Codes below): rows of q's type, and rows of
+// 8-bit codes with a scale for each block of 16 rows of a head, two of which are a tile.  Codes, the
+// same GB300 and heads (e4m3, bf16 q unless stated): 128 ragged sequences of 8000 rows, 2.1 GB, 317 us
+// (6.6 TB/s, 0.97 of the copy rate; int8 333 us, fp32 q 324 us); 64 of 2000 rows 55 us (4.7 TB/s);
+// one of 131000 rows 49 us (5.4 TB/s; int8, fp32 q 56 us); 256 heads of 128 rows 9.3 us; one
+// sequence of 500 rows 8.3 us.  Tiles of one block took 434 us on the 2.1 GB: 770 instructions for
+// 16 rows, and two warps a scheduler hide little of them.
 #pragma once
 
 #include <cfloat>
@@ -63,6 +68,8 @@ constexpr int kSmWarps = 8;
 // four warps by 2 to 14 % at 500 to 700 rows, eight by 10 to 40 % at 300 rows and for 8 units of 1400 or
 // 2000; of ragged ones, eight by 3 to 10 % from 700 rows.  Where the tables have columns for 131072
 // rows and few are held: 8 units of 500 rows 8.4 / 8.5, of 2000 12.6 / 9.5, 40 units of 500 11.3 / 11.4.
+// (Tiles of 16 rows.  Of codes, in tiles of 32 and so from half as many on: 8 units of 500 rows 8.3 / 8.9,
+// 2000 11.7 / 11.3, 4000 15.0 / 9.6, 16000 17.8 / 16.1; 32 ragged units of 8000 24.3 / 22.3.)
 constexpr int kLongUnits = 38;
 constexpr int kMaxCtas = 320;
 constexpr int kMaxCtasOfCodes = 480;
@@ -111,7 +118,10 @@ struct Rows {
   static constexpr int kWarps = kSmWarps;  // of an SM, in CTAs of four
   static constexpr bool kCodes = false;
 };
-// Pools of codes of the format F, for q, new rows and outputs of T, in NP pieces of 16 columns.
+// Pools of codes of the format F, for q, new rows and outputs of T, in NP pieces of 16 columns.  Up
+// to 64 columns a tile is half as many bytes for two thirds of the instructions, and twelve warps an
+// SM fit (64 ragged sequences of 4000 rows of 64: 58 us, with eight 66; 128 of 8000 183 and 214;
+// 256 heads of 128 rows 8.3 and 7.8).
 template <typename T_, typename F_, int NP>
 struct Codes {
   using T = T_;
@@ -450,7 +460,10 @@ paged_decode_kernel(const __grid_constant__ PagedArgs a) {
   }
   if (total == 0) return;
   const uint32_t want = (total + kMinTiles - 1) / kMinTiles;
-  const uint32_t Ne = want > (uint32_t)N ? N : want;   // CTAs that take tiles
+  uint32_t Ne = want > (uint32_t)N ? N : want;   // CTAs that take tiles
+  // One sequence: as many to each head, so that no CTA has parts of two (of 2000 rows 11.7 us with 126
+  // CTAs for 8 heads).
+  if (P::kCodes && a.U == 1 && Ne > (uint32_t)a.Hp) Ne -= Ne % a.Hp;
   if (c >= (int)Ne) return;
 
   auto rows_of = [&](int u) { return K == 1 ? sm.lens[u] : clamp_len(a.lens[u], most); };
@@ -1098,7 +1111,8 @@ cudaError_t launch_t(const PagedShape& s, const PagedArgs& a, cudaStream_t st) {
   const int64_t units = (int64_t)s.seqs * s.Hkv;
   // tiles that the tables could hold
   const int64_t tiles = units * cdiv((int64_t)s.max_pages * s.page, Cfg<P>::RT);
-  const bool few_long = units <= kLongUnits && tiles >= 2 * (int64_t)num_sms() * kMinTiles;
+  constexpr int64_t least = 2 * kMinTiles * 16 / (Cfg<P>::RT < 16 ? 16 : Cfg<P>::RT);   // an SM
+  const bool few_long = units <= kLongUnits && tiles >= least * num_sms();
   return few_long ? launch_w<P, 8>(s, a, tiles, st) : launch_w<P, 4>(s, a, tiles, st);
 }
 

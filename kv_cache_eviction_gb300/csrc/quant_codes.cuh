@@ -6,7 +6,7 @@
 // are exact, so a value is rounded once, by its code alone, and a block that moves to a larger
 // scale rounds again only what falls below the code's last place (in e4m3 what is subnormal there).
 // kLeast keeps scales and their reciprocals normal floats with room for the attention's factors:
-// values below 2^-9 2^kLeast (1.2e-31 in e4m3) become zero.
+// in blocks of that scale, values below 2^-106 (1.2e-32; int8 2^-97, 6e-30) become zero.
 //
 // Infinities become the code's largest number and do not count for the scale; a NaN is a NaN in
 // e4m3 and zero in int8.
@@ -22,8 +22,8 @@ namespace quant {
 constexpr int kBlock = 16;     // rows
 constexpr int kLeast = -96;
 
-// Formats: pack4 takes any float, pack4_held only what is within the code's range (after a scale_for of
-// a maximum that is finite).
+// Formats: pack4 takes any float, pack4_held only what is within the code's range (after a
+// scale_for of a maximum that is finite).
 struct E4M3 {
   // 448 = 0.875 * 2^9: a mantissa past 0.875 (1.75 as 1.m) needs a step more
   static constexpr int kTopExp = 9;

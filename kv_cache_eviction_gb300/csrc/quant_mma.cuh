@@ -1,23 +1,22 @@
-// One warp's online softmax over tiles of 32 K and V rows of 8-bit codes, for up to 8 query rows, on the
-// warp matrix instructions in fp16 (paged_mma.cuh has the sums and the tile's layout).
+// One warp's online softmax over tiles of 32 K and V rows of 8-bit codes, for up to 8 query rows,
+// on the warp matrix instructions in fp16 (paged_mma.cuh has the sums and the tile's layout).
 //
 // fp16 holds every code exactly, and the block's scales are factors of a tile's sums: of the scores
-// (after the product with q) and of the outputs (when a tile's sums, which start from zero, are added
-// to o).  So the codes cost their conversion and nothing else.
+// (after the product with q) and of the outputs (when a tile's sums, which start from zero, are
+// added to o).  So the codes cost their conversion and nothing else.
 //   q is taken times a power of two that brings its largest element to 2^13..2^14, which fp16 holds to
 //     2^-24, 2^-37 of it; bf16's 8 bits are then exact, and fp32's are held as two fp16 (22 bits).
 //   p, at most 1, is taken 2^14 times as large and held as two fp16 as well: 22 bits, or 2^-39.
 //
 // m16n8k16's larger side is the codes': scores are K q^T (16 rows, 8 queries), outputs V^T p^T (16
-// columns, 8 queries).  With the queries on that side half of its rows stood empty (or held the lower
-// parts), and its four registers had to be put together for every product: 770 instructions a tile,
-// and 322 us on 2.1 GB.
-// K's words hold four columns of a row, 16 p + 4 c + 0..3 for lane c of 4: they are taken as columns
-// 2 c, 2 c + 1 and 2 c + 8, 2 c + 9 of the instruction, and q's likewise.  V's transposed load moves pairs
-// of columns, so a word has two rows of two columns: rows 0..7 of V^T's 16 are the even ones of a piece,
-// 8..15 the odd ones.  A lane (4 g + c) has the scores of rows g and g + 8 for queries 2 c and 2 c + 1;
-// as right operand the second product wants rows 2 c and 2 c + 1 for query g: a transposition of 8 by
-// 8, movmatrix.
+// columns, 8 queries).  With the queries on that side half of its rows stood empty (or held the
+// lower parts), and its four registers had to be put together for every product: 770 instructions a
+// tile, and 322 us on 2.1 GB. K's words hold four columns of a row, 16 p + 4 c + 0..3 for lane c of
+// 4: they are taken as columns 2 c, 2 c + 1 and 2 c + 8, 2 c + 9 of the instruction, and q's
+// likewise.  V's transposed load moves pairs of columns, so a word has two rows of two columns:
+// rows 0..7 of V^T's 16 are the even ones of a piece, 8..15 the odd ones.  A lane (4 g + c) has the
+// scores of rows g and g + 8 for queries 2 c and 2 c + 1; as right operand the second product wants
+// rows 2 c and 2 c + 1 for query g: a transposition of 8 by 8, movmatrix.
 #pragma once
 
 #include "paged_mma.cuh"
@@ -41,7 +40,8 @@ __device__ __forceinline__ void mma_f16_new(float (&d)[4], const uint32_t (&a)[4
       : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
 }
-// An 8 by 8 matrix of 16-bit elements, transposed: lane 4 g + c gives row g, columns 2 c and 2 c + 1.
+// An 8 by 8 matrix of 16-bit elements, transposed: lane 4 g + c gives row g, columns 2 c and 2 c +
+// 1.
 __device__ __forceinline__ uint32_t transposed(uint32_t x) {
   uint32_t r;
   asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));

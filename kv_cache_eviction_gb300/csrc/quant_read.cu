@@ -1,5 +1,8 @@
 // Rows of the 8-bit cache as the values they stand for: code * scale, which bf16 and fp32 hold
-// exactly.  Bound by reading the codes and writing the rows once.
+// exactly.  Bound by reading the codes and writing the rows once.  A lane writes 16 bytes of K's
+// rows and of V's at a time, its neighbours those beside them.  On GB300: 131072 rows of 8 heads of
+// 128 bf16 from int8 (806 MB) 121.6 us, 6.6 TB/s or 0.98 of the measured copy rate (141 us with 16
+// codes a lane, whose stores fill half sectors); 513 rows 2.4 us.
 #include "quant_codes.cuh"
 #include "tc_ptx.cuh"
 
@@ -123,8 +126,8 @@ quant_read_kernel(const __grid_constant__ QReadArgs a) {
 template <typename T, typename F>
 cudaError_t launch(const QReadArgs& a, cudaStream_t st) {
   int64_t grid = cdiv(a.rows, (int64_t)(32 * kPieces >> a.pad_shift) * (kThreads / 32));
-  // (many small CTAs even out what the SMs get through: 131072 rows 121.6 us; 122.9 with 32 of twice the
-  // threads, 130.6 with 8, 126.2 without a limit)
+  // (many small CTAs even out what the SMs get through: 131072 rows 121.6 us; 122.9 with 32 of
+  // twice the threads, 130.6 with 8, 126.2 without a limit)
   const int64_t most = (int64_t)num_sms() * 64;
   if (grid > most) grid = most;
   cudaLaunchConfig_t cfg{};

@@ -1,9 +1,14 @@
-// Rows of K and V stored in 8 bits at their slots, with a scale for each block of 16 slots and
-// head (quant_codes.cuh).  Bound by reading the rows and writing the codes once.
+// Rows of K and V stored in 8 bits at their slots, with a scale for each block of 16 slots and head
+// (quant_codes.cuh).  Bound by reading the rows and writing the codes once.
 //
 // A run of rows whose slots follow each other within one block is a unit: a warp loads a head's
-// rows of it, finds their largest magnitude, and writes the codes from its registers.  Rows of
-// the block below the run were held before: where the scale grows, their codes are rounded to it.
+// rows of it, finds their largest magnitude, and writes the codes from its registers.  Rows of the
+// block below the run were held before: where the scale grows, their codes are rounded to it. The
+// slots of a warp's next rows are under way while it works (a chain of slots, rows, codes
+// otherwise).  On GB300: 131072 rows of 8 heads of 128 bf16 (806 MB read and written) 120 us, 6.7
+// TB/s or 0.99 of the measured copy rate (134 us without, 32 bytes a lane and two divisions a
+// piece); 100003 fp32 rows of one head of 64 15.8 us (21.9), 4.1 TB/s: 3.4 runs a warp; 64 rows 2.3
+// us.
 #include "quant_codes.cuh"
 #include "tc_ptx.cuh"
 
@@ -12,7 +17,9 @@ namespace {
 
 using quant::Piece;
 constexpr int kThreads = 128;
-// CTAs of an SM: as many as the pieces in registers allow
+// CTAs of an SM by a lane's pieces.  131072 bf16 rows of 128 (8 pieces), us: 4 CTAs 133, 5 124, 6
+// 120, 7 134, 8 (the registers then spill) 140; 100003 fp32 rows of 64 (8 pieces): 16.9, 15.1,
+// 15.8, 15.6, 15.5.
 constexpr int resident(int pieces) { return pieces <= 4 ? 8 : pieces <= 8 ? 6 : 3; }
 
 struct QWriteArgs {

@@ -1,29 +1,31 @@
-// Rotary positions: the pairs (a, b) of a head's first `rot` columns turned by position * frequency,
+// Rotary positions: the pairs (a, b) of a head's first `rot` columns turned by position *
+// frequency,
 //   (a, b) -> m (a cos t - b sin t, a sin t + b cos t),
-// pairs (x_i, x_{i + rot/2}) or (x_2i, x_2i+1).  A copy with a few operations: bound by reading
-// and writing every row once.
+// pairs (x_i, x_{i + rot/2}) or (x_2i, x_2i+1).  A copy with a few operations: bound by reading and
+// writing every row once.
 //
-// Angles are counted in turns, as 64-bit fractions of one: frequency / 2 pi is cut to 2^-64 of a turn
-// once (in integers: 64-bit floats are slow here), and position * frequency is an integer product whose whole turns fall off at the top.
-// So a position of 2^31 has the angle of a small one, to 2^-32 of a turn.  The fraction is cut
-// to its nearest quarter turn before it becomes a float, which then has it to 2^-27 of a turn.
+// Angles are counted in turns, as 64-bit fractions of one: frequency / 2 pi is cut to 2^-64 of a
+// turn once (in integers: 64-bit floats are slow here), and position * frequency is an integer
+// product whose whole turns fall off at the top. So a position of 2^31 has the angle of a small
+// one, to 2^-32 of a turn.  The fraction is cut to its nearest quarter turn before it becomes a
+// float, which then has it to 2^-27 of a turn.
 //
-// A warp takes a row: a lane's pairs are the same ones in every head, so their sines and cosines are
-// worked out once a row, shared by the lanes of the heads that it turns at a time.  Rows of small calls
-// are split by heads.  On GB300: 131072 rows of 32 + 8 heads of 128 bf16 (2.7 GB read and written)
-// 412 us, 6.5 TB/s or 0.96 of the measured copy rate; 20011 fp32 rows of 8 heads of 80, 24 columns of them
-// turned, 21.5 us (24.4 with the other columns copied one after the other); 64 rows 2.6 us (3.7 with
-// every lane working out all of its pairs' sines).
+// A warp takes a row: a lane's pairs are the same ones in every head, so their sines and cosines
+// are worked out once a row, shared by the lanes of the heads that it turns at a time.  Rows of
+// small calls are split by heads.  On GB300: 131072 rows of 32 + 8 heads of 128 bf16 (2.7 GB read
+// and written) 412 us, 6.5 TB/s or 0.96 of the measured copy rate; 20011 fp32 rows of 8 heads of
+// 80, 24 columns of them turned, 21.5 us (24.4 with the other columns copied one after the other);
+// 64 rows 2.6 us (3.7 with every lane working out all of its pairs' sines).
 #include "kv_internal.cuh"
 #include "tc_ptx.cuh"
 
 namespace kv {
 namespace {
 
-// Small CTAs, and more of them than are resident, even out what the SMs get through.  131072 rows / 20011
-// fp32 rows, us: 128 CTAs of two warps 412 / 21.5, 64 of four 413 / 23.0, 16 of four 447 / 22.8, 8 of
-// eight 442 / 21.4.  (Heads loaded ahead of the one that is turned: 447 / 24.0.  One head at a time instead
-// of four unrolled: 462 / 22.4.)
+// Small CTAs, and more of them than are resident, even out what the SMs get through.  131072 rows /
+// 20011 fp32 rows, us: 128 CTAs of two warps 412 / 21.5, 64 of four 413 / 23.0, 16 of four 447 /
+// 22.8, 8 of eight 442 / 21.4.  (Heads loaded ahead of the one that is turned: 447 / 24.0.  One
+// head at a time instead of four unrolled: 462 / 22.4.)
 constexpr int kThreads = 64;
 constexpr int kGrid = 128;      // CTAs of an SM, at most
 constexpr uint64_t kInvTwoPi = 0x28be60db9391054aull;   // 2^64 / 2 pi
@@ -79,8 +81,8 @@ struct Vec {
   }
 };
 
-// frequency / 2 pi as a fraction of a turn, to 2^-64 of the frequency: the double's 53 bits times the
-// first 64 of 1 / 2 pi, whole turns dropped.  Zero for what is no number below 2^52.
+// frequency / 2 pi as a fraction of a turn, to 2^-64 of the frequency: the double's 53 bits times
+// the first 64 of 1 / 2 pi, whole turns dropped.  Zero for what is no number below 2^52.
 __device__ __forceinline__ uint64_t fraction(double frequency) {
   const uint64_t bits = (uint64_t)__double_as_longlong(frequency);
   const int e = (int)(bits >> 52) & 0x7FF, sh = 1075 - e;   // frequency = m 2^-sh
