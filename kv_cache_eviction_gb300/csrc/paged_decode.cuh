@@ -81,10 +81,12 @@ constexpr int kMinTiles = 4;
 // the workspace and a ticket cost 2 us, the tiles less than that.  16 / 24 / 32 / 48 tiles: 256 heads
 // of 128 rows 11.2 / 10.9 / 10.6 / 10.6 us; units of 500 rows (32 tiles), 8 of them 8.2 / 8.2 / 11.2 /
 // 11.2, 16 9.8 / 9.8 / 11.4 / 11.4, 64 11.6 / 11.7 / 11.7 / 13.2, 128 13.2 / 13.2 / 13.1 / 15.2;
-// units of 2000 rows level.  (Tiles of 16 rows; in rows the same holds for those of 32: one sequence of
-// 500 rows 10.4 us with 24 of them, 8.8 with 12 or 8; 256 heads of 128 9.6, 9.6 and 11.8.)
+// units of 2000 rows level.  Those are tiles of 16 rows.  Of 32, 8 / 12 / 15 / 20 tiles: units of 500 rows
+// (16 tiles), 8 of them 8.3 / 8.3 / 8.3 / 10.2 us; 64 ragged ones 10.5 / 10.5 / 10.5 / 10.7; 256 heads of
+// 128 rows, all of at most 10 tiles, 11.8 / 9.4 / 9.4 / 9.4, two of them of 13 and 14 11.7 with 12, 11.0
+// with 15 and 20.
 template <int RT>
-constexpr int kSnapTiles = RT == 32 ? 12 : 24;
+constexpr int kSnapTiles = RT == 32 ? 15 : 24;
 // Part of a unit in the workspace: max[8], sum[8], then o[G][D].
 constexpr int kPartHead = 16;
 constexpr int kPartFloats = kPartHead + 8 * 128;
