@@ -597,7 +597,10 @@ KV_API kv_status paged_decode_attn(const kv_paged_shape* shape, const void* q, c
  * For i < rows, with slot = slot_map[i] and the scales as above: code = round(x / scale), halves to
  * even.  Rows with slot -1 are skipped; any other slot outside the pool sets the device error word
  * (10) and is skipped.  The rows of one block are neighbours in slot_map, in ascending order and with
- * no gap (kv_page_map's are); a block's rows appear once per call.
+ * no gap (kv_page_map's are); a block's rows appear once per call.  Where a row's neighbour before it
+ * is of the same block and not the row before it there, the row, and those that follow on from it, are
+ * skipped and reported (10); a block that comes again further on is not noticed, and its scale and
+ * codes are then undefined.
  *
  * k, v, src_stride, rows, n_rows as in kv_paged_write
  */

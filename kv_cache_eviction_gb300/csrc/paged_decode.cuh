@@ -1102,7 +1102,9 @@ cudaError_t launch_w(const PagedShape& s, const PagedArgs& a, int64_t tiles, cud
   // sequence of 500 rows: 8.1 us on the device either way, 9.2 against 10.0 us from Python).
   cudaLaunchAttribute attr[1] = {pdl_attribute()};
   cfg.attrs = attr;
-  cfg.numAttrs = grid >= per_sm * num_sms() ? 1 : 0;
+  // Codes: quant_decode_attn's call costs the host 3 us (csrc/binding.cpp), so always: 8.7 us a call of
+  // 500 rows from Python, 10.3 without.
+  cfg.numAttrs = P::kCodes || grid >= per_sm * num_sms() ? 1 : 0;
   const cudaError_t e = cudaLaunchKernelEx(&cfg, paged_decode_kernel<P, kPWarps>, a);
   if (e == cudaSuccess) count_launches(1);
   return e;

@@ -136,7 +136,7 @@ cudaError_t launch(const QReadArgs& a, cudaStream_t st) {
   cfg.stream = st;
   cudaLaunchAttribute attr[1] = {pdl_attribute()};
   cfg.attrs = attr;
-  cfg.numAttrs = grid == most ? 1 : 0;
+  cfg.numAttrs = 1;   // (calls of 513 rows one after the other 3.0 us, 4.2 without)
   const cudaError_t e = cudaLaunchKernelEx(&cfg, quant_read_kernel<T, F>, a);
   if (e == cudaSuccess) count_launches(1);
   return e;

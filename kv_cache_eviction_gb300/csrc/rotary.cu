@@ -217,7 +217,7 @@ cudaError_t launch_own(const RotaryArgs& a, cudaStream_t st) {
   cfg.stream = st;
   cudaLaunchAttribute attr[1] = {pdl_attribute()};
   cfg.attrs = attr;
-  cfg.numAttrs = grid == most ? 1 : 0;
+  cfg.numAttrs = 1;   // (calls of 64 rows one after the other 2.6 us, 4.2 without)
   const cudaError_t e = cudaLaunchKernelEx(&cfg, rotary_kernel<T, V, kHalf, kOwn>, a);
   if (e == cudaSuccess) count_launches(1);
   return e;

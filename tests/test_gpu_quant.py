@@ -168,6 +168,25 @@ def test_write_bad_slots(fmt):
     pool.check()
 
 
+@pytest.mark.parametrize("many", [1, 400])
+def test_write_slots_astray(many):
+    """A row whose neighbour is of its block but not the row before it there (a gap, a step back,
+    the same slot again) is skipped with what follows on from it, and reported; the rest is stored."""
+    one = [5, 7, 8, 40, 39, 70, 70, 71, 100, 101, 103, 112, 160, 175, 176, 177, 200, 199, 200, 201]
+    kept = [0, 3, 5, 8, 9, 11, 12, 14, 15, 16]
+    slots = np.concatenate([np.array(one) + 256 * i for i in range(many)])
+    keep = np.concatenate([np.array(kept) + len(one) * i for i in range(many)])
+    pool = Pool(16 * many, 2, 16, 64, "int8", 7)
+    s = shape_of(pool, "bf16")
+    x = rows_of(2, len(slots), 2, 64, "bf16")
+    ws = write(pool, s, x[0].cuda(), x[1].cuda(), slots)
+    assert kv.kv_check_device_status(ws) == ERR_ID
+    left = np.full(len(slots), -1)
+    left[keep] = slots[keep]
+    pool.put(*x.double().numpy(), left)
+    pool.check()
+
+
 @pytest.mark.parametrize("fmt", ["e4m3", "int8"])
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("rows,heads,tables,d,page,fused,extra", [

@@ -527,3 +527,55 @@ def test_evicted_cache_into_8_bits(fmt):
             tol = (2.0 ** -8 * np.abs(want) + mag * 2.0 ** -23 * (
                 4 * (d + 10) * (1 + np.abs(z).max() * 8) + 3 * len(z)))
             assert (np.abs(out[u // hkv, h].double().cpu().numpy() - want) <= tol).all()
+
+
+@pytest.mark.parametrize("fmt", ["e4m3", "int8"])
+def test_steps_back_to_back(fmt):
+    """Steps whose kernels start before the ones ahead of them have ended give what steps with waits
+    between them give: rows and scales of the step before are read, from sectors that other CTAs
+    wrote, and scales change at every step."""
+    seqs, hq, hkv, d, page, cols, steps = 24, 16, 8, 64, 32, 9, 60
+    num = seqs * cols
+    shape = kv.KvPagedShape.of(seqs, hq, hkv, d, 1, page, cols, "bf16", num)
+    g = torch.Generator().manual_seed(3)
+    size = torch.exp2(torch.arange(steps) % 13 + torch.arange(steps) // 13).view(-1, 1, 1, 1)
+    q, k, v = ((torch.randn(steps, seqs, h, d, generator=g) * f).bfloat16().cuda()
+               for h, f in ((hq, 1.0), (hkv, size ** 0.25), (hkv, size)))
+    start = torch.randint(0, 200, (seqs,), generator=g, dtype=torch.int32)
+    got = []
+    for wait in (True, False):
+        i32 = lambda x: torch.as_tensor(x, dtype=torch.int32).cuda()
+        lens, add, state = i32(torch.zeros(seqs)), start.cuda(), torch.tensor([0, num]).cuda()
+        ring, table = i32(torch.arange(num)), i32(torch.zeros(seqs, cols))
+        cu = torch.zeros(seqs + 1, dtype=torch.int64, device="cuda")
+        codes = torch.zeros(2, num, hkv, page, d, dtype=torch.uint8, device="cuda")
+        codes = codes.view(torch.float8_e4m3fn if fmt == "e4m3" else torch.int8)
+        sc = torch.full((2, num, hkv, page // 16), 2.0 ** -5, device="cuda")
+        out = torch.zeros(steps, seqs, hq, d, dtype=torch.bfloat16, device="cuda")
+        ws = workspace(kv.KV_OP_QUANT_DECODE, shape)
+        slots = torch.full((int(start.sum()),), -1, dtype=torch.int64, device="cuda")
+        kv.kv_page_map(shape, lens, add, ring, state, table, lens, state, cu, slots, ws)
+        rows = torch.randn(2, len(slots), hkv, d, generator=torch.Generator().manual_seed(5))
+        rows = rows.bfloat16().cuda()
+        kv.kv_quant_write(shape, FORMATS[fmt], rows[0], rows[1], slots, None, codes[0], codes[1],
+                          sc[0], sc[1], ws)
+        add.fill_(1)
+        torch.cuda.synchronize()
+        for i in range(steps):
+            for call in (lambda: kv.kv_page_map(shape, lens, add, ring, state, table, lens, state,
+                                                cu, slots[:seqs], ws),
+                         lambda: kv.quant_decode_attn(shape, FORMATS[fmt], q[i], k[i], v[i], cu,
+                                                      slots[:seqs], codes[0], codes[1], sc[0],
+                                                      sc[1], table, lens, 0.1, out[i], ws),
+                         lambda: kv.quant_decode_attn(shape, FORMATS[fmt], q[i], None, None, None,
+                                                      None, codes[0], codes[1], sc[0], sc[1],
+                                                      table, lens, 0.1, out[i], ws)):
+                call()
+                if wait:
+                    torch.cuda.synchronize()
+        torch.cuda.synchronize()
+        assert kv.kv_check_device_status(ws) == 0
+        got.append([out, codes.view(torch.uint8), sc, table, lens])
+    for a, b in zip(*got):
+        assert torch.equal(a, b)
+    assert bool(torch.isfinite(got[0][0]).all())
