@@ -293,6 +293,11 @@ __device__ __forceinline__ void cp_async_wait() {   // all groups but the last N
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
+// The line-th 128 bytes of a tensor of `bytes`, if it has them, into L2.
+__device__ __forceinline__ void prefetch_line(const void* p, int64_t line, int64_t bytes) {
+  if (line * 128 < bytes)
+    asm volatile("prefetch.global.L2 [%0];" ::"l"((const char*)p + line * 128));
+}
 __device__ __forceinline__ uint32_t atomic_add_acq_rel(uint32_t* p, uint32_t x) {
   uint32_t r;
   asm volatile("atom.add.acq_rel.gpu.global.u32 %0, [%1], %2;" : "=r"(r) : "l"(p), "r"(x) : "memory");
@@ -402,6 +407,17 @@ paged_decode_kernel(const __grid_constant__ PagedArgs a) {
   const int most = a.max_pages << a.shift;
   // a programmatic dependent launch: nothing of the call before is read or written until it ends
   ptx::griddep_launch_dependents();
+  if constexpr (P::kCodes) {
+    // (what the chain of loads below begins with, into L2 while the call before ends: no reading)
+    const int64_t line = (int64_t)c * kPThreads + tid;
+    prefetch_line(a.lens, line, (int64_t)a.U * 4);
+    prefetch_line(a.table, line, (int64_t)a.U * a.max_pages * 4);
+    prefetch_line(a.q, line, (int64_t)a.U * a.Hp * G * d * (int)sizeof(T));
+    if (a.kn != nullptr) {
+      prefetch_line(a.kn, line, (int64_t)a.U * a.Hp * d * (int)sizeof(T));
+      prefetch_line(a.vn, line, (int64_t)a.U * a.Hp * d * (int)sizeof(T));
+    }
+  }
   ptx::griddep_wait();
 
   // ---- 1. tiles of all tables.  Up to 32 tables fit a warp's window: every warp finds its

@@ -100,6 +100,32 @@ def test_every_width_over_many_ctas(d, G):
         finish(c, out, ws)
 
 
+@pytest.mark.parametrize("d,G,dtype", [(16, 1, "f32"), (80, 7, "bf16"), (128, 8, "f32"),
+                                       (64, 5, "bf16")])
+def test_nothing_around_the_outputs(d, G, dtype):
+    """Sentinels before and behind the output and the workspace stay, and so do all inputs."""
+    for lens in ([9000, 0, 33], [5] * 300):
+        c = QuantCache(len(lens), 2, G, d, 1, 32, lens, dtype, "int8", d)
+        n, pad = c.seqs * c.hkv * G * d, 256
+        buf = torch.full((n + 2 * pad,), 3.0, dtype=c.dt, device="cuda")
+        out = buf[pad:pad + n].view(c.seqs, c.hkv * G, d)
+        m = kv.kv_paged_workspace_size(kv.KV_OP_QUANT_DECODE, c.shape)
+        wbuf = torch.full((m + 512,), 77, dtype=torch.uint8, device="cuda")
+        wbuf[256:256 + m] = 0
+        ins = [c.qd, c.knd, c.vnd, c.cu, c.slots, c.table, c.lens_t]
+        was = [t.clone() for t in ins]
+        c.run(ws=wbuf[256:256 + m], out=out)
+        torch.cuda.synchronize()
+        assert bool((buf[:pad] == 3.0).all()) and bool((buf[pad + n:] == 3.0).all())
+        assert bool((wbuf[:256] == 77).all()) and bool((wbuf[256 + m:] == 77).all())
+        assert all(torch.equal(a, b) for a, b in zip(ins, was))
+        # what the calls that share the workspace need at zero: the error word and the tickets
+        assert not bool(wbuf[256:256 + 256 + 2048].any())
+        c.put()
+        c.check(out)
+        c.check_pools()
+
+
 @pytest.mark.parametrize("extra", [16, 128, 4096])
 def test_page_stride(extra):
     c = QuantCache(3, 2, 4, 128, 1, 16, [100, 0, 333], "bf16", "e4m3", 5, extra=extra)
