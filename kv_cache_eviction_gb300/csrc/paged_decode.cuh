@@ -648,7 +648,15 @@ paged_decode_kernel(const __grid_constant__ PagedArgs a) {
         cp_async16(x, k, bytes);
         cp_async16(H % 2 == 0 ? x + C::kStage / 2 : (dst_v ^ flip) + row, v, bytes);
       };
-      if (W::whole(word)) {
+      if (P::kCodes && d == D && W::whole(word)) {
+        // rows that fill their pieces: the strides are constants (int8 on the 2.1 GB 333 us, 338 without)
+        const E *k2 = ks + skip, *v2 = vs + skip;
+#pragma unroll
+        for (int i = 0; i < RT / C::kRows; ++i) {
+          const bool second = i * C::kRows >= RT / 2;
+          copy(i, (second ? k2 : ks) + i * C::kRows * D, (second ? v2 : vs) + i * C::kRows * D, 16);
+        }
+      } else if (W::whole(word)) {
 #pragma unroll
         for (int i = 0; i < RT / C::kRows; ++i) {
           const int64_t o = i * C::kRows * d + (i * C::kRows >= RT / 2 ? skip : (int64_t)0);
