@@ -937,8 +937,10 @@ paged_decode_kernel(const __grid_constant__ PagedArgs a) {
     // little code.  (Few CTAs get here, so its instructions are not at hand; one unit after the other,
     // 8 ragged sequences of 2000 rows took 18.8 us.)
     const int part4s = (kPartHead + G * D) / 4;   // 16-byte pieces of a part
-    int room = kPWarps * S * C::kStage / 16 / part4s;   // parts
-    if (n0 > 0 && n1 > 0) room /= 2;
+    // The parts of a unit are summed `half` at a time, whether the CTA has one unit or two: what it
+    // has depends on which CTA was the last, and the sums shall not.
+    const int half = kPWarps * S * C::kStage / 32 / part4s;   // half of what the rings hold
+    const int room = n0 > 0 && n1 > 0 ? half : 2 * half;
     constexpr int kSlices = (8 * (D / 4) + kPThreads - 1) / kPThreads;   // of a thread, at most
     const uint32_t to = ptx::smem_u32(sm.ring);
     const float* ring_f = reinterpret_cast<const float*>(sm.ring);
@@ -978,28 +980,33 @@ paged_decode_kernel(const __grid_constant__ PagedArgs a) {
         for (int j = 0; j < kSlices; ++j) {
           const int idx = tid + j * kPThreads, g = idx / (D / 4);
           if (idx >= nsl) continue;
-          float mn = M[y][j];
+#pragma unroll 1
+          for (int from = 0; from < n; from += half) {
+            const float* at = in + from * part4s * 4;
+            const int count = min(half, n - from);
+            float mn = M[y][j];
 #pragma unroll 4
-          for (int k = 0; k < n; ++k) mn = fmaxf(mn, in[k * part4s * 4 + g]);
-          const float base = mn == -INFINITY ? 0.f : mn;
-          const float f = ptx::ex2((M[y][j] - base) * a.scale.c2);   // 0 while M is -inf
-          float4 o = acc[y][j];
-          float l = L[y][j] * f;
-          o = make_float4(o.x * f, o.y * f, o.z * f, o.w * f);
+            for (int k = 0; k < count; ++k) mn = fmaxf(mn, at[k * part4s * 4 + g]);
+            const float base = mn == -INFINITY ? 0.f : mn;
+            const float f = ptx::ex2((M[y][j] - base) * a.scale.c2);   // 0 while M is -inf
+            float4 o = acc[y][j];
+            float l = L[y][j] * f;
+            o = make_float4(o.x * f, o.y * f, o.z * f, o.w * f);
 #pragma unroll 4
-          for (int k = 0; k < n; ++k) {
-            const float* W = in + k * part4s * 4;
-            const float w = ptx::ex2((W[g] - base) * a.scale.c2);
-            const float4 x = *reinterpret_cast<const float4*>(W + kPartHead + idx * 4);
-            l = fmaf(W[8 + g], w, l);
-            o.x = fmaf(x.x, w, o.x);
-            o.y = fmaf(x.y, w, o.y);
-            o.z = fmaf(x.z, w, o.z);
-            o.w = fmaf(x.w, w, o.w);
+            for (int k = 0; k < count; ++k) {
+              const float* W = at + k * part4s * 4;
+              const float w = ptx::ex2((W[g] - base) * a.scale.c2);
+              const float4 x = *reinterpret_cast<const float4*>(W + kPartHead + idx * 4);
+              l = fmaf(W[8 + g], w, l);
+              o.x = fmaf(x.x, w, o.x);
+              o.y = fmaf(x.y, w, o.y);
+              o.z = fmaf(x.z, w, o.z);
+              o.w = fmaf(x.w, w, o.w);
+            }
+            M[y][j] = mn;
+            L[y][j] = l;
+            acc[y][j] = o;
           }
-          M[y][j] = mn;
-          L[y][j] = l;
-          acc[y][j] = o;
         }
       }
       __syncthreads();

@@ -100,6 +100,16 @@ def test_every_width_over_many_ctas(d, G):
         finish(c, out, ws)
 
 
+def test_thousands_of_tables():
+    """More tables than a CTA has threads: strips of tables, windows that move on."""
+    rng = np.random.default_rng(7)
+    lens = rng.integers(0, 30, 5000)
+    lens[[3, 2500, 4990]] = [2000, 900, 40]
+    c = QuantCache(1250, 4, 2, 32, 4, 16, lens, "bf16", "e4m3", 8, new=rng.random(5000) < 0.7)
+    out, ws = c.run()
+    finish(c, out, ws)
+
+
 @pytest.mark.parametrize("d,G,dtype", [(16, 1, "f32"), (80, 7, "bf16"), (128, 8, "f32"),
                                        (64, 5, "bf16")])
 def test_nothing_around_the_outputs(d, G, dtype):
@@ -124,6 +134,26 @@ def test_nothing_around_the_outputs(d, G, dtype):
         c.put()
         c.check(out)
         c.check_pools()
+
+
+@pytest.mark.parametrize("hkv,G,d,lens", [(2, 8, 96, [2061, 2500]), (1, 8, 128, [1500] * 40),
+                                          (8, 5, 128, [4000]), (4, 8, 112, [900, 2000, 5100, 333]),
+                                          (3, 7, 48, [3100, 1250, 7000])])
+def test_same_bits_whoever_is_last(hkv, G, d, lens):
+    """Units of many parts, cut in the middle of CTAs: which CTA ends last, and whether it then has
+    one unit to merge or two, changes from run to run, with other work on the GPU; the bits do not."""
+    noise = torch.randn(4096, 4096, device="cuda")
+    side = torch.cuda.Stream()
+    for seed in range(3):
+        c = QuantCache(len(lens), hkv, G, d, 1, 64, lens, "f32", ("e4m3", "int8")[seed % 2], seed)
+        out, ws = c.run()
+        for i in range(40):
+            if i % 4 == 1:
+                side.wait_stream(torch.cuda.current_stream())
+                with torch.cuda.stream(side):
+                    noise @ noise if i % 8 == 1 else noise.add_(1)
+            assert torch.equal(out, c.run(ws=ws)[0])
+        finish(c, out, ws)
 
 
 @pytest.mark.parametrize("extra", [16, 128, 4096])
