@@ -581,10 +581,11 @@ KV_API kv_status paged_decode_attn(const kv_paged_shape* shape, const void* q, c
  * infinities become the largest code, a NaN stays one in e4m3 and becomes 0 in int8.
  *
  * Rows that are added to a block which holds some take its scale, or raise it: the codes of the
- * rows held are then rounded to the new scale (in e4m3 that changes only values below 2^-6 of it).
- * The rows that a call writes to a block are rounded once, at the scale that holds them all.  The rows
- * held are those below the first that the call writes, so a block that is filled anew from its first
- * row on forgets what it had.  A block that gets rows belongs to one table.
+ * rows held are then rounded to the new scale (in e4m3 that changes only values below 2^-6 of it;
+ * in int8 each raise adds up to half of the new scale to what a value is off by).  The rows that a
+ * call writes to a block are rounded once, at the scale that holds them all.  The rows held are those
+ * below the first that the call writes, so a block that is filled anew from its first row on forgets
+ * what it had.  A block that gets rows belongs to one table.
  *
  * Limits: those of the paged cache, and page >= 16, d a multiple of 16 (KV_ERR_UNSUPPORTED).
  * page_stride is a multiple of 16.  Workspaces: kv_paged_workspace_size with the ops of kv_quant_op;
@@ -634,9 +635,10 @@ KV_API kv_status kv_quant_read(const kv_paged_shape* shape, int format, const vo
  * above.  A table's slot has to be the place that its block table gives row lens - 1 (kv_page_map's
  * is): at any other one in the pool the row is not stored, and the error word is set (10).
  * Sums, the softmax and out before its rounding are float32 (fp32 q is held to 22 bits, the softmax
- * numerators to 22 bits or 2^-39 of the largest; bf16 q and the values are exact).  q, the values attended to and their scores
- * have to be finite (a NaN among them makes the outputs it reaches NaN, an infinity may).  Every
- * result is the same in every run.
+ * numerators to 22 bits or 2^-39 of the largest; bf16 q and the values are exact).  q, the values
+ * attended to and their scores have to be finite (a NaN among them makes the outputs it reaches NaN,
+ * an infinity may); anything may stand behind a table's last row, in pages of no table and in the
+ * scales of blocks that hold no row.  Every result is the same in every run.
  */
 KV_API kv_status quant_decode_attn(const kv_paged_shape* shape, int format, const void* q,
                                    const void* k_new, const void* v_new, const int64_t* cu_add,
