@@ -676,7 +676,7 @@ typedef struct {
  *           other overlaps of the range from q's (k's) first row to its last with that of q_out (k_out)
  *           are refused (KV_ERR_INVALID_ARG), and neither output's rows lie over the other's, or over
  *           the other's input
- * positions [rows] int32, inv_freq [rot / 2] float64 (below 2^52)
+ * positions [rows] int32, inv_freq [rot / 2] float64 (below 2^52 in size; a larger one turns nothing)
  * rows, n_rows as in kv_paged_write
  * Limits: d a multiple of 8 up to 256, rot a multiple of 8, hq and hkv up to 4096.  No workspace.
  * Alignment: rows 16 bytes, strides multiples of 16 bytes, positions 4, inv_freq and n_rows 8.

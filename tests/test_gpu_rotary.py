@@ -1,5 +1,7 @@
 """kv_rotary on the GPU against its formula in 64 bits (angles in the host's long double), as a
 linear map with its gradient, and with the calls around it."""
+from fractions import Fraction
+
 import numpy as np
 import pytest
 import torch
@@ -217,3 +219,34 @@ def test_rows_past_32_bits():
     want, tol = expected(keep, p, freq.numpy(), d, "half", 1.0, False)
     assert (np.abs(x[-3:].cpu().double().numpy() - want) <= tol).all()
     assert bool((x[:-3] == 0).all())   # (of either sign)
+
+
+# 2 pi to 10^-59
+TWO_PI = Fraction(2 * 314159265358979323846264338327950288419716939937510582097494, 10 ** 59)
+
+
+@pytest.mark.parametrize("layout", ["half", "interleaved"])
+@pytest.mark.parametrize("back", [False, True])
+def test_any_frequency_below_the_limit(layout, back):
+    """Whole turns drop off whatever the frequency's size, at the farthest positions too: angles in
+    fractions of whole numbers, the sines in 64 bits, and the bound of expected()."""
+    freq = [1.5, 1000.5, 2.0 ** 20 + 0.5, 2.0 ** 33 + 1, 2.0 ** 45 + 0.125, 2.0 ** 52 - 1,
+            -7.25, -2.0 ** 40 - 3, 3.0e-5, 2.0 ** -70, 0.0, 977.0 / 1024] + [2.5] * 4
+    rot, d, pos = 2 * len(freq), 40, [0, 1, 131071, 2 ** 24 + 1, 2 ** 30 + 7, 2 ** 31 - 1]
+    x = torch.randn(len(pos), 3, d, generator=torch.Generator().manual_seed(3))
+    s = kv.KvRotaryShape.of(3, 0, d, rot, LAYOUT[layout], "f32")
+    out = torch.zeros_like(x, device="cuda")
+    kv.kv_rotary(s, x.cuda(), None, dev(pos, torch.int32), dev(freq, torch.float64), out, None,
+                 back=back)
+    t = np.array([[float(p * Fraction(f) % TWO_PI) for f in freq] for p in pos])[:, None]
+    c, n = np.cos(t), np.sin(t) * (-1 if back else 1)
+    y, half = x.double().numpy(), rot // 2
+    a, b = (y[..., :half], y[..., half:rot]) if layout == "half" else (y[..., 0:rot:2],
+                                                                       y[..., 1:rot:2])
+    got = out.cpu().double().numpy()
+    u, w = (got[..., :half], got[..., half:rot]) if layout == "half" else (got[..., 0:rot:2],
+                                                                           got[..., 1:rot:2])
+    # (the output's rounding, 2^-24 of it, beside the 2^-21 of the rest)
+    tol = (np.abs(a) + np.abs(b)) * (2.0 ** -21 + 2.0 ** -24)
+    assert (np.abs(u - (a * c - b * n)) <= tol).all()
+    assert (np.abs(w - (a * n + b * c)) <= tol).all()
