@@ -585,7 +585,9 @@ KV_API kv_status paged_decode_attn(const kv_paged_shape* shape, const void* q, c
  * in int8 each raise adds up to half of the new scale to what a value is off by).  The rows that a
  * call writes to a block are rounded once, at the scale that holds them all.  The rows held are those
  * below the first that the call writes, so a block that is filled anew from its first row on forgets
- * what it had.  A block that gets rows belongs to one table.
+ * what it had.  A block that gets rows belongs to one table.  Where its rows held have a scale that is
+ * no finite number (pages begun past a block's first row, scales never set), they are what that makes
+ * them, NaN and infinities, and follow the new rows' scale as such.
  *
  * Limits: those of the paged cache, and page >= 16, d a multiple of 16 (KV_ERR_UNSUPPORTED).
  * page_stride is a multiple of 16.  Workspaces: kv_paged_workspace_size with the ops of kv_quant_op;

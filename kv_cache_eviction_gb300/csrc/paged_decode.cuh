@@ -361,8 +361,8 @@ __device__ __forceinline__ float2 put_rows(unsigned char* stage, int above,
   for (int o = 1; o < 8; o <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
   top = __shfl_sync(0xffffffffu, top, lane & 16);
   const float old = r == 0 ? 0.f : v ? scale.y : scale.x;   // (a block that is begun anew has none)
-  const float now = fmaxf(quant::scale_for<F>(top), old), inv = 1.f / now;
-  if (now > old) {
+  const float now = quant::scale_after<F>(top, old), inv = 1.f / now;
+  if (now != old) {   // (raised, or in the place of a NaN or an infinity)
     for (int i = part; i < r * pieces; i += 16) {
       const int row = i / pieces;
       uint4* from = place(row, i - row * pieces);

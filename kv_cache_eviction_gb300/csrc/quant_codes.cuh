@@ -106,6 +106,16 @@ __device__ __forceinline__ float scale_for(uint32_t top) {
   return __uint_as_float((uint32_t)(t + 127) << 23);
 }
 
+// The scale of a block after it got rows of that maximum: `old`, that of the rows held (0 where there
+// are none), or what the new rows need where that is more.  An old one that is no finite number does not
+// count, as the values it stands for do not; times old / the new one they are then coded as what they
+// are, NaN and infinities.
+template <typename F>
+__device__ __forceinline__ float scale_after(uint32_t top, float old) {
+  const float need = scale_for<F>(top);
+  return need < old && old < INFINITY ? old : need;
+}
+
 // 16 codes of a piece at another scale: rounded times `by`.
 template <typename F>
 __device__ __forceinline__ uint4 again(uint4 c, float by) {

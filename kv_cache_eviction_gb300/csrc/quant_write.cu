@@ -107,8 +107,8 @@ quant_write_kernel(const __grid_constant__ QWriteArgs a) {
         for (int j = 0; j < KP; ++j) top = x[j].finite_top(top);
         top = __reduce_max_sync(0xffffffffu, top);
       }
-      const float now = fmaxf(quant::scale_for<F>(top), old), inv = 1.f / now;
-      if (now > old) {
+      const float now = quant::scale_after<F>(top, old), inv = 1.f / now;
+      if (now != old) {   // (raised, or in the place of a NaN or an infinity)
         // (the run's rows are contiguous in the pool, and so are those before it)
         for (int p = lane; p < first * (a.d / 16); p += 32) {
           uint4* at = reinterpret_cast<uint4*>(dst - first * a.d) + p;

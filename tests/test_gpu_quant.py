@@ -424,3 +424,40 @@ def test_binding_refuses_wrong_tensors(monkeypatch):
                     call(args[0], 7, *args[2:])
             assert kv.kv_kernel_launches() == before
     torch.cuda.synchronize()
+
+
+@pytest.mark.parametrize("fmt", ["e4m3", "int8"])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), -float("inf")])
+def test_rows_added_to_a_scale_that_is_no_number(fmt, dtype, bad):
+    """Rows written behind rows of a block whose scale was never set: they are stored with a scale of
+    their own, and read back as any others; the rows held stay NaN and infinities as far as the
+    format has those (int8: zeros and the largest codes)."""
+    heads, d, page = 2, 48, 32
+    pool = Pool(3, heads, page, d, fmt, 7, scales=bad)
+    s = shape_of(pool, dtype)
+    runs_of = ((0, 5, 4), (1, 16 + 15, 1), (2, 1, 15), (2, 16 + 8, 8))   # page, first row, rows
+    slots = np.concatenate([p * page + r + np.arange(n) for p, r, n in runs_of])
+    x = rows_of(11, len(slots), heads, d, dtype)
+    ws = write(pool, s, x[0].cuda(), x[1].cuda(), slots)
+    for name, rows in (("k", x[0].double().numpy()), ("v", x[1].double().numpy())):
+        at = 0
+        for p, r, n in runs_of:
+            b, new = r // BLOCK, rows[at:at + n]
+            at += n
+            for h in range(heads):
+                now = scale_for(new[:, h], fmt)
+                held = pool.num[name][p, h, b * BLOCK:r]
+                with np.errstate(invalid="ignore"):
+                    pool.num[name][p, h, b * BLOCK:r] = nearest(held * bad, fmt)
+                pool.num[name][p, h, r:r + n] = nearest(new[:, h] / now, fmt)
+                pool.scale[name][p, h, b] = now
+    pool.check()
+    k, v = (torch.zeros(len(slots), heads, d, dtype=DT[dtype], device="cuda") for _ in range(2))
+    kv.kv_quant_read(s, FORMATS[fmt], *pool.args(), i64(slots), None, k, v, ws)
+    for name, got in (("k", k), ("v", v)):
+        with np.errstate(invalid="ignore"):     # (blocks that got no row)
+            values = pool.values(name)
+        want = np.stack([values[i // page, :, i % page] for i in slots])
+        assert np.isfinite(want).all() and np.array_equal(got.double().cpu().numpy(), want)
+    assert kv.kv_check_device_status(ws) == 0

@@ -635,3 +635,38 @@ def test_steps_back_to_back(fmt):
     for a, b in zip(*got):
         assert torch.equal(a, b)
     assert bool(torch.isfinite(got[0][0]).all())
+
+
+@pytest.mark.parametrize("fmt", ["e4m3", "int8"])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+def test_new_row_beside_a_scale_that_is_no_number(fmt, dtype, bad):
+    """A new row behind rows of a block whose scale was never set is stored with a scale of its own,
+    as kv_quant_write stores it; this step and the next attend over the same numbers."""
+    lens = [38, 17, 5, 64]
+    a, b = (QuantCache(4, 2, 2, 64, 1, 32, lens, dtype, fmt, 6) for _ in range(2))
+    for c in (a, b):
+        for name in ("k", "v"):                     # rows 32..36 of the first table
+            c.scale_dev[name][c.table_host[0, 1], :, 0] = bad
+    x, ws = a.run()
+    rows = lambda t: t.reshape(-1, 2, 64).contiguous().cuda()
+    kv.kv_quant_write(b.shape, FORMATS[fmt], rows(b.k_new), rows(b.v_new), b.slots, None, *b.args(),
+                      ws)
+    for name in ("k", "v"):
+        assert torch.equal(a.pool[name][0].view(torch.uint8), b.pool[name][0].view(torch.uint8))
+        assert torch.equal(a.scale_dev[name].view(torch.int32), b.scale_dev[name].view(torch.int32))
+        assert bool(torch.isfinite(a.scale_dev[name][a.table_host[0, 1], :, 0]).all())
+    again = a.run(with_new=False, ws=ws)[0]
+    assert torch.equal(torch.isnan(x), torch.isnan(again))
+    assert torch.equal(x.nan_to_num(nan=7.0), again.nan_to_num(nan=7.0))
+    assert bool(torch.isfinite(x[1:]).all())
+    # A number held is NaN now where the scale was one, or, that being infinite, where its code was
+    # zero (other codes are the largest then, a finite number); in int8 nowhere.  A NaN in K reaches
+    # every output of its head, one in V those of its column.
+    page = a.table_host[0, 1]
+    nan = {n: np.full((2, 5, 64), fmt == "e4m3") & (np.isnan(bad) | (b.num[n][page, :, :5] == 0))
+           for n in ("k", "v")}
+    want = nan["k"].any((1, 2))[:, None] | nan["v"].any(1)
+    assert np.array_equal(torch.isnan(x[0]).cpu().numpy().reshape(2, 2, 64),
+                          want[:, None].repeat(2, 1))
+    assert kv.kv_check_device_status(ws) == 0
