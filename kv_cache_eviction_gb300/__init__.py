@@ -342,20 +342,29 @@ _CODES = {}   # types that the codes of a format may come as
 
 
 # csrc/binding.cpp as a module, once torch is there: it checks a call's tensors and calls the C
-# function, or returns None for the code below to do it.  None: not built, calls go through ctypes.
+# function, or returns None for the code below to do it.  None: not built, or for another torch or
+# Python than these; calls go through ctypes.
 _quick = None
 _FAST_CALLS = ("kv_quant_write", "kv_quant_read", "quant_decode_attn", "kv_rotary")
 
 
 def _init_fast() -> None:
     global _quick
-    if not os.path.exists(os.path.join(_HERE, "_fast.so")):
+    from . import _build
+    if not os.path.exists(_build.FAST):
         return
-    try:
-        fast = importlib.import_module("._fast", __package__)
-    except ImportError as e:       # (built for another torch or Python)
+    why = ""
+    # (it may load with another torch and read tensors at the wrong places, so this comes first)
+    if _build.binding_built_for() != _build.binding_tag():
+        why = "is not built for this torch and Python"
+    else:
+        try:
+            fast = importlib.import_module("._fast", __package__)
+        except ImportError as e:
+            why = "does not load (%s)" % e
+    if why:
         import warnings
-        warnings.warn("kv_cache_eviction_gb300: _fast.so does not load (%s): build again" % e)
+        warnings.warn("kv_cache_eviction_gb300: _fast.so %s: build again" % why)
         return
     fast.bind(*(ctypes.cast(getattr(lib(), f), _vp).value for f in _FAST_CALLS))
     _quick = fast

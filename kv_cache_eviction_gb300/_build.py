@@ -14,7 +14,8 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libkvevict.so")
-FAST = os.path.join(PKG, "_fast.so")   # the Python binding's common case (csrc/binding.cpp)
+FAST = os.path.join(PKG, "_fast.so")   # the Python binding's common case (csrc/binding.cpp),
+STAMP = os.path.join(BUILD, "binding.txt")   # and the torch and Python that it was built for
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ARCH + ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC,-fvisibility=hidden",
@@ -40,19 +41,30 @@ def _stale(target: str, inputs) -> bool:
     return any(os.path.getmtime(p) > t for p in inputs)
 
 
+def binding_tag() -> str:
+    """The torch and the Python at hand: _fast.so reads tensors by their layout in one of each."""
+    import torch
+    return "%s %s %s" % (torch.__version__, sys.version, os.path.dirname(torch.__file__))
+
+
+def binding_built_for() -> str:
+    """The tag that _fast.so was built for, empty where that is not known."""
+    if not os.path.exists(STAMP):
+        return ""
+    with open(STAMP) as f:
+        return f.read()
+
+
 def _build_fast() -> None:
     """Compile csrc/binding.cpp against the torch at hand.  Without it (no Python or torch headers,
     no g++) calls go through ctypes, 6 us slower each: said, not raised."""
     src = os.path.join(CSRC, "binding.cpp")
-    # (built for one torch and one Python: those are part of the name that says what was built)
     try:
         import torch
-        tag = "%s %s %s" % (torch.__version__, sys.version, os.path.dirname(torch.__file__))
     except ImportError:
         return
-    stamp = os.path.join(BUILD, "binding.txt")
-    built = open(stamp).read() if os.path.exists(stamp) else None
-    if built == tag and not _stale(FAST, [src] + _deps()):
+    tag = binding_tag()
+    if binding_built_for() == tag and not _stale(FAST, [src] + _deps()):
         return
     root = os.path.dirname(torch.__file__)
     inc = [os.path.join(root, "include"),
@@ -75,8 +87,10 @@ def _build_fast() -> None:
         if os.path.exists(FAST):
             os.remove(FAST)
         return
+    if os.path.exists(STAMP):   # (never an old tag beside a new module, wherever this is cut short)
+        os.remove(STAMP)
     os.replace(tmp, FAST)
-    with open(stamp, "w") as f:
+    with open(STAMP, "w") as f:
         f.write(tag)
 
 

@@ -2,6 +2,9 @@
 is enqueued, the definition's own pieces, and the frequencies."""
 import ctypes
 import math
+import os
+import sys
+import warnings
 
 import numpy as np
 import pytest
@@ -268,3 +271,27 @@ def test_rotary_frequencies():
                 dict(slow=2.0, fast=2.0), dict(trained=0), dict(rot=2, scaling="base")):
         with pytest.raises(ValueError):
             kv.kv_rotary_inv_freq(**{"rot": 64, **bad})
+
+
+@pytest.mark.parametrize("what", ["torch", "python", "no stamp"])
+def test_fast_module_for_another_torch_is_not_loaded(L, monkeypatch, tmp_path, what):
+    """_fast.so reads tensors by their layout: with another torch or Python than it was built for,
+    or where that is not known, calls go through ctypes, with a warning."""
+    if not os.path.exists(_build.FAST):
+        pytest.skip("no _fast.so")
+    with monkeypatch.context() as m:
+        m.setattr(kv, "_quick", None)
+        if what == "torch":
+            m.setattr(torch, "__version__", "1.0.0")
+        elif what == "python":
+            m.setattr(sys, "version", "3.99")
+        else:
+            m.setattr(_build, "STAMP", str(tmp_path / "none.txt"), raising=False)
+        with pytest.warns(UserWarning, match="_fast.so"):
+            kv._init_fast()
+        assert kv._quick is None
+    with monkeypatch.context() as m, warnings.catch_warnings():
+        warnings.simplefilter("error")
+        m.setattr(kv, "_quick", None)
+        kv._init_fast()
+        assert kv._quick is not None
