@@ -55,6 +55,13 @@ def binding_built_for() -> str:
         return f.read()
 
 
+def _no_fast(why: str) -> None:
+    print("kv_cache_eviction_gb300: no _fast.so (calls go through ctypes): %s" % why,
+          file=sys.stderr)
+    if os.path.exists(FAST):
+        os.remove(FAST)
+
+
 def _build_fast() -> None:
     """Compile csrc/binding.cpp against the torch at hand.  Without it (no Python or torch headers,
     no g++) calls go through ctypes, 6 us slower each: said, not raised."""
@@ -62,6 +69,9 @@ def _build_fast() -> None:
     try:
         import torch
     except ImportError:
+        return
+    except Exception as e:   # (a torch whose libraries do not load: OSError, RuntimeError)
+        _no_fast("torch does not load: %s" % e)
         return
     tag = binding_tag()
     if binding_built_for() == tag and not _stale(FAST, [src] + _deps()):
@@ -82,10 +92,7 @@ def _build_fast() -> None:
     except OSError as e:
         why = str(e)
     if why:
-        print("kv_cache_eviction_gb300: no _fast.so (calls go through ctypes): %s" % why,
-              file=sys.stderr)
-        if os.path.exists(FAST):
-            os.remove(FAST)
+        _no_fast(why)
         return
     if os.path.exists(STAMP):   # (never an old tag beside a new module, wherever this is cut short)
         os.remove(STAMP)

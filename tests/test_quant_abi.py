@@ -1,5 +1,6 @@
 """The cache in 8 bits and the rotary positions without a GPU: refusals on the host before anything
 is enqueued, the definition's own pieces, and the frequencies."""
+import builtins
 import ctypes
 import math
 import os
@@ -295,3 +296,21 @@ def test_fast_module_for_another_torch_is_not_loaded(L, monkeypatch, tmp_path, w
         m.setattr(kv, "_quick", None)
         kv._init_fast()
         assert kv._quick is not None
+
+
+@pytest.mark.parametrize("error", [ImportError, OSError, RuntimeError])
+def test_build_with_a_torch_that_does_not_load(monkeypatch, tmp_path, capsys, error):
+    """The library is built without torch; one that fails to load is said, not raised."""
+    real = builtins.__import__
+
+    def fails(name, *args, **kw):
+        if name == "torch":
+            raise error("libtorch_cpu.so: cannot open")
+        return real(name, *args, **kw)
+
+    monkeypatch.setattr(_build, "FAST", str(tmp_path / "_fast.so"))
+    monkeypatch.setattr(builtins, "__import__", fails)
+    _build._build_fast()
+    monkeypatch.undo()
+    said = "cannot open" in capsys.readouterr().err
+    assert said == (error is not ImportError)
