@@ -20,7 +20,8 @@ def kv_rotary_inv_freq(rot: int, base: float = 10000.0, scaling: str = "none",
       length: f_i / factor up to ``slow`` of them, f_i from ``fast`` on, and between the mix
       with the weight (n_i - slow) / (fast - slow) on f_i;
     * ``"yarn"``: the same two ends, mixed by a ramp over the pairs' numbers, from the pair of
-      ``fast`` turns (rounded down) to that of ``slow`` turns (rounded up); the magnitude is
+      ``fast`` turns (rounded down, pair 0 at least) to that of ``slow`` turns (rounded up), which
+      lies behind the last pair where all of them make more turns; the magnitude is
       0.1 ln(factor) + 1.
     """
     import torch
@@ -45,7 +46,7 @@ def kv_rotary_inv_freq(rot: int, base: float = 10000.0, scaling: str = "none",
         def pair(turns):
             return rot * math.log(trained / (turns * 2 * math.pi)) / (2 * math.log(base))
         lo = max(math.floor(pair(fast)), 0)
-        hi = min(math.ceil(pair(slow)), rot // 2 - 1)
+        hi = math.ceil(pair(slow))
         ramp = ((i - lo) / max(hi - lo, 1e-3)).clamp(0.0, 1.0)
         return f / factor * ramp + f * (1 - ramp), 0.1 * math.log(factor) + 1.0
     raise ValueError("scaling must be none, linear, base, bands or yarn")

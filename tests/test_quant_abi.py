@@ -314,3 +314,19 @@ def test_build_with_a_torch_that_does_not_load(monkeypatch, tmp_path, capsys, er
     monkeypatch.undo()
     said = "cannot open" in capsys.readouterr().err
     assert said == (error is not ImportError)
+
+
+def test_yarn_where_every_pair_makes_a_turn():
+    """The ramp ends at the pair of `slow` turns also where that lies behind the last one, as for long
+    trained lengths on a small base: here pair(turns) = 64 ln(131072 / (2 pi turns)) / ln(10000) is 69.1
+    for one turn and 45.03 for 32, so the ramp is from 45 to 70 and pair i is (i - 45) / 25 of the way."""
+    f = kv.kv_rotary_inv_freq(128, 10000.0)[0]
+    y = kv.kv_rotary_inv_freq(128, 10000.0, "yarn", 4.0, trained=131072)[0]
+    i = torch.arange(64, dtype=torch.float64)
+    w = ((i - 45) / 25).clamp(0, 1)
+    assert torch.allclose(y, f * (1 - w) + f / 4 * w, rtol=1e-14)
+    # before the first pair it does not begin: no pair of 200 positions makes 32 turns but the first
+    y = kv.kv_rotary_inv_freq(8, 10000.0, "yarn", 4.0, trained=128, slow=1.0, fast=32.0)[0]
+    f = kv.kv_rotary_inv_freq(8, 10000.0)[0]
+    w = (torch.arange(4, dtype=torch.float64) / 2).clamp(0, 1)   # pair(32) = -0.2, pair(1) = 1.3
+    assert torch.allclose(y, f * (1 - w) + f / 4 * w, rtol=1e-14)
