@@ -637,10 +637,14 @@ KV_API kv_status kv_quant_read(const kv_paged_shape* shape, int format, const vo
  * above.  A table's slot has to be the place that its block table gives row lens - 1 (kv_page_map's
  * is): at any other one in the pool the row is not stored, and the error word is set (10).
  * Sums, the softmax and out before its rounding are float32 (fp32 q is held to 22 bits, the softmax
- * numerators to 22 bits or 2^-39 of the largest; bf16 q and the values are exact).  q, the values
- * attended to and their scores have to be finite (a NaN among them makes the outputs it reaches NaN,
- * an infinity may); anything may stand behind a table's last row, in pages of no table and in the
- * scales of blocks that hold no row.  Every result is the same in every run.
+ * numerators to 22 bits or 2^-39 of the largest; the values are exact, and so are elements of bf16 q from
+ * 2^-30 of their head's largest on; of either type, what is smaller is off by at most 2^-38 of that, or
+ * 2^-145).
+ * q, the values attended to and their scores have to be finite (a NaN among them makes the outputs it
+ * reaches NaN, an infinity may), and the largest element of a head of q times the largest of a block of
+ * K below 2^127; scores below 2^-118, before softmax_scale, may count as 0.  Anything may stand
+ * behind a table's last row, in pages of no table and in the scales of blocks that hold no row.  Every
+ * result is the same in every run.
  */
 KV_API kv_status quant_decode_attn(const kv_paged_shape* shape, int format, const void* q,
                                    const void* k_new, const void* v_new, const int64_t* cu_add,
