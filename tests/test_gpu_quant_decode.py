@@ -670,3 +670,22 @@ def test_new_row_beside_a_scale_that_is_no_number(fmt, dtype, bad):
     assert np.array_equal(torch.isnan(x[0]).cpu().numpy().reshape(2, 2, 64),
                           want[:, None].repeat(2, 1))
     assert kv.kv_check_device_status(ws) == 0
+
+
+@pytest.mark.parametrize("where", ["k", "v"])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_nan_in_the_only_row_held(where, dtype):
+    """A table of one row that is no new one, with a NaN in it: the outputs that it reaches, and nowhere
+    else."""
+    c = QuantCache(3, 2, 2, 64, 1, 16, [33, 1, 70], dtype, "e4m3", 11, new=[1, 0, 1])
+    c.pool[where][1].view(torch.uint8)[c.table_host[1, 0], 0, 0, 7] = 127
+    out, ws = c.run()
+    torch.cuda.synchronize()
+    assert kv.kv_check_device_status(ws) == 0
+    nan = torch.isnan(out.cpu().float())
+    want = torch.zeros_like(nan)
+    if where == "v":
+        want[1, :2, 7] = True
+    else:
+        want[1, :2] = True
+    assert torch.equal(nan, want)
