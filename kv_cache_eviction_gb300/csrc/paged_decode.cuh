@@ -614,8 +614,9 @@ paged_decode_kernel(const __grid_constant__ PagedArgs a) {
       const int64_t blocks = (int64_t)a.Hp << (a.shift - 4);   // of a page
       nxt.scale = (bad ? 0 : p_page * blocks) + (p_row >> 4);
       nxt.scale2 = page < RT ? (bad2 ? 0 : p_page2 * blocks) + (p_row >> 4) : nxt.scale + 1;
-      if (bad) nxt.at = -1;   // no row's place
-      if (bad2) nxt.at2 = -1;
+      // (no row's place; a second page's at2 is one of page 0's.  What keeps a new row out of a page
+      // outside the pool is its row in the mask, which does not count.)
+      if (bad) nxt.at = -1;
     }
     nxt.at2 = (bad2 ? 0 : p_page2) * a.page_stride + p_row * (int64_t)d;
     if (bad || bad2) nxt.word = W::without(nxt.word, bad, page < RT ? bad2 : bad);
