@@ -34,8 +34,8 @@
 // same GB300 and heads (e4m3, bf16 q unless stated): 128 ragged sequences of 8000 rows, 2.1 GB, 317 us
 // (6.6 TB/s, 0.97 of the copy rate; int8 333 us, fp32 q 324 us); 64 of 2000 rows 55 us (4.7 TB/s);
 // one of 131000 rows 49 us (5.4 TB/s; int8, fp32 q 56 us); 256 heads of 128 rows 9.3 us; one
-// sequence of 500 rows 8.3 us.  Tiles of one block took 434 us on the 2.1 GB: 770 instructions for
-// 16 rows, and two warps a scheduler hide little of them.
+// sequence of 500 rows 8.3 us.  Tiles of one block took 434 us on the 2.1 GB: what a tile costs
+// beside its products is then spent every 16 rows, and two warps a scheduler hide little of it.
 #pragma once
 
 #include <cfloat>
@@ -84,7 +84,9 @@ constexpr int kMinTiles = 4;
 // units of 2000 rows level.  Those are tiles of 16 rows.  Of 32, 8 / 12 / 15 / 20 tiles: units of 500 rows
 // (16 tiles), 8 of them 8.3 / 8.3 / 8.3 / 10.2 us; 64 ragged ones 10.5 / 10.5 / 10.5 / 10.7; 256 heads of
 // 128 rows, all of at most 10 tiles, 11.8 / 9.4 / 9.4 / 9.4, two of them of 13 and 14 11.7 with 12, 11.0
-// with 15 and 20.
+// with 15 and 20.  Few units of 13 to 15 tiles pay for that: 8 of 384 / 416 / 448 / 480 / 500 rows 8.9 /
+// 9.3 / 9.3 / 9.3 / 8.5 us with 15, 8.9 / 8.8 / 8.9 / 9.0 / 8.5 with 12; 32 of them 9.2 / 9.9 / 10.1 /
+// 10.2 / 9.1 and 9.2 / 9.7 / 9.7 / 10.1 / 9.0.  (The rule knows a unit's length, not how many there are.)
 template <int RT>
 constexpr int kSnapTiles = RT == 32 ? 15 : 24;
 // Part of a unit in the workspace: max[8], sum[8], then o[G][D].
@@ -480,7 +482,10 @@ paged_decode_kernel(const __grid_constant__ PagedArgs a) {
   const uint32_t want = (total + kMinTiles - 1) / kMinTiles;
   uint32_t Ne = want > (uint32_t)N ? N : want;   // CTAs that take tiles
   // One sequence: as many to each head, so that no CTA has parts of two (of 2000 rows 11.7 us with 126
-  // CTAs for 8 heads).
+  // CTAs for 8 heads).  Good for short ones, and for long ones as long as what it takes off is little.
+  // With / without, us, one query a head: 2000 rows of 8 / 40 / 64 / 96 / 112 heads 9.7 / 11.3 / 13.7 /
+  // 15.3 / 19.1 and 10.7 / 12.5 / 14.4 / 16.3 / 17.6; 32000 rows 18.1 / 59.0 / 94.9 / 124.6 / 180.5 and
+  // 17.9 / 59.5 / 84.0 / 124.6 / 143.6 (64 heads leave 256 of 304 CTAs, 112 leave 224).
   if (P::kCodes && a.U == 1 && Ne > (uint32_t)a.Hp) Ne -= Ne % a.Hp;
   if (c >= (int)Ne) return;
 

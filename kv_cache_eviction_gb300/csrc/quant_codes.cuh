@@ -76,7 +76,8 @@ struct Int8 {
     const uint32_t c = __float_as_uint(fmaf(z, by, kBase)), d = __float_as_uint(fmaf(w, by, kBase));
     return __byte_perm(__byte_perm(a, b, 0x0040), __byte_perm(c, d, 0x0040), 0x5410);
   }
-  // code + 128 in the last places of 1024: less 1152 it is the code, exactly
+  // code + 128 in the last places of 1024 (fp16 has ten of them, so 1024 + n is 0x6400 + n for n below
+  // 1024): less 1152 it is the code, exactly
   static __device__ __forceinline__ uint32_t less(uint32_t x) {
     uint32_t r;
     asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(x), "r"(0x64806480u));

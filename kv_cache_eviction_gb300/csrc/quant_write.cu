@@ -17,9 +17,10 @@ namespace {
 
 using quant::Piece;
 constexpr int kThreads = 128;
-// CTAs of an SM by a lane's pieces.  131072 bf16 rows of 128 (8 pieces), us: 4 CTAs 133, 5 124, 6
-// 120, 7 134, 8 (the registers then spill) 140; 100003 fp32 rows of 64 (8 pieces): 16.9, 15.1,
-// 15.8, 15.6, 15.5.
+// CTAs of an SM by a lane's pieces, for both types.  131072 bf16 rows of 128 (8 pieces), us: 4 CTAs
+// 133, 5 124, 6 120, 7 134, 8 (the registers then spill) 140; 100003 fp32 rows of 64 (8 pieces): 16.9,
+// 15.1, 15.8, 15.6, 15.5.  So fp32 would be 4 % better off with 5: its kernel spills 60 bytes with 6.
+// fp32 rows of 128 (16 pieces, 159 registers, 3 CTAs): 131072 of 8 heads 209 us, 6.4 TB/s.
 constexpr int resident(int pieces) { return pieces <= 4 ? 8 : pieces <= 8 ? 6 : 3; }
 
 struct QWriteArgs {

@@ -15,7 +15,10 @@
 // small calls are split by heads.  On GB300: 131072 rows of 32 + 8 heads of 128 bf16 (2.7 GB read
 // and written) 412 us, 6.5 TB/s or 0.96 of the measured copy rate; 20011 fp32 rows of 8 heads of
 // 80, 24 columns of them turned, 21.5 us (24.4 with the other columns copied one after the other);
-// 64 rows 2.6 us (3.7 with every lane working out all of its pairs' sines).
+// 64 rows 2.6 us (3.7 with every lane working out all of its pairs' sines); 65536 fp32 rows of 32 + 8
+// heads of 128 397 us, 6.8 TB/s.  What the small and the fp32 calls gained by the shared sines and the
+// pieces copied four at a time cost the 131072 rows 1 % (408 us before).  bf16's `half` kernel of 8 pairs
+// a lane spills one register at its 72.
 #include "kv_internal.cuh"
 #include "tc_ptx.cuh"
 
